@@ -39,8 +39,9 @@
  *     takes `ws` clears that word (and the fault-site word after it) on
  *     `stream` before any of its kernels can latch a fault: quoka_select,
  *     quoka_select_ex and quoka_prefill_chunk in their first kernel,
- *     quoka_gather_kv and quoka_decode_attn in a one-thread kernel of their
- *     own, the other calls with an 8-byte memset; a kernel latches only
+ *     quoka_cache_select in the kernel that makes its group means,
+ *     quoka_gather_kv, quoka_decode_attn and the other cache calls in a
+ *     one-thread kernel of their own, the other calls with an 8-byte memset; a kernel latches only
  *     after the kernel before it in the call has completed. The word
  *     reports the faults of the latest call.
  *   - Calls on different streams with different workspaces may run
@@ -361,6 +362,125 @@ quoka_status quoka_combine_partials(const void* O_parts, const float* lse_parts,
                                     int N, int b, int nq, int BCP, int d,
                                     quoka_dtype dtype, void* O, float* lse,
                                     void* stream);
+
+/* ---- A paged cache held in 8 bits ---------------------------------------
+ * For serving with long caches: [QUOKA §4.2 problem 3] takes the KV cache as
+ * given; these calls write, select from, read and attend over one that is
+ * kept in pages of e4m3 codes.
+ *   k, v       (npages, nkv, page, d) codes (1 byte each; sign, 4 bits of
+ *              exponent with bias 7, 3 of fraction). page 16, 32, 64 or 128
+ *              tokens; d 64 or 128. Strides in bytes, shared by k and v,
+ *              multiples of 16; a row's d codes are contiguous; rows must
+ *              not overlap. k and v 16-byte aligned.
+ *   k_scale, v_scale  (npages, nkv) float, contiguous: powers of two 2^e,
+ *              -50 <= e <= 50. A row's value is code * scale. Anything else
+ *              in the scale of a page that holds tokens latches
+ *              QUOKA_ERR_BOUNDS (its exponent field, kept to the range, is
+ *              used).
+ *   page_table (b, max_pages) int32, rows table_stride entries apart: column
+ *              c names the page of tokens [c * page, (c + 1) * page). Entries
+ *              that no token needs are not read and may hold anything;
+ *              sequences may share pages that are only read.
+ *   seq_len    (b) int32: tokens held.
+ * All of it is device memory of the caller, which also hands out pages and
+ * advances seq_len. `max_len` of the calls below is a host-side bound of
+ * seq_len (at most max_pages * page; it fixes output shapes and grids).
+ * Faults that only the device can see latch QUOKA_ERR_BOUNDS in ws and read
+ * no memory: a table entry outside [0, npages) (the rows of that page count
+ * as zeros), a seq_len outside [0, max_len] (taken as the nearer bound), a
+ * key index outside [0, seq_len) (a row of zeros). */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t npages;
+  int32_t nkv, page, d;
+  int64_t page_stride, head_stride, row_stride; /* bytes */
+  const int32_t* page_table;
+  int64_t table_stride; /* elements */
+  int32_t b, max_pages;
+  const int32_t* seq_len;
+} quoka_cache;
+
+/* Option of quoka_cache_append: pairs are neighbouring columns. */
+#define QUOKA_ROTATE_NEIGHBOURS 1u
+
+/* Writes a chunk's keys and values behind the tokens each sequence holds,
+ * rotating the keys (and the chunk's queries) by their positions.
+ *   K, V (b, nkv, BCP, d), Q (b, nq, BCP, d) or NULL, of one dtype. Token t
+ *   of sequence s takes position p = seq_len[s] + t.
+ *   Rotation of the first `rot` columns (a multiple of 16, at most d; 0: none)
+ *   by cos, sin (npos, rot / 2) float, contiguous, 16-byte aligned, row p:
+ *     x1' = x1 cos - x2 sin,  x2' = x2 cos + x1 sin   (fp32, each operation
+ *   rounded by itself), pairs (x1, x2) being columns (i, i + rot / 2), or
+ *   (2i, 2i + 1) with QUOKA_ROTATE_NEIGHBOURS.
+ *   Quantisation, per touched page and head: a = the largest finite magnitude
+ *   of the page's new rows (fp32, before any rounding); the scale becomes the
+ *   smallest 2^e, -50 <= e <= 50, with a <= 448 * 2^e, but not below the
+ *   scale of a page that already holds earlier tokens; if that scale grows,
+ *   the codes the page holds are brought to it. Codes are rounded to nearest
+ *   even and saturate at 448 (infinities too); NaN stays NaN.
+ *   new_len (b) int32 or NULL: new tokens of each sequence, in [0, BCP] (NULL:
+ *   BCP each). Tokens past it are neither read nor written, in any output.
+ *   Kr (b, nkv, BCP, d) or NULL, Qr (b, nq, BCP, d, with Q): out, contiguous,
+ *   the rotated keys and queries rounded to their dtype. They must not
+ *   overlap K, V or Q (QUOKA_ERR_INVALID_ARG).
+ * seq_len is not changed: the caller advances it once the chunk's attention
+ * is done. A page that is written belongs to one sequence and one column.
+ * Tokens whose position lies past the page table or the angles, a new_len
+ * outside [0, BCP] and pages outside the cache latch QUOKA_ERR_BOUNDS in `ws`
+ * (which may be NULL) and are left out. */
+quoka_status quoka_cache_append(const quoka_cache* cache, const quoka_tensor* K,
+                                const quoka_tensor* V, const quoka_tensor* Q,
+                                const float* cos, const float* sin,
+                                int64_t npos, int rot, uint32_t flags,
+                                const int32_t* new_len, void* Kr, void* Qr,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* Steps (a)-(e) of quoka_select over the cached keys, [QUOKA §2.1 Algorithm 1,
+ * §2.2, §2.3]: per sequence and KV head the min(BSA, seq_len) keys with the
+ * largest S_agg (a key's scale cancels in its cosine), ties to the lower
+ * index, ascending.
+ *   Q (b, nq, BCP, d). kv_idx (b, nkv, min(BSA, max_len)), kv_count (b, nkv),
+ *   q_idx (b, nq, NQ) or NULL and s_agg (b, nkv, max_len) or NULL as in
+ *   quoka_select; entries of kv_idx past the count and of s_agg past seq_len
+ *   are left as they were. After a device fault kv_count is 0. A key whose
+ *   codes are all zero scores 0.
+ *   ws at least quoka_select_workspace_size(b, nq, nkv, d, max_len, BCP, NQ,
+ *   BSA, dtype of Q) bytes. */
+quoka_status quoka_cache_select(const quoka_tensor* Q, const quoka_cache* cache,
+                                int max_len, int NQ, int BSA, int32_t* kv_idx,
+                                int32_t* kv_count, int32_t* q_idx, float* s_agg,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* Step (f) over the cache: Ksel[b, j, n] = the value of key kv_idx[b, j, n]
+ * for n < kv_count[b, j], and the same for V; with kv_idx and kv_count NULL,
+ * N = max_len and row n is key n, n < seq_len[b]. Rows past the count are
+ * zeros. Ksel, Vsel out (b, nkv, N, d), contiguous, of `dtype`, which holds
+ * every cached value exactly. ws may be NULL. */
+quoka_status quoka_cache_gather(const quoka_cache* cache, int max_len,
+                                const int32_t* kv_idx, const int32_t* kv_count,
+                                int N, quoka_dtype dtype, void* Ksel, void* Vsel,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* Steps (f)+(g) over the cache: the attention of quoka_sparse_gqa_attn over
+ * the cached keys of an index list (as in quoka_cache_gather, N entries a
+ * row), or over all keys below seq_len (kv_idx and kv_count NULL, N =
+ * max_len), and over the chunk's own keys Kc[b, j, s], s <= t (Kc and Vc both
+ * NULL: without them).
+ *   Q (b, nq, BCP, d); Kc, Vc (b, nkv, BCP, d), dtype of Q; O out
+ *   (b, nq, BCP, d), contiguous; lse out (b, nq, BCP) float or NULL. A row
+ *   that sees no key gives O = 0, lse = -inf.
+ *   ws at least quoka_cache_attn_workspace_size() bytes, 256-byte aligned. */
+size_t quoka_cache_attn_workspace_size(int b, int nq, int nkv, int d, int BCP,
+                                       int N, quoka_dtype dtype);
+quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache,
+                              int max_len, const int32_t* kv_idx,
+                              const int32_t* kv_count, int N,
+                              const quoka_tensor* Kc, const quoka_tensor* Vc,
+                              float scale, void* O, float* lse, void* ws,
+                              size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, then reads the device status word of `ws` into
  * *device_status (a quoka_status value; QUOKA_OK if the latest call that

@@ -31,6 +31,12 @@ __all__ = [
     "quoka_topk",
     "quoka_shard_take",
     "quoka_combine_partials",
+    "QuokaCache",
+    "quoka_cache_append",
+    "quoka_cache_select",
+    "quoka_cache_gather",
+    "quoka_cache_attn_workspace_size",
+    "quoka_cache_attn",
 ]
 
 

@@ -58,6 +58,11 @@ EXPORTS = (
     "quoka_decode_attn",
     "quoka_get_device_fault_site",
     "quoka_debug_set_wait_hooks",
+    "quoka_cache_append",
+    "quoka_cache_select",
+    "quoka_cache_gather",
+    "quoka_cache_attn_workspace_size",
+    "quoka_cache_attn",
 )
 
 
@@ -76,11 +81,33 @@ class quoka_tensor(ctypes.Structure):
     ]
 
 
+class quoka_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("npages", ctypes.c_int64),
+        ("nkv", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("b", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("seq_len", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
 _P = ctypes.c_void_p
 _T = ctypes.POINTER(quoka_tensor)
+_C = ctypes.POINTER(quoka_cache)
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
@@ -141,6 +168,16 @@ def load() -> ctypes.CDLL:
         lib.quoka_get_device_fault_site.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_int32)]
         lib.quoka_debug_set_wait_hooks.restype = _I
         lib.quoka_debug_set_wait_hooks.argtypes = [ctypes.c_uint64, ctypes.c_uint32]
+        lib.quoka_cache_append.restype = _I
+        lib.quoka_cache_append.argtypes = [_C, _T, _T, _T, _P, _P, _I64, _I, ctypes.c_uint32, _P, _P, _P, _P, _SZ, _P]
+        lib.quoka_cache_select.restype = _I
+        lib.quoka_cache_select.argtypes = [_T, _C, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]
+        lib.quoka_cache_gather.restype = _I
+        lib.quoka_cache_gather.argtypes = [_C, _I, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]
+        lib.quoka_cache_attn_workspace_size.restype = _SZ
+        lib.quoka_cache_attn_workspace_size.argtypes = [_I, _I, _I, _I, _I, _I, _I]
+        lib.quoka_cache_attn.restype = _I
+        lib.quoka_cache_attn.argtypes = [_T, _C, _I, _P, _P, _I, _T, _T, _F, _P, _P, _P, _SZ, _P]
         lib.quoka_combine_partials.restype = _I
         lib.quoka_combine_partials.argtypes = [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]
         _lib = lib
@@ -521,4 +558,260 @@ def quoka_combine_partials(O_parts, lse_parts, *, O=None, lse=None, stream=None)
     st = lib.quoka_combine_partials(_ptr(O_parts), _ptr(lse_parts), N, b, nq, BCP, d, _dtype_code(O_parts),
                                     _ptr(O), _ptr(lse), _stream(stream))
     _check(st, "quoka_combine_partials")
+    return O, lse
+
+
+# ---------------------------------------------------------------- the paged 8-bit cache
+
+class QuokaCache:
+    """A paged key/value cache held in 8 bits, for the quoka_cache_* calls:
+    a description of the caller's tensors, which it keeps alive.
+
+    k, v (npages, nkv, page, d) e4m3 codes (torch.float8_e4m3fn or uint8) of
+    the same strides; k_scale, v_scale (npages, nkv) float32, powers of two
+    from 2^-50 to 2^50; page_table (b, max_pages) int32; seq_len (b) int32,
+    tokens held. page is 16, 32, 64 or 128, d 64 or 128. The tensors are
+    updated in place (quoka_cache_append writes codes and scales; pages are
+    handed out and seq_len advanced by the caller); to use others, make
+    another QuokaCache."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table, seq_len):
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError("k and v must be (npages, nkv, page, d) with the same strides")
+        npages, nkv, page, d = k.shape
+        if page not in (16, 32, 64, 128) or d not in (64, 128):
+            raise ValueError("page must be 16, 32, 64 or 128 and d 64 or 128")
+        if npages < 1 or nkv < 1 or k.stride(3) != 1:
+            raise ValueError("k and v must hold a page and contiguous rows")
+        for x in (k, v):
+            if x.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise TypeError(f"codes must be float8_e4m3fn or uint8, not {x.dtype}")
+        for x in (k_scale, v_scale):
+            _expect(x, "scales", torch.float32, (npages, nkv), k.device)
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1 or \
+                page_table.shape[0] < 1 or page_table.shape[1] < 1:
+            raise ValueError("page_table must be (b, max_pages) int32 with contiguous rows")
+        b, max_pages = page_table.shape
+        _expect(seq_len, "seq_len", torch.int32, (b,), k.device)
+        if v.device != k.device or page_table.device != k.device:
+            raise ValueError("the cache's tensors must be on one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table, self.seq_len = page_table, seq_len
+        self.device = k.device
+        self.b, self.nkv, self.page, self.d, self.max_pages = b, nkv, page, d, max_pages
+        self._view = quoka_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), npages, nkv, page,
+                                 d, k.stride(0), k.stride(1), k.stride(2), page_table.data_ptr(),
+                                 max(page_table.stride(0), max_pages), b, max_pages, seq_len.data_ptr())
+        self._ref = ctypes.byref(self._view)
+
+
+def _expect(t, name, dtype, shape, device) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+
+
+class _on:
+    """The cache's device and `stream` (its current one by default) for the
+    duration of a call, so that what the call allocates belongs to them."""
+
+    def __init__(self, cache, stream, *tensors):
+        dev = cache.device
+        if dev.type != "cuda":
+            raise ValueError("the cache must be on a CUDA device")
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise ValueError(f"every tensor must be on the cache's device {dev}, not {t.device}")
+        if stream is None:
+            self.ctx = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        else:
+            if stream.device != dev:
+                raise ValueError(f"the stream must be on the cache's device {dev}")
+            self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _heads(x, name, b, heads, rows, d):
+    if x.dim() != 4 or x.shape[0] != b or x.shape[3] != d or (heads and x.shape[1] != heads) or \
+            (rows and x.shape[2] != rows):
+        raise ValueError(f"{name} must be ({b}, {heads or 'nq'}, {rows or 'BCP'}, {d}), not {tuple(x.shape)}")
+    return ctypes.byref(tensor_view(x))
+
+
+def _ws_args(ws):
+    return _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def quoka_cache_append(cache, K, V, Q=None, cos=None, sin=None, *, interleaved=False, new_len=None, Kr=None, Qr=None,
+                       want_Kr=False, ws=None, stream=None):
+    """Writes a chunk's keys and values (b, nkv, BCP, d) behind the tokens
+    each sequence holds, the keys rotated by their positions with cos, sin
+    (npos, rot / 2) float32 (None: no rotation; interleaved: the pairs are
+    neighbouring columns). Returns (Kr, Qr): the rotated keys (None unless
+    given or wanted) and the rotated Q (b, nq, BCP, d) (None without Q), in
+    their dtype. Tokens from new_len (b) int32 on (None: BCP) are left out;
+    their rows of Kr and Qr stay as they were (zeros when made here).
+    cache.seq_len stays: advance it when the chunk is done."""
+    lib = load()
+    b, nkv, d = cache.b, cache.nkv, cache.d
+    kv = _heads(K, "K", b, nkv, None, d)
+    BCP = K.shape[2]
+    vv = _heads(V, "V", b, nkv, BCP, d)
+    qv = None if Q is None else _heads(Q, "Q", b, None, BCP, d)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    rot = npos = 0
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError("cos and sin must be (npos, rot / 2)")
+        npos, rot = cos.shape[0], 2 * cos.shape[1]
+        _expect(cos, "cos", torch.float32, (npos, rot // 2), cache.device)
+        _expect(sin, "sin", torch.float32, (npos, rot // 2), cache.device)
+    if new_len is not None:
+        _expect(new_len, "new_len", torch.int32, (b,), cache.device)
+    if Qr is not None and Q is None:
+        raise ValueError("Qr without Q")
+    for t, x, name in ((Kr, K, "Kr"), (Qr, Q, "Qr")):
+        if t is not None:
+            _expect(t, name, x.dtype, x.shape, cache.device)
+    with _on(cache, stream, K, V, Q, ws) as s:
+        if Kr is None and want_Kr:
+            Kr = torch.zeros(K.shape, dtype=K.dtype, device=K.device)
+        if Qr is None and Q is not None:
+            make = torch.empty if new_len is None else torch.zeros
+            Qr = make(Q.shape, dtype=Q.dtype, device=Q.device)
+        st = lib.quoka_cache_append(cache._ref, kv, vv, qv, _ptr(cos), _ptr(sin), npos, rot,
+                                    ROTATE_NEIGHBOURS if interleaved else 0, _ptr(new_len), _ptr(Kr), _ptr(Qr),
+                                    *_ws_args(ws), s)
+    _check(st, "quoka_cache_append")
+    return Kr, Qr
+
+
+ROTATE_NEIGHBOURS = 1  # quoka_cache_append flag: pairs are neighbouring columns
+
+
+def quoka_cache_select(Q, cache, max_len: int, NQ: int, BSA: int, *, kv_idx=None, kv_count=None, q_idx=None,
+                       s_agg=None, want_q_idx=False, want_s_agg=False, ws=None, stream=None):
+    """Steps (a)-(e) over the cached keys. Returns (kv_idx (b, nkv,
+    min(BSA, max_len)) int32 ascending, kv_count (b, nkv) int32, q_idx or
+    None, s_agg (b, nkv, max_len) or None); max_len bounds cache.seq_len.
+    Entries past a count, and scores past a sequence's end, are not written."""
+    lib = load()
+    b, nkv, d, dev = cache.b, cache.nkv, cache.d, cache.device
+    qv = _heads(Q, "Q", b, None, None, d)
+    nq, BCP = Q.shape[1], Q.shape[2]
+    n = max(0, min(BSA, max_len))
+    for t, name, dtype, shape in ((kv_idx, "kv_idx", torch.int32, (b, nkv, n)),
+                                  (kv_count, "kv_count", torch.int32, (b, nkv)),
+                                  (q_idx, "q_idx", torch.int32, (b, nq, NQ)),
+                                  (s_agg, "s_agg", torch.float32, (b, nkv, max_len))):
+        if t is not None:
+            _expect(t, name, dtype, shape, dev)
+    with _on(cache, stream, Q, ws) as s:
+        if kv_idx is None:
+            kv_idx = torch.empty((b, nkv, n), dtype=torch.int32, device=dev)
+        if kv_count is None:
+            kv_count = torch.empty((b, nkv), dtype=torch.int32, device=dev)
+        if q_idx is None and want_q_idx:
+            q_idx = torch.empty((b, nq, NQ), dtype=torch.int32, device=dev)
+        if s_agg is None and want_s_agg:
+            s_agg = torch.empty((b, nkv, max_len), dtype=torch.float32, device=dev)
+        if ws is None:
+            size = quoka_select_workspace_size(b, nq, nkv, d, max_len, BCP, max(1, NQ), max(0, BSA), Q.dtype)
+            ws = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+        st = lib.quoka_cache_select(qv, cache._ref, max_len, NQ, BSA, _ptr(kv_idx) if n else None, _ptr(kv_count),
+                                    _ptr(q_idx), _ptr(s_agg) if max_len else None, *_ws_args(ws), s)
+    _check(st, "quoka_cache_select")
+    return kv_idx, kv_count, q_idx, s_agg
+
+
+def _index_list(cache, max_len, kv_idx, kv_count):
+    """The rows N of an index list (b, nkv, N) with counts, or max_len without one."""
+    if (kv_idx is None) != (kv_count is None):
+        raise ValueError("kv_idx and kv_count go together")
+    if kv_idx is None:
+        return max_len
+    if kv_idx.dim() != 3:
+        raise ValueError("kv_idx must be (b, nkv, N)")
+    _expect(kv_idx, "kv_idx", torch.int32, (cache.b, cache.nkv, kv_idx.shape[2]), cache.device)
+    _expect(kv_count, "kv_count", torch.int32, (cache.b, cache.nkv), cache.device)
+    return kv_idx.shape[2]
+
+
+def quoka_cache_gather(cache, max_len: int, kv_idx=None, kv_count=None, *, dtype=torch.bfloat16, Ksel=None, Vsel=None,
+                       ws=None, stream=None):
+    """Step (f) over the cache. Returns (Ksel, Vsel) (b, nkv, N, d) of dtype
+    (bfloat16 or float32): the rows of the index list kv_idx (b, nkv, N) with
+    kv_count (b, nkv), or, without one, all rows below each seq_len (N =
+    max_len). Rows past the count are zeros."""
+    lib = load()
+    n = _index_list(cache, max_len, kv_idx, kv_count)
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype}")
+    shape = (cache.b, cache.nkv, n, cache.d)
+    for t, name in ((Ksel, "Ksel"), (Vsel, "Vsel")):
+        if t is not None:
+            _expect(t, name, dtype, shape, cache.device)
+    with _on(cache, stream, ws) as s:
+        if Ksel is None:
+            Ksel = torch.empty(shape, dtype=dtype, device=cache.device)
+        if Vsel is None:
+            Vsel = torch.empty(shape, dtype=dtype, device=cache.device)
+        idx = kv_count if kv_idx is not None and n == 0 else kv_idx  # (an empty list is a list: not null)
+        st = lib.quoka_cache_gather(cache._ref, max_len, _ptr(idx), _ptr(kv_count), n, _code(dtype),
+                                    _ptr(Ksel) if n else None, _ptr(Vsel) if n else None, *_ws_args(ws), s)
+    _check(st, "quoka_cache_gather")
+    return Ksel, Vsel
+
+
+def quoka_cache_attn_workspace_size(b, nq, nkv, d, BCP, N, dtype) -> int:
+    return int(load().quoka_cache_attn_workspace_size(b, nq, nkv, d, BCP, N, _code(dtype)))
+
+
+def quoka_cache_attn(Q, cache, max_len: int, kv_idx=None, kv_count=None, Kc=None, Vc=None, scale=None, *, O=None,
+                     lse=None, want_lse=False, ws=None, stream=None):
+    """Steps (f)+(g) over the cache: attention of Q (b, nq, BCP, d) over the
+    cached keys of an index list (or all below each seq_len) and the chunk's
+    own keys Kc, Vc (b, nkv, BCP, d), causal (None: without them). Returns
+    (O (b, nq, BCP, d), lse (b, nq, BCP) or None); a row that sees no key gives
+    0 and -inf. `ws` defaults to a new workspace of
+    quoka_cache_attn_workspace_size bytes."""
+    lib = load()
+    b, nkv, d, dev = cache.b, cache.nkv, cache.d, cache.device
+    qv = _heads(Q, "Q", b, None, None, d)
+    nq, BCP = Q.shape[1], Q.shape[2]
+    n = _index_list(cache, max_len, kv_idx, kv_count)
+    if (Kc is None) != (Vc is None):
+        raise ValueError("Kc and Vc go together")
+    kcv = None if Kc is None else _heads(Kc, "Kc", b, nkv, BCP, d)
+    vcv = None if Vc is None else _heads(Vc, "Vc", b, nkv, BCP, d)
+    if O is not None:
+        _expect(O, "O", Q.dtype, Q.shape, dev)
+    if lse is not None:
+        _expect(lse, "lse", torch.float32, Q.shape[:3], dev)
+    if scale is None:
+        scale = d ** -0.5
+    with _on(cache, stream, Q, Kc, Vc, ws) as s:
+        if O is None:
+            O = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        if lse is None and want_lse:
+            lse = torch.empty((b, nq, BCP), dtype=torch.float32, device=dev)
+        if ws is None:
+            size = quoka_cache_attn_workspace_size(b, nq, nkv, d, BCP, n, Q.dtype)
+            ws = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+        idx = kv_count if kv_idx is not None and n == 0 else kv_idx  # (an empty list is a list: not null)
+        st = lib.quoka_cache_attn(qv, cache._ref, max_len, _ptr(idx), _ptr(kv_count), n, kcv, vcv, float(scale),
+                                  _ptr(O), _ptr(lse), *_ws_args(ws), s)
+    _check(st, "quoka_cache_attn")
     return O, lse

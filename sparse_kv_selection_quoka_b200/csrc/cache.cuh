@@ -1,0 +1,88 @@
+// Device helpers of the paged 8-bit cache: addressing, and the conversions
+// between e4m3 codes and wider types.
+//
+// The cache holds keys and values as e4m3 codes in pages of `page` tokens,
+// each page with one scale per KV head for its keys and one for its values,
+// a power of two 2^e: a row's value is code * 2^e. With a power of two the
+// product is exact in fp16, bf16 and fp32, a code moved to a larger scale
+// keeps its value unless it becomes subnormal, and a scale acts on a score
+// (base-2 logarithm) as an addition of e.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace quoka {
+namespace cache {
+
+// Two e4m3 codes (low byte first) to two halves; every code is exact in fp16.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+
+// Two floats to e4m3 codes (lo in the low byte), to nearest even; beyond
+// +-448 (infinities too) saturates, NaN stays NaN.
+__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t c, float* v) {
+  const uint32_t a = e4m3x2_to_f16x2((uint16_t)c), b = e4m3x2_to_f16x2((uint16_t)(c >> 16));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  v[0] = x.x;
+  v[1] = x.y;
+  v[2] = y.x;
+  v[3] = y.y;
+}
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// The exponent of a stored scale. Only the exponent field is used, kept to
+// the range of scales; anything that is not a power of two in that range is
+// latched.
+__device__ __forceinline__ int scale_exp(float s, int* status) {
+  const int u = __float_as_int(s);
+  const int e = (u >> 23) - 127;  // (a sign bit makes it negative, out of range)
+  const int k = min(max(e, kCacheMinExp), kCacheMaxExp);
+  if ((k != e || (u & 0x7FFFFF) != 0) && status != nullptr) latch_status(status, 6 /* QUOKA_ERR_BOUNDS */);
+  return k;
+}
+
+// The smallest e with amax <= 448 * 2^e (448 = 1.75 * 2^8), in the range of
+// scales; amax is finite and >= 0.
+__device__ __forceinline__ int scale_exp_for(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int k = (int)(u >> 23) - 127;  // amax = m * 2^k, 1 <= m < 2 (subnormals lie below every scale)
+  const int e = k - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return min(max(e, kCacheMinExp), kCacheMaxExp);
+}
+
+// Tokens a kernel may read of sequence bi: seq_len, kept to [0, max_len].
+// A length outside that range is latched.
+__device__ __forceinline__ int cache_len(const CacheView& c, int bi, int max_len, int* status) {
+  const int n = __ldcg(c.seq_len + bi);
+  if ((n < 0 || n > max_len) && status != nullptr) latch_status(status, 6 /* QUOKA_ERR_BOUNDS */);
+  return min(max(n, 0), max_len);
+}
+
+// The page of table column `col` of sequence bi, or -1 (latched) when the
+// entry names none.
+__device__ __forceinline__ int cache_page(const CacheView& c, int bi, int col, int* status) {
+  const int p = __ldcg(c.page_table + (int64_t)bi * c.table_stride + col);
+  if (p >= 0 && p < c.npages) return p;
+  if (status != nullptr) latch_status(status, 6 /* QUOKA_ERR_BOUNDS */);
+  return -1;
+}
+
+}  // namespace cache
+}  // namespace quoka

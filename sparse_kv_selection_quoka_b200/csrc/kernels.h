@@ -79,10 +79,11 @@ cudaError_t launch_score_tc(int d, Strided K, int b, int nkv, int64_t T,
 int64_t topk_max_T();
 // `hist`, when not null, is the (b * nkv, TOPK_HIST_BINS) histogram of the
 // scores' value buckets made by the scoring kernel; the first pass is then
-// skipped.
+// skipped. `row_len`, when not null, holds each batch entry's own number of
+// keys (b, clamped to [0, T]): its rows pick min(bsa, row_len) of them.
 cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa,
                         const uint32_t* hist, int32_t* kv_idx, int32_t* kv_count, int* status,
-                        bool pdl, cudaStream_t stream);
+                        bool pdl, cudaStream_t stream, const int32_t* row_len = nullptr);
 
 // Step (f): gather of the selected K and V rows into contiguous
 // (b, nkv, bsa, d) buffers. Rows past kv_count, and rows whose index is out
@@ -157,5 +158,89 @@ struct DecodeArgs {
 };
 int decode_splits(int bsa, int BCP);
 cudaError_t launch_decode_attn(bool bf16, const DecodeArgs& a, bool pdl, cudaStream_t stream);
+
+// ---- the paged 8-bit cache (cache.cuh)
+
+constexpr int kCacheMinExp = -50, kCacheMaxExp = 50;  // scales are 2^e, e in this range
+
+// Pages of e4m3 codes with one scale per page and KV head; strides in bytes.
+struct CacheView {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;  // (npages, nkv)
+  float* v_scale;
+  int64_t sp, sh, sr;  // strides of page, head and row
+  int npages, nkv, page_log2;
+  const int32_t* page_table;  // (b, table_stride)
+  int64_t table_stride;
+  const int32_t* seq_len;  // (b)
+};
+
+// Appends a chunk to the cache, rotating keys (and queries into Qr) by their
+// positions (cache_append.cu).
+struct CacheAppendArgs {
+  CacheView c;
+  Strided K, V, Q;
+  int b, nq, BCP;
+  const float* cos;  // (npos, rot / 2); unused when rot = 0
+  const float* sin;
+  int rot, interleaved;
+  const int32_t* new_len;  // (b) or null: BCP each
+  int limit;               // positions below it can be appended
+  void* Kr;                // (b, nkv, BCP, d) or null
+  void* Qr;                // (b, nq, BCP, d) or null (then Q is not read)
+  int* status;
+};
+cudaError_t launch_cache_append(bool bf16, int d, const CacheAppendArgs& a, bool pdl, cudaStream_t stream);
+
+// Rows of the cache, dequantised into (b, nkv, N, d); without kv_idx row n is
+// key n. Rows past the count are zeros (cache_gather.cu).
+struct CacheGatherArgs {
+  CacheView c;
+  int b, max_len;
+  const int32_t* kv_idx;    // (b, nkv, N) or null
+  const int32_t* kv_count;  // (b, nkv), with kv_idx
+  int N;
+  void* Ksel;
+  void* Vsel;
+  int32_t* count_out;  // (b, nkv) or null: the rows there are
+  int* status;
+};
+cudaError_t launch_cache_gather(bool bf16, int d, const CacheGatherArgs& a, bool pdl, cudaStream_t stream);
+
+// Attention of at most kCacheMaxRows query rows per KV head over the cache
+// and the chunk's own keys, by key ranges joined by a second kernel
+// (cache_attn.cu).
+constexpr int kCacheMaxRows = 64;  // G * BCP
+struct CacheAttnArgs {
+  CacheView c;
+  Strided Q, Kc, Vc;
+  int b, nq, BCP, max_len;
+  const int32_t* kv_idx;    // (b, nkv, N) or null: all keys below seq_len
+  const int32_t* kv_count;  // (b, nkv), with kv_idx
+  int N;                    // most keys of a row
+  int chunk;                // 1: the chunk's own keys too
+  float scale;
+  float* O_parts;           // (nsplit, b, nq, BCP, d) fp32
+  float* lse_parts;         // (nsplit, b, nq, BCP) fp32, in log2 units
+  int nsplit;               // cache_attn_splits(b * nkv, N)
+  void* O;
+  float* lse;
+  int* status;
+};
+int cache_attn_splits(int64_t heads, int N);
+cudaError_t launch_cache_attn(bool bf16, int d, const CacheAttnArgs& a, bool pdl, cudaStream_t stream);
+
+// Step (d) over the cache's keys: S_agg (b, nkv, max_len); entries at and
+// past seq_len are not written (cache_score.cu).
+struct CacheScoreArgs {
+  CacheView c;
+  int b, max_len;
+  const float* Qg;  // (b, nkv, NQ, d) fp32 group means
+  int NQ;
+  float* S_agg;
+  int* status;
+};
+cudaError_t launch_cache_score(int d, const CacheScoreArgs& a, cudaStream_t stream);
 
 }  // namespace quoka

@@ -425,6 +425,102 @@ quoka_status run_decode(const quoka_tensor* Q, const quoka_tensor* K, const quok
   return cuda_status(quoka::launch_decode_attn(Q->dtype == QUOKA_BF16, a, pdl, stream));
 }
 
+// ---- the paged 8-bit cache
+
+bool cache_page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+// Checks the description of a cache and turns it into the kernels' view.
+quoka_status validate_cache(const quoka_cache* c, quoka::CacheView* v) {
+  if (c == nullptr || c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr ||
+      c->page_table == nullptr || c->seq_len == nullptr)
+    return QUOKA_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v)) return QUOKA_ERR_INVALID_ARG;
+  if (c->npages < 1 || c->nkv < 1 || c->b < 1 || c->max_pages < 1 || c->table_stride < c->max_pages)
+    return QUOKA_ERR_INVALID_ARG;
+  const int64_t st[3] = {c->page_stride, c->head_stride, c->row_stride};
+  const int64_t n[3] = {c->npages, c->nkv, c->page};
+  for (int i = 0; i < 3; ++i)
+    if (st[i] < 0 || st[i] % 16 != 0 || (n[i] > 1 && st[i] < c->d)) return QUOKA_ERR_INVALID_ARG;
+  if (!supported_d(c->d) || !cache_page_ok(c->page)) return QUOKA_ERR_UNSUPPORTED;
+  if (c->b > kMaxHeads || c->nkv > kMaxHeads || c->npages > (int64_t)INT32_MAX) return QUOKA_ERR_UNSUPPORTED;
+  v->k = static_cast<uint8_t*>(c->k);
+  v->v = static_cast<uint8_t*>(c->v);
+  v->k_scale = c->k_scale;
+  v->v_scale = c->v_scale;
+  v->sp = st[0];
+  v->sh = st[1];
+  v->sr = st[2];
+  v->npages = (int)c->npages;
+  v->nkv = c->nkv;
+  v->page_log2 = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
+  v->page_table = c->page_table;
+  v->table_stride = c->table_stride;
+  v->seq_len = c->seq_len;
+  return QUOKA_OK;
+}
+
+// Positions that the page table's columns cover (kept clear of the end of int32).
+int cache_room(const quoka_cache* c) {
+  return (int)std::min<int64_t>((int64_t)c->max_pages * c->page, (int64_t)1 << 30);
+}
+
+// The optional workspace of the calls that only need the status words there:
+// clears them and returns their address.
+quoka_status optional_status(void* ws, size_t ws_bytes, cudaStream_t stream, int** status) {
+  *status = nullptr;
+  if (ws == nullptr) return QUOKA_OK;
+  if (((uintptr_t)ws % kAlign) != 0 || ws_bytes < 2 * sizeof(int)) return QUOKA_ERR_WORKSPACE;
+  *status = static_cast<int*>(ws);
+  return quoka::clear_status_async(*status, stream) == cudaSuccess ? QUOKA_OK : QUOKA_ERR_CUDA;
+}
+
+// Whether [a, a + na) and the bytes that t spans overlap.
+bool overlaps(const void* a, size_t na, const quoka_tensor* t) {
+  int64_t last = 0;
+  for (int i = 0; i < 4; ++i) {
+    if (t->shape[i] == 0) return false;
+    last += (t->shape[i] - 1) * t->stride[i];
+  }
+  const uintptr_t a0 = (uintptr_t)a, t0 = (uintptr_t)t->data;
+  const uintptr_t t1 = t0 + (size_t)(last + 1) * elt_size(t->dtype);
+  return a0 < t1 && t0 < a0 + na;
+}
+
+// Workspace of quoka_cache_attn: the status words, then either the partials
+// of the key ranges (few query rows) or the dequantised keys and values with
+// their counts and the partials of the tensor-core attention.
+struct CacheAttnWs {
+  bool few;
+  int nsplit;
+  size_t o_parts, lse_parts, ksel, vsel, count, aparts, aparts_bytes, total;
+};
+
+CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t BCP, int64_t N, quoka_dtype dtype,
+                          bool no_chunk) {
+  CacheAttnWs w = {};
+  size_t off = kAlign;
+  auto take = [&](size_t bytes) {
+    const size_t p = off;
+    off += align_up(bytes);
+    return p;
+  };
+  w.few = (nq / nkv) * BCP <= quoka::kCacheMaxRows;
+  if (w.few) {
+    w.nsplit = quoka::cache_attn_splits(b * nkv, (int)N);
+    const int64_t rows = w.nsplit * b * nq * BCP;
+    w.o_parts = take((size_t)(rows * d) * 4);
+    w.lse_parts = take((size_t)rows * 4);
+  } else {
+    w.ksel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
+    w.vsel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
+    w.count = take((size_t)(b * nkv) * 4);
+    w.aparts_bytes = attn_parts_bytes(b, nq, BCP, d, attn_nsplit(b, nq, BCP, d, N, dtype == QUOKA_BF16, no_chunk));
+    w.aparts = take(w.aparts_bytes);
+  }
+  w.total = off;
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -639,6 +735,220 @@ quoka_status quoka_prefill_chunk(const quoka_tensor* Q, const quoka_tensor* K,
   return gather_then_attn(Q, K, V, Kc, Vc, as, kv_idx, kv_count, (int)bsa_eff, scale, O, lse,
                           gb ? at<void>(ws, L.ksel) : nullptr, gb ? at<void>(ws, L.vsel) : nullptr, status, cs,
                           false, L.aparts_bytes > 0 ? at<void>(ws, L.aparts) : nullptr, L.aparts_bytes);
+}
+
+quoka_status quoka_cache_append(const quoka_cache* cache, const quoka_tensor* K, const quoka_tensor* V,
+                                const quoka_tensor* Q, const float* cos, const float* sin, int64_t npos, int rot,
+                                uint32_t flags, const int32_t* new_len, void* Kr, void* Qr, void* ws,
+                                size_t ws_bytes, void* stream) {
+  quoka::NvtxRange nvtx_range("quoka_cache_append");
+  quoka::CacheAppendArgs a = {};
+  quoka_status st = validate_cache(cache, &a.c);
+  if (st != QUOKA_OK) return st;
+  if ((flags & ~QUOKA_ROTATE_NEIGHBOURS) != 0u || K == nullptr || V == nullptr) return QUOKA_ERR_INVALID_ARG;
+  if (K->dtype != QUOKA_F32 && K->dtype != QUOKA_BF16) return QUOKA_ERR_INVALID_ARG;
+  int64_t ks[4] = {cache->b, cache->nkv, -1, cache->d};
+  if (!check_tensor(K, K->dtype, ks) || !check_tensor(V, K->dtype, ks)) return QUOKA_ERR_INVALID_ARG;
+  const int64_t BCP = ks[2];
+  int64_t nq = 0;
+  if ((Q == nullptr) != (Qr == nullptr)) return QUOKA_ERR_INVALID_ARG;
+  if (Q != nullptr) {
+    int64_t qs[4] = {cache->b, -1, BCP, cache->d};
+    if (!check_tensor(Q, K->dtype, qs) || qs[1] < 1) return QUOKA_ERR_INVALID_ARG;
+    nq = qs[1];
+    if (!aligned16(Qr)) return QUOKA_ERR_INVALID_ARG;
+  }
+  if (rot < 0 || rot > cache->d || rot % 16 != 0) return QUOKA_ERR_INVALID_ARG;
+  if (rot > 0 && (cos == nullptr || sin == nullptr || !aligned16(cos) || !aligned16(sin) || npos < 1))
+    return QUOKA_ERR_INVALID_ARG;
+  if (Kr != nullptr && !aligned16(Kr)) return QUOKA_ERR_INVALID_ARG;
+  if (BCP > kMaxBCP || nq > kMaxHeads) return QUOKA_ERR_UNSUPPORTED;
+  // the rotation reads both columns of a pair: it cannot run in place
+  const size_t es = elt_size(K->dtype), kb = (size_t)(cache->b * cache->nkv * BCP * cache->d) * es;
+  const size_t qb = (size_t)(cache->b * nq * BCP * cache->d) * es;
+  const quoka_tensor* ins[3] = {K, V, Q};
+  for (const quoka_tensor* t : ins) {
+    if (t == nullptr) continue;
+    if (Kr != nullptr && overlaps(Kr, kb, t)) return QUOKA_ERR_INVALID_ARG;
+    if (Qr != nullptr && overlaps(Qr, qb, t)) return QUOKA_ERR_INVALID_ARG;
+  }
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  st = optional_status(ws, ws_bytes, cs, &a.status);
+  if (st != QUOKA_OK || BCP == 0) return st;
+  a.K = strided(K);
+  a.V = strided(V);
+  if (Q != nullptr) a.Q = strided(Q);
+  a.b = cache->b;
+  a.nq = (int)nq;
+  a.BCP = (int)BCP;
+  a.cos = cos;
+  a.sin = sin;
+  a.rot = rot;
+  a.interleaved = (flags & QUOKA_ROTATE_NEIGHBOURS) != 0u ? 1 : 0;
+  a.new_len = new_len;
+  a.limit = rot > 0 ? (int)std::min<int64_t>(cache_room(cache), npos) : cache_room(cache);
+  a.Kr = Kr;
+  a.Qr = Qr;
+  return cuda_status(quoka::launch_cache_append(K->dtype == QUOKA_BF16, cache->d, a, a.status != nullptr, cs));
+}
+
+quoka_status quoka_cache_select(const quoka_tensor* Q, const quoka_cache* cache, int max_len, int NQ, int BSA,
+                                int32_t* kv_idx, int32_t* kv_count, int32_t* q_idx, float* s_agg, void* ws,
+                                size_t ws_bytes, void* stream) {
+  quoka::NvtxRange nvtx_range("quoka_cache_select");
+  quoka::CacheScoreArgs a = {};
+  quoka_status st = validate_cache(cache, &a.c);
+  if (st != QUOKA_OK) return st;
+  if (Q == nullptr || (Q->dtype != QUOKA_F32 && Q->dtype != QUOKA_BF16)) return QUOKA_ERR_INVALID_ARG;
+  int64_t qs[4] = {cache->b, -1, -1, cache->d};
+  if (!check_tensor(Q, Q->dtype, qs)) return QUOKA_ERR_INVALID_ARG;
+  const int b = cache->b, nkv = cache->nkv, d = cache->d;
+  if (qs[1] < 1 || qs[2] < 1 || qs[1] % nkv != 0 || NQ < 1 || NQ > qs[2] || BSA < 0) return QUOKA_ERR_INVALID_ARG;
+  if (max_len < 0 || max_len > cache_room(cache) || kv_count == nullptr) return QUOKA_ERR_INVALID_ARG;
+  if (qs[1] > kMaxHeads || qs[2] > kMaxBCP || max_len > quoka::topk_max_T()) return QUOKA_ERR_UNSUPPORTED;
+  const int nq = (int)qs[1], BCP = (int)qs[2], bsa_eff = std::min(BSA, max_len);
+  if (bsa_eff > 0 && kv_idx == nullptr) return QUOKA_ERR_INVALID_ARG;
+  const WsLayout L = ws_layout(b, nq, nkv, d, max_len, NQ, bsa_eff, false);
+  st = check_ws(ws, ws_bytes, L.select_total);
+  if (st != QUOKA_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const bool bf = Q->dtype == QUOKA_BF16;
+  float* qg = at<float>(ws, L.qgroup);
+  int32_t* qidx = q_idx != nullptr ? q_idx : at<int32_t>(ws, L.qidx);
+  a.status = at<int>(ws, L.status);
+  // (the status words are cleared by the kernel that makes the group means)
+  cudaError_t e = cudaErrorNotSupported;
+  if (bf && d == 128)
+    e = quoka::launch_qsel_group_fast(strided(Q), b, nq, nkv, BCP, NQ, qidx, qg, nullptr, nullptr, a.status, true, cs);
+  if (e == cudaErrorNotSupported) {
+    e = quoka::launch_qsel(bf, d, strided(Q), b, nq, BCP, NQ, at<float>(ws, L.qhat), qidx, true, cs);
+    if (e != cudaSuccess) return cuda_status(e);
+    e = quoka::launch_qgroup(d, at<float>(ws, L.qhat), b, nq, nkv, NQ, qg, nullptr, nullptr, a.status, cs);
+  }
+  if (e != cudaSuccess) return cuda_status(e);
+  a.b = b;
+  a.max_len = max_len;
+  a.Qg = qg;
+  a.NQ = NQ;
+  a.S_agg = s_agg != nullptr ? s_agg : at<float>(ws, L.sagg);
+  if (max_len > 0) {
+    e = quoka::launch_cache_score(d, a, cs);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  if (bsa_eff > 0)
+    return cuda_status(quoka::launch_topk(a.S_agg, b, nkv, max_len, bsa_eff, nullptr, kv_idx, kv_count, a.status, true,
+                                          cs, cache->seq_len));
+  return cudaMemsetAsync(kv_count, 0, sizeof(int32_t) * b * nkv, cs) == cudaSuccess ? QUOKA_OK : QUOKA_ERR_CUDA;
+}
+
+quoka_status quoka_cache_gather(const quoka_cache* cache, int max_len, const int32_t* kv_idx,
+                                const int32_t* kv_count, int N, quoka_dtype dtype, void* Ksel, void* Vsel, void* ws,
+                                size_t ws_bytes, void* stream) {
+  quoka::NvtxRange nvtx_range("quoka_cache_gather");
+  quoka::CacheGatherArgs a = {};
+  quoka_status st = validate_cache(cache, &a.c);
+  if (st != QUOKA_OK) return st;
+  if (dtype != QUOKA_F32 && dtype != QUOKA_BF16) return QUOKA_ERR_INVALID_ARG;
+  if (max_len < 0 || max_len > cache_room(cache) || N < 0 || (kv_idx == nullptr) != (kv_count == nullptr))
+    return QUOKA_ERR_INVALID_ARG;
+  if (kv_idx == nullptr && N != max_len) return QUOKA_ERR_INVALID_ARG;
+  if (N > 0 && (Ksel == nullptr || Vsel == nullptr || !aligned16(Ksel) || !aligned16(Vsel)))
+    return QUOKA_ERR_INVALID_ARG;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  st = optional_status(ws, ws_bytes, cs, &a.status);
+  if (st != QUOKA_OK || N == 0) return st;
+  a.b = cache->b;
+  a.max_len = max_len;
+  a.kv_idx = kv_idx;
+  a.kv_count = kv_count;
+  a.N = N;
+  a.Ksel = Ksel;
+  a.Vsel = Vsel;
+  return cuda_status(quoka::launch_cache_gather(dtype == QUOKA_BF16, cache->d, a, a.status != nullptr, cs));
+}
+
+size_t quoka_cache_attn_workspace_size(int b, int nq, int nkv, int d, int BCP, int N, quoka_dtype dtype) {
+  if (b < 1 || nq < 1 || nkv < 1 || BCP < 1 || N < 0 || nq % nkv != 0 || !supported_d(d)) return 0;
+  if (dtype != QUOKA_F32 && dtype != QUOKA_BF16) return 0;
+  return std::max(cache_attn_ws(b, nq, nkv, d, BCP, N, dtype, false).total,
+                  cache_attn_ws(b, nq, nkv, d, BCP, N, dtype, true).total);
+}
+
+quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, int max_len, const int32_t* kv_idx,
+                              const int32_t* kv_count, int N, const quoka_tensor* Kc, const quoka_tensor* Vc,
+                              float scale, void* O, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  quoka::NvtxRange nvtx_range("quoka_cache_attn");
+  quoka::CacheAttnArgs a = {};
+  quoka_status st = validate_cache(cache, &a.c);
+  if (st != QUOKA_OK) return st;
+  if (Q == nullptr || (Q->dtype != QUOKA_F32 && Q->dtype != QUOKA_BF16)) return QUOKA_ERR_INVALID_ARG;
+  int64_t qs[4] = {cache->b, -1, -1, cache->d};
+  if (!check_tensor(Q, Q->dtype, qs)) return QUOKA_ERR_INVALID_ARG;
+  const int64_t b = cache->b, nkv = cache->nkv, d = cache->d, nq = qs[1], BCP = qs[2];
+  if (nq < 1 || BCP < 1 || nq % nkv != 0) return QUOKA_ERR_INVALID_ARG;
+  if ((Kc == nullptr) != (Vc == nullptr)) return QUOKA_ERR_INVALID_ARG;
+  int64_t cs4[4] = {b, nkv, BCP, d};
+  if (Kc != nullptr && (!check_tensor(Kc, Q->dtype, cs4) || !check_tensor(Vc, Q->dtype, cs4)))
+    return QUOKA_ERR_INVALID_ARG;
+  if (max_len < 0 || max_len > cache_room(cache) || N < 0 || (kv_idx == nullptr) != (kv_count == nullptr))
+    return QUOKA_ERR_INVALID_ARG;
+  if (kv_idx == nullptr && N != max_len) return QUOKA_ERR_INVALID_ARG;
+  if (O == nullptr || !aligned16(O) || !(scale > 0.f)) return QUOKA_ERR_INVALID_ARG;
+  if (nq > kMaxHeads || BCP > kMaxBCP) return QUOKA_ERR_UNSUPPORTED;
+  const bool no_chunk = Kc == nullptr, bf = Q->dtype == QUOKA_BF16;
+  const CacheAttnWs w = cache_attn_ws(b, nq, nkv, d, BCP, N, Q->dtype, no_chunk);
+  st = check_ws(ws, ws_bytes, w.total);
+  if (st != QUOKA_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  int* status = static_cast<int*>(ws);
+  if (quoka::clear_status_async(status, cs) != cudaSuccess) return QUOKA_ERR_CUDA;
+  if (w.few) {
+    a.Q = strided(Q);
+    if (!no_chunk) {
+      a.Kc = strided(Kc);
+      a.Vc = strided(Vc);
+    }
+    a.b = (int)b;
+    a.nq = (int)nq;
+    a.BCP = (int)BCP;
+    a.max_len = max_len;
+    a.kv_idx = kv_idx;
+    a.kv_count = kv_count;
+    a.N = N;
+    a.chunk = no_chunk ? 0 : 1;
+    a.scale = scale;
+    a.O_parts = at<float>(ws, w.o_parts);
+    a.lse_parts = at<float>(ws, w.lse_parts);
+    a.nsplit = w.nsplit;
+    a.O = O;
+    a.lse = lse;
+    a.status = status;
+    return cuda_status(quoka::launch_cache_attn(bf, (int)d, a, true, cs));
+  }
+  // many query rows: the rows dequantised once, then the attention over dense rows
+  if (N > 0) {
+    quoka::CacheGatherArgs g = {};
+    g.c = a.c;
+    g.b = (int)b;
+    g.max_len = max_len;
+    g.kv_idx = kv_idx;
+    g.kv_count = kv_count;
+    g.N = N;
+    g.Ksel = at<void>(ws, w.ksel);
+    g.Vsel = at<void>(ws, w.vsel);
+    g.count_out = at<int32_t>(ws, w.count);
+    g.status = status;
+    const cudaError_t e = quoka::launch_cache_gather(bf, (int)d, g, true, cs);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  const int64_t sh = (int64_t)N * d, sb = nkv * sh;
+  const AttnShapes s{b, nq, nkv, d, N, BCP};
+  quoka_tensor own = *Q;  // without chunk keys: any valid tensor of their shape, not read
+  own.shape[1] = nkv;
+  return run_attn(Q, Strided{at<void>(ws, w.ksel), sb, sh, d}, Strided{at<void>(ws, w.vsel), sb, sh, d},
+                  no_chunk ? &own : Kc, no_chunk ? &own : Vc, s, N, nullptr, at<int32_t>(ws, w.count), N, scale, O,
+                  lse, status, cs, true, no_chunk, w.aparts_bytes > 0 ? at<void>(ws, w.aparts) : nullptr,
+                  w.aparts_bytes);
 }
 
 quoka_status quoka_get_device_status(const void* ws, void* stream, int32_t* device_status) {

@@ -122,7 +122,8 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 template <bool CLUSTER>
 __global__ void __launch_bounds__(TOPK_THREADS)
 topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const uint32_t* __restrict__ ghist,
-            int32_t* __restrict__ kv_idx, int32_t* __restrict__ kv_count, const int* __restrict__ status) {
+            const int32_t* __restrict__ row_len, int32_t* __restrict__ kv_idx, int32_t* __restrict__ kv_count,
+            const int* __restrict__ status) {
   extern __shared__ uint32_t smem_dyn[];
   uint32_t* keys = smem_dyn;          // [slice]: this CTA's keys
   uint32_t* glist = smem_dyn + slice;  // [TOPK_LIST_MAX]: all ranks' candidates, in rank order
@@ -137,10 +138,20 @@ topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const ui
   const int64_t row = (int64_t)bi * nkv + j;
   const float* Sr = S + row * T;
   const int64_t lo = (int64_t)c * slice;
-  const int n = (int)max((int64_t)0, min((int64_t)slice, T - lo));
+  // the row's keys (per batch entry when row_len is given: an input of the
+  // call, written by no kernel of it) and picks; every CTA of a row's cluster
+  // leaves here together when it has none
+  const int64_t Tr = row_len != nullptr ? max((int64_t)0, min((int64_t)__ldg(row_len + bi), T)) : T;
+  const int take_n = (int)min((int64_t)bsa, Tr);
+  const int n = (int)max((int64_t)0, min((int64_t)slice, Tr - lo));
   const int n_round = (n + TOPK_THREADS - 1) / TOPK_THREADS * TOPK_THREADS;
 
   pdl_trigger();
+  if (take_n == 0) {
+    pdl_wait();
+    if (c == 0 && tid == 0) kv_count[row] = 0;
+    return;
+  }
   if (tid == 0) {
     sh.kmin = 0xFFFFFFFFu;
     sh.kmax = 0u;
@@ -253,7 +264,7 @@ topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const ui
   // testing the bucket (histograms summed over the cluster); else walk
   // list[0 .. nlist) (this CTA alone). Returns u*; `need` becomes the
   // number of keys == u* to keep.
-  uint32_t need = (uint32_t)bsa;  // rank (1-based, from the top) still to place
+  uint32_t need = (uint32_t)take_n;  // rank (1-based, from the top) still to place
   uint32_t b0 = 0u, above = 0u;
   auto exact_passes = [&](uint32_t kmin, uint32_t kmax, bool full_scan, const uint32_t* list, int nlist) {
     uint32_t prefix = kmin;  // all candidates equal: u* is their key
@@ -566,14 +577,14 @@ topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const ui
       bool take = k[u] > ustar;
       if (k[u] == ustar) take = eq_seen++ < take_cta;
       if (take) {
-        if (pos < (uint32_t)bsa) dst[pos] = (int32_t)(lo + e0 + u);
+        if (pos < (uint32_t)take_n) dst[pos] = (int32_t)(lo + e0 + u);
         ++pos;
       }
     }
     out_base += (tot >> 16) + min(eq_base + (tot & 0xFFFFu), take_cta) - min(eq_base, take_cta);
     eq_base += tot & 0xFFFFu;
   }
-  if (c == 0 && tid == 0) kv_count[row] = bsa;
+  if (c == 0 && tid == 0) kv_count[row] = take_n;
   // every CTA stays until the others are done reading its shared memory
   if (CLUSTER) {
     if (gathered) cluster_wait();
@@ -586,7 +597,8 @@ topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const ui
 int64_t topk_max_T() { return (int64_t)TOPK_MAX_CLUSTER * TOPK_MAX_SLICE; }
 
 cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, const uint32_t* hist,
-                        int32_t* kv_idx, int32_t* kv_count, int* status, bool pdl, cudaStream_t stream) {
+                        int32_t* kv_idx, int32_t* kv_count, int* status, bool pdl, cudaStream_t stream,
+                        const int32_t* row_len) {
   // (every wait in the kernel is a hardware barrier phase that all threads
   // reach; `status` is only read, to skip the select after an earlier fault)
   if (bsa <= 0 || T <= 0 || bsa > T || T > topk_max_T()) return cudaErrorInvalidValue;
@@ -620,7 +632,7 @@ cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, 
   }
   cfg.attrs = attr;
   cfg.numAttrs = na;
-  return cudaLaunchKernelEx(&cfg, kern, S_agg, T, bsa, slice, hist, kv_idx, kv_count,
+  return cudaLaunchKernelEx(&cfg, kern, S_agg, T, bsa, slice, hist, row_len, kv_idx, kv_count,
                             static_cast<const int*>(status));
 }
 

@@ -1,0 +1,804 @@
+"""The paged 8-bit cache: quoka_cache_append, _select, _gather and _attn
+against plain 64-bit forms, their edge cases, their refusals, and the calls
+together as a serving loop makes them."""
+import ctypes
+
+import pytest
+import torch
+
+from tests import parity as P
+from tests.test_library import _view, lib  # noqa: F401 (lib is a fixture)
+
+E4M3 = torch.float8_e4m3fn
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+gpu = pytest.mark.gpu
+
+
+def q():
+    import sparse_kv_selection_quoka_b200 as m
+    return m
+
+
+# ------------------------------------------------------------ plain forms
+
+def code_values():
+    """The 256 values of e4m3, from the format: sign, 4 bits of exponent (bias 7), 3 of fraction."""
+    out = []
+    for u in range(256):
+        e, f, s = (u >> 3) & 15, u & 7, -1.0 if u >> 7 else 1.0
+        out.append(float("nan") if u & 127 == 127 else s * (f / 8 * 2.0**-6 if e == 0 else (1 + f / 8) * 2.0 ** (e - 7)))
+    return torch.tensor(out, dtype=torch.float64)
+
+
+VALUES = code_values()
+GRID = VALUES[:127]  # 0 .. 448, ascending
+
+
+def encode(y):
+    """e4m3 codes of 64-bit numbers: the nearest value, ties to the even code, at most 448 in magnitude."""
+    m = y.abs().clamp(max=448.0).nan_to_num(0.0)
+    hi = torch.searchsorted(GRID, m).clamp(max=126)  # GRID[hi] >= m
+    lo = (hi - 1).clamp(min=0)
+    up, down = GRID[hi] - m, m - GRID[lo]
+    code = torch.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    code = torch.where(GRID[hi] == m, hi, code)
+    code = code + 128 * torch.signbit(y).long()
+    return torch.where(y.isnan(), 127, code).to(torch.uint8)
+
+
+def same_codes(a, b):
+    """Equal codes; the sign of a NaN is free."""
+    nan = ((a & 127) == 127) & ((b & 127) == 127)
+    return bool(((a == b) | nan).all())
+
+
+class Pages:
+    """A cache on the CPU: uint8 codes, scales, table and lengths, with the pages in random order."""
+
+    def __init__(self, lens, room, nkv, d, page, seed, scales=(-3, 3), order="hnd"):
+        g = torch.Generator().manual_seed(seed)
+        self.page, self.nkv, self.d, self.lens = page, nkv, d, list(lens)
+        b, cols = len(lens), max(1, -(-max(room) // page))
+        need = [-(-r // page) for r in room]
+        npages = sum(need) + 2
+        ids = torch.randperm(npages, generator=g)
+        self.table = torch.full((b, cols), 10**6, dtype=torch.int32)  # past the need: names no page
+        at = 0
+        for i, n in enumerate(need):
+            self.table[i, :n] = ids[at:at + n]
+            at += n
+        codes = torch.randint(0, 256, (2, npages, nkv, page, d), generator=g).to(torch.uint8)
+        codes[(codes & 127) == 127] -= 1  # (NaN codes are planted where a test wants them)
+        self.k, self.v = codes[0], codes[1]
+        e = torch.randint(scales[0], scales[1] + 1, (2, npages, nkv), generator=g)
+        self.k_scale, self.v_scale = (2.0 ** e[0]).float(), (2.0 ** e[1]).float()
+        self.order = order
+
+    def rows(self, i, n=None):
+        """K, V (nkv, n, d) in 64 bits of sequence i."""
+        n = self.lens[i] if n is None else n
+        out = []
+        for codes, scale in ((self.k, self.k_scale), (self.v, self.v_scale)):
+            ids = self.table[i, : -(-n // self.page)].long()
+            x = VALUES[codes[ids].long()] * scale[ids].double()[..., None, None]
+            out.append(x.transpose(0, 1).reshape(self.nkv, len(ids) * self.page, self.d)[:, :n])
+        return out
+
+    def cuda(self, dtype=E4M3):
+        def pool(c):
+            if self.order == "nhd":  # rows of all heads next to one another
+                return c.transpose(1, 2).contiguous().cuda().transpose(1, 2).view(dtype)
+            return c.cuda().view(dtype)
+        seq = torch.tensor(self.lens, dtype=torch.int32).cuda()
+        return q().QuokaCache(pool(self.k), pool(self.v), self.k_scale.cuda(), self.v_scale.cuda(), self.table.cuda(), seq)
+
+
+def rotate(x, cos, sin, neighbours):
+    """x (h, t, d) fp32 by rows of cos, sin (t, rot / 2): elementary fp32 operations."""
+    r = cos.shape[1]
+    x = x.clone()
+    if r:
+        lo = slice(0, 2 * r, 2) if neighbours else slice(0, r)
+        hi = slice(1, 2 * r, 2) if neighbours else slice(r, 2 * r)
+        a, z = x[..., lo].clone(), x[..., hi].clone()
+        x[..., lo] = a * cos - z * sin
+        x[..., hi] = z * cos + a * sin
+    return x
+
+
+def append(c, K, V, cos, sin, neighbours, new):
+    """Appends to the Pages c in place; returns the rotated keys (b, nkv, BCP, d) fp32."""
+    turned = K.float().clone()
+    for i, m in enumerate(new):
+        n = c.lens[i]
+        if m == 0:
+            continue
+        turned[i, :, :m] = rotate(K[i, :, :m].float(), cos[n:n + m], sin[n:n + m], neighbours)
+        for codes, scales, x in ((c.k, c.k_scale, turned[i, :, :m]), (c.v, c.v_scale, V[i, :, :m].float())):
+            for p in range(n // c.page, (n + m - 1) // c.page + 1):
+                t0, t1, id_ = max(n, p * c.page), min(n + m, (p + 1) * c.page), int(c.table[i, p])
+                for j in range(c.nkv):
+                    y = x[j, t0 - n:t1 - n].double()
+                    top = float(torch.where(y.isfinite(), y.abs(), 0.0).max())
+                    e = -50
+                    while e < 50 and top > 448 * 2.0**e:
+                        e += 1
+                    held = t0 - p * c.page
+                    if held:
+                        old = float(scales[id_, j])
+                        e = max(e, round(torch.tensor(old).log2().item()))
+                        codes[id_, j, :held] = encode(VALUES[codes[id_, j, :held].long()] * (old / 2.0**e))
+                    scales[id_, j] = 2.0**e
+                    codes[id_, j, held:held + t1 - t0] = encode(y * 2.0**-e)
+    return turned
+
+
+def attention(c, Q, Kc, Vc, idx=None, counts=None, scale=None):
+    """O, lse in 64 bits, and what the error bounds are made of: per output
+    sum_k p_k |v_k|, per row the largest sum_i |q_i k_i| * scale, and per output
+    the sum over the cached keys of |v_k| 2^(E - ev_k), 2^ev_k a key's value
+    scale and 2^E the largest."""
+    b, nq, L, d = Q.shape
+    G = nq // c.nkv
+    scale = d**-0.5 if scale is None else scale
+    O, A = torch.zeros(b, nq, L, d, dtype=torch.float64), torch.zeros(b, nq, L, d, dtype=torch.float64)
+    B = torch.zeros_like(A)
+    lse, size = torch.full((b, nq, L), -torch.inf, dtype=torch.float64), torch.zeros(b, nq, L, dtype=torch.float64)
+    for i in range(b):
+        K, V = c.rows(i)
+        at_page = c.table[i, torch.arange(c.lens[i]) // c.page].long()
+        for j in range(c.nkv):
+            k, v, f = K[j], V[j], c.v_scale[at_page, j].double()
+            if idx is not None:
+                at = idx[i, j, : int(counts[i, j])].long()
+                k, v, f = k[at], v[at], f[at]
+            if f.numel():
+                B[i, j * G:(j + 1) * G] = (v.abs() * (f.max() / f)[:, None]).sum(0)
+            n = k.shape[0]
+            if Kc is not None:
+                k, v = torch.cat((k, Kc[i, j].double())), torch.cat((v, Vc[i, j].double()))
+            for h in range(j * G, (j + 1) * G):
+                for t in range(L):
+                    m = n + (t + 1 if Kc is not None else 0)
+                    if m == 0:
+                        continue
+                    x = Q[i, h, t].double()
+                    s = (k[:m] @ x) * scale
+                    lse[i, h, t] = torch.logsumexp(s, 0)
+                    p = torch.exp(s - lse[i, h, t])
+                    O[i, h, t], A[i, h, t] = p @ v[:m], p @ v[:m].abs()
+                    size[i, h, t] = float((k[:m].abs() @ x.abs()).max()) * scale
+    return O, lse, A, size, B
+
+
+def check_attention(O, lse, want, dt, d, n, few):
+    """Bounds on the kernels' roundings:
+    score: d fp32 additions of a tensor-core product, each off by at most
+      2^-22 of the sum of magnitudes (`size`), and the fp32 query as two halves
+      (2^-22): ds = (d + 8) 2^-22 size;
+    weight: 2^x of an fp32 x, |x| <= 64 where it matters (2^-17), the rounding
+      to the operand type (few rows: fp16 2^-11, two halves 2^-21 for fp32
+      inputs; many rows: bf16 2^-8, and once more for a range's bf16 partial;
+      fp32: none), twice the score's error in numerator and denominator; with
+      few rows 2^-32 of the largest w_k = p_k 2^ev_k at least (fp16 subnormals),
+      which is at most 2^E L, L the denominator: 2^-32 B;
+    sums: n keys, each addition off by 2^-22 of the sum of magnitudes;
+    output: half a step of its type."""
+    wO, wl, A, size, B = want
+    ds = (d + 8) * 2.0**-22 * size
+    weight = {True: {"bf16": 2.0**-11, "f32": 2.0**-21}, False: {"bf16": 2 * 2.0**-8, "f32": 0.0}}[few][dt]
+    rel = weight + 2.0**-17 + 2 * ds + (n + 64) * 2.0**-22
+    half = torch.finfo(TYPES[dt]).eps / 2
+    O, lse = O.double().cpu(), lse.double().cpu()
+    bad = (O - wO).abs() - (half * wO.abs() + 2 * rel[..., None] * A + (2.0**-32 * B if few else 0.0))
+    assert O.isfinite().all() and bad.max() <= 0, f"O is {bad.max():.3e} past its bound"
+    there = wl > -torch.inf
+    assert torch.equal(lse > -torch.inf, there)
+    off = (lse - wl)[there].abs() - (rel + 2.0**-22 * wl.abs())[there]
+    assert off.numel() == 0 or off.max() <= 0, f"lse is {off.max():.3e} past its bound"
+
+
+def randn(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed))
+
+
+def angles(npos, rot):
+    a = torch.arange(npos, dtype=torch.float64)[:, None] * 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(1, rot))
+    return a.cos().float(), a.sin().float()
+
+
+def strided(x):
+    """x on the GPU as part of a larger tensor: other strides, the same values."""
+    b, h, t, d = x.shape
+    big = torch.full((b, t + 3, h + 1, d), float("nan"), dtype=x.dtype, device="cuda")
+    view = big.transpose(1, 2)[:, :h, :t]
+    view.copy_(x)
+    return view
+
+
+# ------------------------------------------------------------ append
+
+APPENDS = [
+    # lens, new (None: BCP each), BCP, nkv, nq, d, page, rot, neighbours, dtype, order of the pool
+    ([0], None, 1, 1, 1, 64, 16, 64, False, "bf16", "hnd"),
+    ([5, 63, 64, 127], None, 1, 2, 4, 128, 64, 128, False, "bf16", "hnd"),
+    ([0, 15, 16, 30], [7, 0, 40, 39], 40, 3, 6, 64, 16, 32, True, "f32", "nhd"),
+    ([100], None, 300, 2, 10, 128, 128, 64, False, "f32", "hnd"),
+    ([31, 1], [200, 33], 200, 1, 8, 128, 32, 128, True, "bf16", "nhd"),
+    ([17, 90], None, 129, 2, 2, 64, 128, 0, False, "bf16", "hnd"),
+]
+
+
+@gpu
+@pytest.mark.parametrize("k", range(len(APPENDS)))
+def test_append(k):
+    """Codes, scales and the rotated copies, bit for bit; every byte of the
+    pool that no new token concerns stays as it was."""
+    lens, new, BCP, nkv, nq, d, page, rot, nb, dt, order = APPENDS[k]
+    b, t = len(lens), TYPES[dt]
+    c = Pages(lens, [n + BCP for n in lens], nkv, d, page, 10 + k, order=order)
+    K, V, Q = randn(20 + k, b, nkv, BCP, d), randn(30 + k, b, nkv, BCP, d), randn(40 + k, b, nq, BCP, d)
+    K *= torch.logspace(-3, 3, BCP)[:, None]  # pages whose scale has to grow, and ones where it need not
+    V[:, :, ::5] = 0
+    V[0, 0, 0, :3] = torch.tensor([float("inf"), -float("inf"), 1e30])
+    K[0, 0, 0, 1] = float("inf") if rot == 0 else 3.0
+    K, V, Q = K.to(t), V.to(t), Q.to(t)
+    cos, sin = angles(max(lens) + BCP, rot)
+    dev = c.cuda()
+    nl = None if new is None else torch.tensor(new, dtype=torch.int32).cuda()
+    Kr0, Qr0 = randn(1, *K.shape).to(t), randn(2, *Q.shape).to(t)
+    Kr, Qr = Kr0.cuda(), Qr0.cuda()
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    got = q().quoka_cache_append(dev, strided(K), strided(V), strided(Q), *((cos.cuda(), sin.cuda()) if rot else (None, None)),
+                                 interleaved=nb, new_len=nl, Kr=Kr, Qr=Qr, ws=ws)
+    assert q().quoka_get_device_status(ws) == 0
+    assert got[0] is Kr and got[1] is Qr
+    news = [BCP] * b if new is None else new
+    c2 = Pages(lens, [n + BCP for n in lens], nkv, d, page, 10 + k)
+    turned = append(c2, K, V, cos, sin, nb, news)
+    assert same_codes(dev.k.view(torch.uint8).cpu(), c2.k) and same_codes(dev.v.view(torch.uint8).cpu(), c2.v)
+    assert torch.equal(dev.k_scale.cpu(), c2.k_scale) and torch.equal(dev.v_scale.cpu(), c2.v_scale)
+    for i, m in enumerate(news):
+        Kr0[i, :, :m] = turned[i, :, :m].to(t)
+        Qr0[i, :, :m] = rotate(Q[i, :, :m].float(), cos[lens[i]:lens[i] + m], sin[lens[i]:lens[i] + m], nb).to(t)
+    assert torch.equal(Kr.cpu().double(), Kr0.double()) and torch.equal(Qr.cpu().double(), Qr0.double())
+
+
+@gpu
+def test_append_special_values():
+    """NaN stays NaN, infinities saturate, neither moves the scale; values
+    beyond the scales' range saturate or vanish; codes with NaN are moved."""
+    c = Pages([3], [64], 1, 64, 16, 5)
+    c.k[c.table[0, 0].long(), 0, 1, 2] = 127
+    K = torch.zeros(1, 1, 40, 64)
+    K[0, 0, 0, 0], K[0, 0, 0, 1], K[0, 0, 1, 5] = float("nan"), -float("inf"), 1e4
+    K[0, 0, 20] = 1e-30
+    K[0, 0, 35, 3] = 3e38
+    V = randn(3, 1, 1, 40, 64)
+    dev = c.cuda(torch.uint8)
+    q().quoka_cache_append(dev, K.cuda(), V.cuda())
+    cos, sin = angles(64, 0)
+    append(c, K, V, cos, sin, False, [40])
+    assert same_codes(dev.k.cpu(), c.k) and same_codes(dev.v.cpu(), c.v)
+    assert torch.equal(dev.k_scale.cpu(), c.k_scale) and torch.equal(dev.v_scale.cpu(), c.v_scale)
+
+
+@gpu
+def test_append_leaves_out_what_does_not_fit():
+    """Positions past the table or the angles, bad counts and pages outside
+    the cache are latched and left out; the rest is written."""
+    c = Pages([60, 4, 10], [64, 40, 40], 1, 64, 16, 6)
+    c.table[2, 1] = -5  # sequence 2's second page: tokens 16 .. 31
+    K, V = randn(1, 3, 1, 20, 64), randn(2, 3, 1, 20, 64)
+    dev = c.cuda(torch.uint8)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    q().quoka_cache_append(dev, K.cuda(), V.cuda(), new_len=torch.tensor([20, 20, 20], dtype=torch.int32).cuda(), ws=ws)
+    assert q().quoka_get_device_status(ws) == 6
+    cos, sin = angles(100, 0)
+    lens = c.lens
+    append(c, K, V, cos, sin, False, [4, 20, 6])
+    assert same_codes(dev.k.cpu(), c.k) and torch.equal(dev.v_scale.cpu(), c.v_scale)
+    # angles for 10 positions only: sequence 1 (4 held) takes 6 of its tokens, the others none
+    c = Pages(lens, [64, 40, 40], 1, 64, 16, 6)
+    dev = c.cuda(torch.uint8)
+    cos, sin = angles(10, 64)
+    q().quoka_cache_append(dev, K.cuda(), V.cuda(), None, cos.cuda(), sin.cuda(), ws=ws)
+    assert q().quoka_get_device_status(ws) == 6
+    append(c, K, V, cos, sin, False, [0, 6, 0])
+    assert same_codes(dev.k.cpu(), c.k) and torch.equal(dev.k_scale.cpu(), c.k_scale)
+    # a count outside [0, BCP], and a negative length
+    c = Pages([4, 4, 4], [40, 40, 40], 1, 64, 16, 7)
+    dev = c.cuda(torch.uint8)
+    dev.seq_len[2] = -1
+    q().quoka_cache_append(dev, K.cuda(), V.cuda(), new_len=torch.tensor([-3, 99, 5], dtype=torch.int32).cuda(), ws=ws)
+    assert q().quoka_get_device_status(ws) == 6
+    append(c, K, V, cos[:, :0], sin[:, :0], False, [0, 20, 0])
+    assert same_codes(dev.k.cpu(), c.k) and same_codes(dev.v.cpu(), c.v)
+
+
+# ------------------------------------------------------------ gather
+
+GATHERS = [
+    # lens, max_len, nkv, d, page, N (0: all rows), dtype, order
+    ([1], 1, 1, 64, 16, 0, "bf16", "hnd"),
+    ([77, 0, 200], 200, 2, 128, 64, 0, "f32", "nhd"),
+    ([130, 129], 140, 3, 64, 128, 50, "bf16", "nhd"),
+    ([1000, 3], 1000, 2, 128, 32, 333, "f32", "hnd"),
+]
+
+
+@gpu
+@pytest.mark.parametrize("k", range(len(GATHERS)))
+def test_gather(k):
+    lens, max_len, nkv, d, page, N, dt, order = GATHERS[k]
+    b = len(lens)
+    c = Pages(lens, lens, nkv, d, page, 50 + k, scales=(-50, 50), order=order)
+    c.k[c.table[0, 0].long(), 0, 0, 0] = 127
+    idx = counts = None
+    if N:
+        g = torch.Generator().manual_seed(k)
+        counts = torch.tensor([[min(n, N) if j == 0 else min(n, N) // 2 for j in range(nkv)] for n in lens], dtype=torch.int32)
+        idx = torch.full((b, nkv, N), 2**31 - 1, dtype=torch.int32)
+        for i, n in enumerate(lens):
+            for j in range(nkv):
+                m = int(counts[i, j])
+                idx[i, j, :m] = torch.randint(0, n, (m,), generator=g)  # any order, repeats among them
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    K, V = q().quoka_cache_gather(c.cuda(), max_len, None if idx is None else idx.cuda(), None if idx is None else counts.cuda(),
+                                  dtype=TYPES[dt], ws=ws)
+    assert q().quoka_get_device_status(ws) == 0
+    assert K.shape == (b, nkv, N or max_len, d) and K.dtype == TYPES[dt]
+    for i, n in enumerate(lens):
+        want = c.rows(i)
+        for got, w in ((K[i], want[0]), (V[i], want[1])):
+            for j in range(nkv):
+                rows = w[j] if idx is None else w[j][idx[i, j, : int(counts[i, j])].long()]
+                full = torch.zeros(N or max_len, d, dtype=torch.float64)
+                full[: rows.shape[0]] = rows
+                assert torch.equal(got[j].double().cpu().nan_to_num(12345.0), full.nan_to_num(12345.0))
+
+
+# ------------------------------------------------------------ select
+
+SELECTS = [
+    # lens, max_len, nkv, nq, d, page, BCP, NQ, BSA, dtype, order
+    ([1], 1, 1, 1, 64, 16, 1, 1, 1, "bf16", "hnd"),
+    ([300, 0, 47, 129], 333, 2, 6, 128, 64, 20, 3, 50, "bf16", "nhd"),
+    ([999], 1000, 3, 3, 64, 16, 70, 70, 1000, "f32", "hnd"),
+    ([2500, 1], 5001, 2, 16, 128, 32, 64, 17, 600, "f32", "hnd"),
+    ([6000, 5999], 6000, 2, 8, 128, 128, 1, 1, 512, "bf16", "hnd"),
+    ([20000], 20000, 1, 4, 64, 64, 33, 8, 4000, "bf16", "hnd"),
+]
+
+
+def select_oracle(c, Q, q_idx):
+    """S_agg (b, nkv, L) in 64 bits for the chosen positions q_idx, by the definition."""
+    b, nq, _, d = Q.shape
+    unit = Q.double() / Q.double().norm(dim=-1, keepdim=True)
+    picked = unit.gather(2, q_idx.long()[..., None].expand(-1, -1, -1, d))
+    group = picked.view(b, c.nkv, nq // c.nkv, -1, d).mean(2)
+    out = []
+    for i in range(b):
+        K = c.rows(i)[0]
+        n = K.norm(dim=-1, keepdim=True)
+        K = torch.where(n > 0, K / n.clamp(min=1e-300), 0.0)
+        out.append((K @ group[i].transpose(1, 2)).amax(-1))
+    return out
+
+
+@gpu
+@pytest.mark.parametrize("k", range(len(SELECTS)))
+def test_select(k):
+    """The scores' bound: the group mean of unit queries (d additions and a
+    square root, (d + 8) 2^-24), its two halves (2^-22), d additions of the
+    product and d of |k|^2 (each 2^-22 of magnitudes that Cauchy bounds by 1):
+    (2 d + 16) 2^-22. Keys may swap across the last place within twice that."""
+    lens, max_len, nkv, nq, d, page, BCP, NQ, BSA, dt, order = SELECTS[k]
+    b, n = len(lens), min(BSA, max_len)
+    c = Pages(lens, [max_len] + lens[1:], nkv, d, page, 60 + k, scales=(-50, 50), order=order)
+    c.k[c.table[0, 0].long(), 0, 0] = 0  # a key of zeros: scores 0
+    Q = (randn(70 + k, b, nq, BCP, d) + 1.0).to(TYPES[dt])
+    kv_idx = torch.full((b, nkv, n), -7, dtype=torch.int32, device="cuda")
+    s_agg = torch.full((b, nkv, max_len), 5.0, device="cuda")
+    size = q().quoka_select_workspace_size(b, nq, nkv, d, max_len, BCP, NQ, BSA, TYPES[dt])
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    idx, count, q_idx, s = q().quoka_cache_select(strided(Q), c.cuda(), max_len, NQ, BSA, kv_idx=kv_idx, s_agg=s_agg,
+                                                  want_q_idx=True, ws=ws)
+    assert q().quoka_get_device_status(ws) == 0
+    # the chosen queries: rank order of -cos(Q, mean), near-ties may swap
+    mean = Q.double().mean(2, keepdim=True)
+    SQ = -torch.nn.functional.cosine_similarity(Q.double(), mean, dim=-1, eps=1e-300)
+    want_q = SQ.sort(dim=-1, descending=True, stable=True).indices[..., :NQ]
+    P.check_q_idx(q_idx.cpu().numpy(), SQ.numpy(), want_q.numpy())
+    want = select_oracle(c, Q, q_idx.cpu())
+    tol = (2 * d + 16) * 2.0**-22
+    for i, L in enumerate(lens):
+        m = min(n, L)
+        got = s[i].double().cpu()
+        assert (got[:, :L] - want[i]).abs().max() <= tol if L else True
+        assert (got[:, L:] == 5.0).all() and (idx[i, :, m:] == -7).all() and (count[i] == m).all()
+        for j in range(nkv):
+            # the picks are exactly the best of the scores returned, ties to the lower index ...
+            best = got[j, :L].sort(descending=True, stable=True).indices[:m].sort().values
+            assert torch.equal(idx[i, j, :m].cpu().long(), best)
+            # ... and of the true ones up to their bound
+            if m:
+                last = want[i][j].sort(descending=True).values[m - 1]
+                assert (want[i][j][best] >= last - 2 * tol).all()
+
+
+@gpu
+def test_select_ties_go_to_the_lower_index():
+    c = Pages([400], [400], 1, 128, 32, 3)
+    for t in range(400):  # ten kinds of keys, in scales that do not matter
+        p, r = divmod(t, 32)
+        c.k[int(c.table[0, p]), 0, r] = c.k[int(c.table[0, 0]), 0, t % 10]
+    Q = randn(4, 1, 4, 8, 128).to(torch.bfloat16)
+    idx, count, _, s = q().quoka_cache_select(Q.cuda(), c.cuda(), 400, 2, 100, want_s_agg=True)
+    s = s[0, 0].cpu()
+    assert torch.equal(s[:10].repeat(40), s)
+    assert torch.equal(idx[0, 0].cpu().long(), s.sort(descending=True, stable=True).indices[:100].sort().values)
+
+
+# ------------------------------------------------------------ attention
+
+ATTNS = [
+    # lens, max_len, nkv, nq, d, page, BCP, N (0: all keys), chunk keys, dtype, order
+    ([1], 1, 1, 1, 64, 16, 1, 0, False, "bf16", "hnd"),
+    ([0, 300, 17, 64], 300, 2, 8, 128, 64, 1, 0, True, "bf16", "nhd"),
+    ([0, 299, 16], 300, 2, 6, 64, 16, 1, 0, False, "f32", "hnd"),
+    ([700, 9], 700, 1, 7, 128, 32, 5, 0, True, "f32", "hnd"),
+    ([900], 1000, 2, 16, 128, 128, 8, 333, True, "bf16", "nhd"),
+    ([500, 40], 500, 3, 6, 64, 64, 3, 100, False, "f32", "hnd"),
+    ([0, 260], 260, 1, 5, 128, 16, 13, 0, True, "bf16", "hnd"),      # 65 rows: the dense path
+    ([300, 0], 310, 2, 4, 128, 64, 130, 200, True, "bf16", "hnd"),
+    ([150], 150, 1, 3, 64, 16, 70, 0, True, "bf16", "nhd"),
+    ([90, 200], 200, 1, 8, 64, 32, 16, 77, False, "f32", "hnd"),
+    ([0], 0, 1, 2, 128, 16, 40, 0, True, "bf16", "hnd"),             # no cached key at all
+    ([0], 0, 1, 2, 64, 16, 2, 0, True, "f32", "hnd"),
+]
+
+
+def index_lists(lens, nkv, N, seed):
+    g = torch.Generator().manual_seed(seed)
+    counts = torch.tensor([[min(n, N) if j == 0 else min(n, N) // 3 for j in range(nkv)] for n in lens], dtype=torch.int32)
+    idx = torch.full((len(lens), nkv, N), 2**31 - 1, dtype=torch.int32)
+    for i, n in enumerate(lens):
+        for j in range(nkv):
+            m = int(counts[i, j])
+            idx[i, j, :m] = torch.randperm(max(1, n), generator=g)[:m].sort().values
+    return idx, counts
+
+
+@gpu
+@pytest.mark.parametrize("k", range(len(ATTNS)))
+def test_attention(k):
+    lens, max_len, nkv, nq, d, page, BCP, N, chunk, dt, order = ATTNS[k]
+    b, t = len(lens), TYPES[dt]
+    c = Pages(lens, lens, nkv, d, page, 80 + k, scales=(-9, -5), order=order)
+    # what lies behind a sequence's end in its last page must not matter
+    for i, n in enumerate(lens):
+        if n % page:
+            p = int(c.table[i, n // page])
+            c.k[p, :, n % page:] = 127
+            c.v[p, :, n % page:] = 127
+    idx = counts = None
+    if N:
+        idx, counts = index_lists(lens, nkv, N, k)
+    Q = (2 * randn(90 + k, b, nq, BCP, d)).to(t)
+    Kc, Vc = (randn(s + k, b, nkv, BCP, d).to(t) for s in (100, 110)) if chunk else (None, None)
+    size = q().quoka_cache_attn_workspace_size(b, nq, nkv, d, BCP, N or max_len, t)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    up = lambda x: None if x is None else x.cuda()
+    O, lse = q().quoka_cache_attn(strided(Q), c.cuda(), max_len, up(idx), up(counts), None if Kc is None else strided(Kc),
+                                  None if Vc is None else strided(Vc), want_lse=True, ws=ws)
+    assert q().quoka_get_device_status(ws) == 0
+    check_attention(O, lse, attention(c, Q, Kc, Vc, idx, counts), dt, d, (N or max_len) + BCP, nq // nkv * BCP <= 64)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_attention_far_scales_and_scores(dt):
+    """Pages whose scales lie far apart: the largest scores in pages of tiny
+    values and the largest values under tiny scores, in ascending order of
+    both, so that the running maximum moves all the time; a large softmax
+    scale leaves one key."""
+    c = Pages([640], [640], 1, 64, 16, 9, scales=(-9, -7))
+    for p in range(40):
+        id_ = int(c.table[0, p])
+        c.v_scale[id_, 0] = 2.0 ** (50 - (p * 5) % 101)
+        c.k_scale[id_, 0] = 2.0 ** (-12 + p // 8)
+    Q = randn(1, 1, 3, 1, 64).to(TYPES[dt])
+    for scale in (0.05, 0.4):
+        O, lse = q().quoka_cache_attn(Q.cuda(), c.cuda(), 640, scale=scale, want_lse=True)
+        want = attention(c, Q, None, None, scale=scale)
+        check_attention(O, lse, want, dt, 64, 640, True)
+
+
+@gpu
+def test_attention_nan_reaches_its_rows_only():
+    """A NaN or an infinity among the inputs makes NaN of the rows that see
+    it and of no others."""
+    c = Pages([100, 100], [100, 100], 2, 64, 16, 4, scales=(-8, -6))
+    c.k[int(c.table[0, 3]), 1, 2, 7] = 127
+    Q = randn(1, 2, 4, 1, 64)
+    Q[1, 0, 0, 5] = float("inf")
+    O, _ = q().quoka_cache_attn(Q.cuda(), c.cuda(), 100)
+    nan = O.isnan().all(-1)[..., 0].cpu()
+    assert torch.equal(nan, torch.tensor([[False, False, True, True], [True, False, False, False]]))
+    assert torch.equal(O.isnan().any(-1)[..., 0].cpu(), nan)
+
+
+# ------------------------------------------------------------ device faults
+
+@gpu
+def test_reads_latch_what_is_out_of_range():
+    """A bad page reads as zeros, a bad index as a zero row, a length beyond
+    max_len as max_len; each is latched, and the next good call clears it."""
+    c = Pages([100], [100], 1, 64, 16, 8, scales=(-8, -6))
+    Q, good = randn(1, 1, 2, 1, 64), c.cuda()
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    status = lambda: q().quoka_get_device_status(ws)
+
+    def calls(cache, max_len=100, idx=None):
+        cnt = None if idx is None else torch.tensor([[idx.shape[2]]], dtype=torch.int32).cuda()
+        K, _ = q().quoka_cache_gather(cache, max_len, idx, cnt, dtype=torch.float32, ws=ws)
+        seen = [status()]
+        O, _ = q().quoka_cache_attn(Q.cuda(), cache, max_len, idx, cnt, ws=ws)
+        seen.append(status())
+        if idx is None:
+            q().quoka_cache_select(Q.cuda(), cache, max_len, 1, 5, ws=ws)
+            seen.append(status())
+        return seen, K, O
+
+    table = c.table.clone()
+    c.table[0, 2] = 10**6
+    seen, K, O = calls(c.cuda())
+    assert seen == [6, 6, 6] and (K[0, 0, 32:48] == 0).all() and K[0, 0, :32].abs().sum() > 0 and O.isfinite().all()
+    c.table = table
+    assert calls(good)[0] == [0, 0, 0]
+    seen, K, O = calls(good, max_len=50)
+    assert seen == [6, 6, 6] and torch.equal(K, calls(good)[1][:, :, :50])
+    seen, K, O = calls(good, idx=torch.tensor([[[3, -1, 100, 99]]], dtype=torch.int32).cuda())
+    assert seen == [6, 6] and (K[0, 0, 1:3] == 0).all() and O.isfinite().all()
+    c.k_scale[c.table[0, 1].long()] = 0.3  # not a power of two
+    assert calls(c.cuda())[0][:2] == [6, 6]
+
+
+# ------------------------------------------------------------ the calls together
+
+@gpu
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f32", 64)])
+def test_serving_loop(dt, d):
+    """Two ragged prompts taken in by chunks and continued token by token:
+    append with rotation, select, attend over the selection and the chunk,
+    advance. The cache of every step is the plain one bit for bit; the
+    attention is checked on the selection made."""
+    t, nkv, nq, page, NQ, BSA = TYPES[dt], 2, 6, 16, 4, 24
+    c = Pages([0, 0], [160, 160], nkv, d, page, 11)
+    dev, room = c.cuda(torch.uint8), 160
+    cos, sin = angles(room, d)
+    steps = [(40, [40, 33]), (40, [40, 1]), (40, [20, 0])] + [(1, [1, 1])] * 4 + [(5, [5, 3])]
+    for k, (BCP, new) in enumerate(steps):
+        K, V, Q = (randn(200 + 3 * k + u, 2, h, BCP, d).to(t) for u, h in enumerate((nkv, nkv, nq)))
+        nl = torch.tensor(new, dtype=torch.int32).cuda()
+        Kr, Qr = q().quoka_cache_append(dev, K.cuda(), V.cuda(), Q.cuda(), cos.cuda(), sin.cuda(), new_len=nl, want_Kr=True)
+        max_len = max(1, max(c.lens))
+        idx, cnt, _, _ = q().quoka_cache_select(Qr, dev, max_len, min(NQ, BCP), BSA)
+        O, lse = q().quoka_cache_attn(Qr, dev, max_len, idx, cnt, Kr, V.cuda(), want_lse=True)
+        want = attention(c, Qr.cpu(), Kr.cpu(), V, idx.cpu(), cnt.cpu())
+        for i, m in enumerate(new):  # rows of padded tokens are nobody's
+            check_attention(O[i:i + 1, :, :m], lse[i:i + 1, :, :m], [w[i:i + 1, :, :m] for w in want], dt, d,
+                            idx.shape[2] + BCP, nq // nkv * BCP <= 64) if m else None
+        append(c, K, V, cos, sin, False, new)
+        assert same_codes(dev.k.cpu(), c.k) and same_codes(dev.v.cpu(), c.v)
+        assert torch.equal(dev.k_scale.cpu(), c.k_scale) and torch.equal(dev.v_scale.cpu(), c.v_scale)
+        dev.seq_len += nl
+        c.lens = [n + m for n, m in zip(c.lens, new)]
+
+
+@gpu
+def test_decode_step_replays_from_a_cuda_graph():
+    """A captured decode step follows the lengths, tables and inputs it finds
+    at each replay, on another stream too; two captured graphs with workspaces
+    of their own do not disturb one another."""
+    m, t = q(), torch.bfloat16
+    c = Pages([30, 50], [128, 128], 2, 128, 16, 12)
+    dev = c.cuda(torch.uint8)
+    cos, sin = (x.cuda() for x in angles(128, 128))
+    K, V = (torch.zeros(2, 2, 1, 128, dtype=t, device="cuda") for _ in range(2))
+    Q = torch.zeros(2, 8, 1, 128, dtype=t, device="cuda")
+
+    def step():
+        Kr, Qr = m.quoka_cache_append(dev, K, V, Q, cos, sin, want_Kr=True)
+        idx, cnt, _, _ = m.quoka_cache_select(Qr, dev, 128, 1, 20)
+        O, lse = m.quoka_cache_attn(Qr, dev, 128, idx, cnt, Kr, V, want_lse=True)
+        full, _ = m.quoka_cache_attn(Qr, dev, 128, None, None, Kr, V)
+        return Kr, Qr, cnt, O, lse, full
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    state = [x.clone() for x in (dev.k, dev.v, dev.k_scale, dev.v_scale)]
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step())
+        graphs.append(g)
+    for k in range(3):
+        for x, u in ((K, 0), (V, 1), (Q, 2)):
+            x.copy_(randn(300 + 3 * k + u, *x.shape).to(t))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for g in graphs:  # the same step twice: append writes the same tokens again
+                g.replay()
+        side.synchronize()
+        got = [x.clone() for x in outs[0]]
+        assert all(torch.equal(x, y) for x, y in zip(got, outs[1]))
+        for x, y in zip((dev.k, dev.v, dev.k_scale, dev.v_scale), state):
+            x.copy_(y)
+        assert all(torch.equal(x, y) for x, y in zip(got, step()))
+        state = [x.clone() for x in (dev.k, dev.v, dev.k_scale, dev.v_scale)]
+        dev.seq_len += 1
+
+
+@gpu
+def test_calls_on_a_given_stream_and_repeatable():
+    """The stream argument, and the same bits on every run."""
+    m = q()
+    c = Pages([3000, 2500], [3000, 3000], 2, 128, 64, 13, scales=(-9, -5))
+    dev = c.cuda()
+    Q = randn(5, 2, 8, 1, 128).to(torch.bfloat16).cuda()
+    torch.cuda.synchronize()
+    want = None
+    for k in range(4):
+        s = torch.cuda.Stream() if k % 2 else None
+        idx, cnt, _, _ = m.quoka_cache_select(Q, dev, 3000, 1, 300, stream=s)
+        O, lse = m.quoka_cache_attn(Q, dev, 3000, idx, cnt, want_lse=True, stream=s)
+        A, _ = m.quoka_cache_attn(Q, dev, 3000, stream=s)
+        torch.cuda.synchronize()
+        got = [x.clone() for x in (idx, cnt, O, lse, A)]
+        want = want or got
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@gpu
+def test_long_table_offsets_pass_32_bits():
+    """A pool of more than 2^32 bytes, with the pages of a sequence at both ends."""
+    page, nkv, d = 128, 8, 128
+    npages = (2**32 + 2**28) // (page * nkv * d)
+    k = torch.zeros(npages, nkv, page, d, dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    scale = torch.ones(npages, nkv, device="cuda")
+    table = torch.tensor([[npages - 1, 0, npages - 2]], dtype=torch.int32, device="cuda")
+    seq = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c = q().QuokaCache(k, v, scale, scale.clone(), table, seq)
+    K, V = (randn(s, 1, nkv, 300, d).to(torch.bfloat16).cuda() for s in (1, 2))
+    q().quoka_cache_append(c, K, V)
+    seq.fill_(300)
+    Kg, Vg = q().quoka_cache_gather(c, 300)
+    for x, y in ((Kg, K), (Vg, V)):  # e4m3: half a step is 2^-4; below 2^-6 of the scale, half of 2^-9 of it
+        assert ((x.double() - y.double()).abs() <= 2.0**-4 * y.double().abs() + 2.0**-10 * 2.0**-5).all()
+    Q = randn(3, 1, 8, 1, d).to(torch.bfloat16).cuda()
+    O, _ = q().quoka_cache_attn(Q, c, 300)
+    cnt = torch.full((1, nkv), 300, dtype=torch.int32, device="cuda")
+    idx = torch.arange(300, dtype=torch.int32, device="cuda").expand(1, nkv, 300).contiguous()
+    O2, _ = q().quoka_cache_attn(Q, c, 300, idx, cnt)
+    assert torch.equal(O, O2) and O.abs().sum() > 0
+
+
+# ------------------------------------------------------------ host side
+
+def cpu_cache(**kw):
+    a = dict(k=torch.zeros(5, 2, 16, 64, dtype=torch.uint8), v=torch.zeros(5, 2, 16, 64, dtype=torch.uint8),
+             k_scale=torch.ones(5, 2), v_scale=torch.ones(5, 2), page_table=torch.zeros(3, 4, dtype=torch.int32),
+             seq_len=torch.zeros(3, dtype=torch.int32))
+    a.update(kw)
+    return q().QuokaCache(**a)
+
+
+def test_cache_refuses_bad_tensors():
+    cpu_cache()
+    cpu_cache(k=torch.zeros(5, 16, 2, 64, dtype=torch.uint8).transpose(1, 2),
+              v=torch.zeros(5, 16, 2, 64, dtype=torch.uint8).transpose(1, 2))
+    for kw in ({"k": torch.zeros(5, 2, 16, 96, dtype=torch.uint8), "v": torch.zeros(5, 2, 16, 96, dtype=torch.uint8)},
+               {"k": torch.zeros(5, 2, 24, 64, dtype=torch.uint8), "v": torch.zeros(5, 2, 24, 64, dtype=torch.uint8)},
+               {"v": torch.zeros(5, 2, 32, 64, dtype=torch.uint8)}, {"k_scale": torch.ones(5, 3)},
+               {"v": torch.zeros(5, 16, 2, 64, dtype=torch.uint8).transpose(1, 2)},
+               {"v_scale": torch.ones(2, 5).t()}, {"page_table": torch.zeros(4, dtype=torch.int32)},
+               {"page_table": torch.zeros(4, 3, dtype=torch.int32).t()}, {"seq_len": torch.zeros(2, dtype=torch.int32)}):
+        with pytest.raises(ValueError):
+            cpu_cache(**kw)
+    for kw in ({"v": torch.zeros(5, 2, 16, 64)}, {"k_scale": torch.ones(5, 2, dtype=torch.float64)},
+               {"seq_len": torch.zeros(3, dtype=torch.int64)}):
+        with pytest.raises(TypeError):
+            cpu_cache(**kw)
+
+
+def test_calls_refuse_bad_tensors(lib):  # noqa: F811
+    m, c = q(), cpu_cache()
+    K, Q = torch.zeros(3, 2, 7, 64), torch.zeros(3, 4, 7, 64)
+    i32 = torch.int32
+    for call in (lambda: m.quoka_cache_append(c, K, K),  # a cache on the CPU
+                 lambda: m.quoka_cache_append(c, K, K[:, :, :6]),
+                 lambda: m.quoka_cache_append(c, K, K, torch.zeros(3, 4, 6, 64)),
+                 lambda: m.quoka_cache_append(c, K, K, Qr=Q),
+                 lambda: m.quoka_cache_append(c, K, K, Q, torch.zeros(9, 32)),
+                 lambda: m.quoka_cache_append(c, K, K, Kr=torch.zeros(3, 2, 8, 64)),
+                 lambda: m.quoka_cache_append(c, K, K, new_len=torch.zeros(2, dtype=i32)),
+                 lambda: m.quoka_cache_select(torch.zeros(2, 4, 7, 64), c, 10, 1, 1),
+                 lambda: m.quoka_cache_select(Q, c, 10, 1, 5, kv_idx=torch.zeros(3, 2, 6, dtype=i32)),
+                 lambda: m.quoka_cache_gather(c, 10, torch.zeros(3, 2, 6, dtype=i32)),
+                 lambda: m.quoka_cache_gather(c, 10, torch.zeros(3, 2, 6, dtype=i32), torch.zeros(3, 3, dtype=i32)),
+                 lambda: m.quoka_cache_attn(torch.zeros(3, 4, 7, 128), c, 10),
+                 lambda: m.quoka_cache_attn(Q, c, 10, Kc=K),
+                 lambda: m.quoka_cache_attn(Q, c, 10, None, None, K, K, O=torch.zeros(3, 4, 7, 64).transpose(1, 2))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: m.quoka_cache_append(c, K, K, new_len=torch.zeros(3)),
+                 lambda: m.quoka_cache_append(c, K.half(), K.half()),
+                 lambda: m.quoka_cache_gather(c, 10, dtype=torch.float16),
+                 lambda: m.quoka_cache_attn(Q, c, 10, lse=torch.zeros(3, 4, 7, dtype=torch.float64))):
+        with pytest.raises(TypeError):
+            call()
+
+
+def _cache(**kw):
+    from sparse_kv_selection_quoka_b200._lib import quoka_cache
+    a = dict(k=0x10000, v=0x20000, k_scale=0x30000, v_scale=0x30100, npages=9, nkv=2, page=16, d=128,
+             page_stride=2 * 16 * 128, head_stride=16 * 128, row_stride=128, page_table=0x40000, table_stride=8, b=1,
+             max_pages=8, seq_len=0x50000)
+    a.update(kw)
+    return quoka_cache(**a)
+
+
+def test_entry_points_reject_bad_arguments_on_host(lib):  # noqa: F811
+    """Every refusal comes before anything is enqueued (no GPU here)."""
+    B = ctypes.byref
+    ws, buf, out = (ctypes.c_void_p(x) for x in (0x100000, 0x200000, 0x300000))
+    Q, K = _view((1, 4, 7, 128)), _view((1, 2, 7, 128), data=0x60000)
+    big = 1 << 30
+
+    def select(c=_cache(), Q=Q, max_len=100, NQ=2, BSA=10, count=buf, ws=ws, n=big):
+        return lib.quoka_cache_select(B(Q), B(c), max_len, NQ, BSA, buf, count, None, None, ws, n, None)
+
+    def attn(c=_cache(), Q=Q, max_len=100, idx=None, count=None, N=100, Kc=K, Vc=K, scale=0.1, O=out, ws=ws, n=big):
+        return lib.quoka_cache_attn(B(Q), B(c), max_len, idx, count, N, Kc and B(Kc), Vc and B(Vc), scale, O, None, ws, n,
+                                    None)
+
+    def gather(c=_cache(), max_len=100, idx=None, count=None, N=100, dtype=1, K=out, V=out, ws=None, n=0):
+        return lib.quoka_cache_gather(B(c), max_len, idx, count, N, dtype, K, V, ws, n, None)
+
+    def app(c=_cache(), K=K, V=K, Q=None, cos=None, sin=None, npos=0, rot=0, flags=0, Kr=None, Qr=None, ws=None, n=0):
+        return lib.quoka_cache_append(B(c), K and B(K), V and B(V), Q and B(Q), cos, sin, npos, rot, flags, None, Kr, Qr, ws,
+                                      n, None)
+
+    for f in (select, attn, gather, app):
+        for kw in (dict(k=None), dict(v=0x20008), dict(k_scale=None), dict(npages=0), dict(b=0), dict(max_pages=0),
+                   dict(table_stride=7), dict(row_stride=64), dict(row_stride=136), dict(head_stride=-2048),
+                   dict(page_stride=0), dict(seq_len=None), dict(page_table=None)):
+            assert f(_cache(**kw)) == 1, kw
+        assert f(_cache(page=24)) == 2 and f(_cache(d=96)) == 2
+    for f in (select, attn, gather):
+        assert f(max_len=-1) == 1 and f(max_len=129) == 1  # 8 pages of 16 tokens
+    assert select(NQ=0) == 1 and select(NQ=8) == 1 and select(BSA=-1) == 1 and select(count=None) == 1
+    assert select(Q=_view((1, 3, 7, 128))) == 1 and select(Q=_view((2, 4, 7, 128))) == 1
+    assert select(ws=None) == 3 and select(n=256) == 3 and select(ws=ctypes.c_void_p(0x100010)) == 3
+    assert attn(Kc=None) == 1 and attn(scale=0.0) == 1 and attn(scale=float("nan")) == 1 and attn(O=None) == 1
+    assert attn(N=99) == 1 and attn(idx=buf) == 1 and attn(idx=buf, count=buf, N=-1) == 1
+    assert attn(Kc=_view((1, 2, 8, 128))) == 1 and attn(Q=_view((1, 4, 7, 128), dtype=0)) == 1
+    need = lib.quoka_cache_attn_workspace_size(1, 4, 2, 128, 7, 100, 1)
+    assert need > 256 and attn(n=need - 1) == 3
+    assert lib.quoka_cache_attn_workspace_size(1, 4, 3, 128, 7, 100, 1) == 0
+    assert lib.quoka_cache_attn_workspace_size(1, 4, 2, 96, 7, 100, 1) == 0
+    assert gather(N=99) == 1 and gather(dtype=2) == 1 and gather(K=None) == 1 and gather(count=buf) == 1
+    assert gather(ws=ctypes.c_void_p(0x100010), n=256) == 3
+    assert app(K=None) == 1 and app(V=_view((1, 2, 8, 128))) == 1 and app(Q=Q) == 1 and app(Qr=out) == 1 and app(flags=2) == 1
+    assert app(rot=8, cos=buf, sin=buf, npos=9) == 1 and app(rot=144, cos=buf, sin=buf, npos=9) == 1
+    assert app(rot=16, cos=buf, sin=None, npos=9) == 1 and app(rot=16, cos=buf, sin=buf, npos=0) == 1
+    # outputs over inputs
+    assert app(Kr=ctypes.c_void_p(0x60000)) == 1 and app(Kr=ctypes.c_void_p(0x60000 + 256)) == 1
+    assert app(Q=Q, Qr=ctypes.c_void_p(0x10000)) == 1
