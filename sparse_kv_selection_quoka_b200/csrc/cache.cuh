@@ -48,13 +48,13 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t c, float* v) {
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
 // The exponent of a stored scale. Only the exponent field is used, kept to
-// the range of scales; anything that is not a power of two in that range is
-// latched.
-__device__ __forceinline__ int scale_exp(float s, int* status) {
+// the range of scales; anything that is not a power of two in that range sets
+// *bad.
+__device__ __forceinline__ int scale_exp(float s, bool* bad) {
   const int u = __float_as_int(s);
   const int e = (u >> 23) - 127;  // (a sign bit makes it negative, out of range)
   const int k = min(max(e, kCacheMinExp), kCacheMaxExp);
-  if ((k != e || (u & 0x7FFFFF) != 0) && status != nullptr) latch_status(status, 6 /* QUOKA_ERR_BOUNDS */);
+  *bad |= k != e || (u & 0x7FFFFF) != 0;
   return k;
 }
 

@@ -201,7 +201,9 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheAppen
   int e = scale_exp_for(__uint_as_float(top));
   uint8_t* dst = (is_v ? a.c.v : a.c.k) + page * a.c.sp + j * a.c.sh;
   if (t0 > p0) {  // the page holds earlier tokens
-    const int eo = scale_exp(old, a.status);
+    bool bad = false;
+    const int eo = scale_exp(old, &bad);
+    if (bad && tid == 0 && a.status != nullptr) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
     if (e > eo) {
       const float f = exp2i(eo - e);
       for (int r = rr; r < t0 - p0; r += RPP) {

@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const CacheGathe
     const int64_t off = p * a.c.sp + j * a.c.sh + (tau & ((1 << a.c.page_log2) - 1)) * a.c.sr + 8 * c;
     kw[u] = ld_codes(a.c.k + off);
     vw[u] = ld_codes(a.c.v + off);
-    kf[u] = exp2i(scale_exp(__ldcg(a.c.k_scale + (int64_t)p * a.c.nkv + j), a.status));
-    vf[u] = exp2i(scale_exp(__ldcg(a.c.v_scale + (int64_t)p * a.c.nkv + j), a.status));
+    kf[u] = exp2i(scale_exp(__ldcg(a.c.k_scale + (int64_t)p * a.c.nkv + j), &bad));
+    vf[u] = exp2i(scale_exp(__ldcg(a.c.v_scale + (int64_t)p * a.c.nkv + j), &bad));
   }
 #pragma unroll
   for (int u = 0; u < kItems; ++u) {

@@ -223,13 +223,14 @@ struct CacheAttnArgs {
   float scale;
   float* O_parts;           // (nsplit, b, nq, BCP, d) fp32
   float* lse_parts;         // (nsplit, b, nq, BCP) fp32, in log2 units
+  int* faults;              // (b, nkv, nsplit): what a range's CTA has to latch
   int nsplit;               // cache_attn_splits(b * nkv, N)
   void* O;
   float* lse;
   int* status;
 };
 int cache_attn_splits(int64_t heads, int N);
-cudaError_t launch_cache_attn(bool bf16, int d, const CacheAttnArgs& a, bool pdl, cudaStream_t stream);
+cudaError_t launch_cache_attn(bool bf16, int d, const CacheAttnArgs& a, cudaStream_t stream);
 
 // Step (d) over the cache's keys: S_agg (b, nkv, max_len); entries at and
 // past seq_len are not written (cache_score.cu).

@@ -492,7 +492,7 @@ bool overlaps(const void* a, size_t na, const quoka_tensor* t) {
 struct CacheAttnWs {
   bool few;
   int nsplit;
-  size_t o_parts, lse_parts, ksel, vsel, count, aparts, aparts_bytes, total;
+  size_t o_parts, lse_parts, faults, ksel, vsel, count, aparts, aparts_bytes, total;
 };
 
 CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t BCP, int64_t N, quoka_dtype dtype,
@@ -510,6 +510,7 @@ CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t
     const int64_t rows = w.nsplit * b * nq * BCP;
     w.o_parts = take((size_t)(rows * d) * 4);
     w.lse_parts = take((size_t)rows * 4);
+    w.faults = take((size_t)(b * nkv * w.nsplit) * 4);
   } else {
     w.ksel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
     w.vsel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
@@ -901,7 +902,6 @@ quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, i
   if (st != QUOKA_OK) return st;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   int* status = static_cast<int*>(ws);
-  if (quoka::clear_status_async(status, cs) != cudaSuccess) return QUOKA_ERR_CUDA;
   if (w.few) {
     a.Q = strided(Q);
     if (!no_chunk) {
@@ -923,8 +923,10 @@ quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, i
     a.O = O;
     a.lse = lse;
     a.status = status;
-    return cuda_status(quoka::launch_cache_attn(bf, (int)d, a, true, cs));
+    a.faults = at<int>(ws, w.faults);
+    return cuda_status(quoka::launch_cache_attn(bf, (int)d, a, cs));
   }
+  if (quoka::clear_status_async(status, cs) != cudaSuccess) return QUOKA_ERR_CUDA;
   // many query rows: the rows dequantised once, then the attention over dense rows
   if (N > 0) {
     quoka::CacheGatherArgs g = {};
