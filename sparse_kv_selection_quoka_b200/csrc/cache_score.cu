@@ -6,17 +6,25 @@
 // The page's scale cancels: the score reads the codes alone.
 //
 // Precision. Codes are exact in fp16; the fp32 group means (|q| <= 1) are
-// scaled by 2^12 and split into two halves (22 bits of each element), both
-// multiplied on the tensor core with fp32 accumulation; |k|^2 is summed in
-// fp32 from the same codes.
+// scaled by 2^12 and split into two halves hi + lo (22 bits of each element),
+// both multiplied on the tensor core with fp32 accumulation. |k|^2 is the
+// diagonal of K K^T, whose operands are the registers already there: its
+// products are exact too.
 //
-// Work split: one CTA of 4 warps per 128 keys of a (sequence, KV head); a warp
-// holds the code rows of 32 keys in registers, loaded in the operand layout of
-// mma.sync (the columns of a k-step may be any 16 as long as Q_group is
-// permuted alike, so a lane reads whole 16-byte chunks), and multiplies them
-// with the group means in 16-row tiles from shared memory, at most 4 tiles
-// at a time.
+// Work split. The keys of a (sequence, KV head) are cut into nsplit contiguous
+// ranges, one CTA each: a loader warp copies 128 code rows at a time into a
+// ring of stages (cp.async, zeros for a page that is not there; the page
+// table is read a stage ahead), four warps take 32 of them each. Keys are the
+// rows of the product and group means its 8 columns: up to 4 group means put
+// hi and lo side by side into one tile, kept in registers, and a 16 x 16 step
+// costs three products; more go through shared memory, 64 at a time. The
+// operand reads are those of cache_attn.cu (any 16 columns make a k-step; chunk
+// c of row r lies at c ^ (r & 7)). The scores' value-bucket histogram (the
+// top-k's first digit) is made on the way: counts in shared memory, added to
+// the row's at the end.
+// Bound by the codes' bytes for few group means.
 #include "cache.cuh"
+#include "sm100.cuh"
 
 namespace quoka {
 
@@ -24,9 +32,11 @@ namespace {
 
 using namespace cache;
 
-constexpr int kThreads = 128;
-constexpr int kKeys = 128;   // keys of one CTA
-constexpr int kTiles = 4;    // 16-row tiles of group means in shared memory at a time
+constexpr int kThreads = 160;     // four computing warps and the loader
+constexpr int kStage = 128;       // keys of a stage
+constexpr int kStages = 3;
+constexpr int kQueries = 64;      // group means in shared memory at a time
+constexpr int kPacked = 4;        // up to this many fit one tile as hi and lo
 constexpr float kQScale = 4096.f;
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -37,151 +47,282 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// acc + x^2 of a half, in fp32
-__device__ __forceinline__ float sq_add(float acc, uint32_t h2) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  return fmaf(f.y, f.y, fmaf(f.x, f.x, acc));
+// Byte of chunk c (16 bytes) of row r of a stage.
+template <int D>
+__device__ __forceinline__ int at_chunk(int r, int c) {
+  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
 
-// grid (ceil(max_len / 128), nkv, b)
+struct Shared {
+  uint64_t full[kStages], empty[kStages];
+  int abort;
+  uint32_t hist[TOPK_HIST_BINS];
+};
+
+// Dynamic shared memory: the ring, then the group means' fragments
+// [n-tile][k-step][lane] of 16 bytes (hi b0, hi b1, lo b0, lo b1).
 template <int D>
-__global__ void __launch_bounds__(kThreads) cache_score_kernel(const CacheScoreArgs a) {
+constexpr size_t smem_bytes(int NQ) {
+  const int nt = NQ <= kPacked ? 1 : ((NQ < kQueries ? NQ : kQueries) + 7) / 8;
+  return (size_t)kStages * kStage * D + (size_t)nt * (D / 16) * 512;
+}
+
+// The loader warp: code rows [k0, k1) of the (sequence, head), `passes` times.
+template <int D>
+__device__ __forceinline__ void load_rows(const CacheScoreArgs& a, Shared& sh, uint8_t* ring, int lane, int bi, int j,
+                                          int k0, int k1, int passes) {
+  constexpr int CPR = D / 16, RPI = 32 / CPR;  // chunks of a row, rows of a warp-wide copy
+  const int plog = a.c.page_log2, pmask = (1 << plog) - 1;
+  const int32_t* table = a.c.page_table + (int64_t)bi * a.c.table_stride;
+  const int nst = (k1 - k0 + kStage - 1) / kStage, total = nst * passes;
+  bool bad = false;
+  // the page of this lane's 16 keys (lane % 8) of the it-th stage
+  auto page_of = [&](int it) {
+    const int key = k0 + it % nst * kStage + 16 * (lane & 7);
+    return it < total && key < k1 ? __ldcg(table + (key >> plog)) : -1;
+  };
+  int p0 = page_of(0), p1 = page_of(1);
+  for (int it = 0; it < total; ++it) {
+    const int p2 = page_of(it + 2);
+    const int st = it % kStages, base = k0 + it % nst * kStage;
+    if (it >= kStages && !__all_sync(0xffffffffu, sm100::mbar_wait(&sh.empty[st], (it / kStages - 1) & 1, &sh.abort))) {
+      if (lane == 0) {
+        sh.abort = 1;
+        latch_status(a.status, 5 /* QUOKA_ERR_TIMEOUT */);
+        latch_where(a.status, 63);
+      }
+      break;
+    }
+    const bool held = p0 >= 0 && p0 < a.c.npages;
+    bad |= !held && base + 16 * (lane & 7) < k1;
+    const int pg = held ? p0 : -1;
+    const uint32_t dst = sm100::smem_u32(ring + st * kStage * D);
+    const int c = lane % CPR, r0 = lane / CPR;
+    const uint8_t* kb = a.c.k + j * a.c.sh + 16 * c;
+#pragma unroll
+    for (int i = 0; i < kStage / RPI; ++i) {
+      const int r = i * RPI + r0;
+      const int p = __shfl_sync(0xffffffffu, pg, i * RPI / 16);  // (a copy's rows lie in one group of 16)
+      const bool there = p >= 0 && base + r < k1;
+      const int64_t off = there ? p * a.c.sp + (int64_t)((base + r) & pmask) * a.c.sr : 0;
+      sm100::cp_async_16(dst + at_chunk<D>(r, c), kb + off, there ? 16u : 0u);
+    }
+    sm100::cp_async_arrive_noinc(&sh.full[st]);
+    p0 = p1;
+    p1 = p2;
+  }
+  sm100::cp_async_commit();
+  sm100::cp_async_wait<0>();
+  if (bad) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
+}
+
+// grid (nsplit, nkv, b). PACKED: NQ <= kPacked.
+template <int D, bool PACKED>
+__global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const CacheScoreArgs a) {
   constexpr int KS = D / 16;
-  __shared__ uint4 qs[kTiles][2][KS][32];  // fragments of the group means: halves hi, lo
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Shared sh;
+  uint8_t* ring = smem;
+  uint4* qs = reinterpret_cast<uint4*>(smem + kStages * kStage * D);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int j = blockIdx.y, bi = blockIdx.z;
   const int64_t row = (int64_t)bi * a.c.nkv + j;
   pdl_trigger();
-  pdl_wait();
-  const int len = cache_len(a.c, bi, a.max_len, a.status);
-  const int key0 = blockIdx.x * kKeys;
-  if (key0 >= len) return;
-  const int base = key0 + warp * 32;
-  const int plog = a.c.page_log2, pmask = (1 << plog) - 1;
-
-  // this warp's keys: n-tile nt holds keys base + 8 nt + g
-  uint32_t kw[4][KS];
-  {
-    int64_t off = -1;  // lane i answers for key i
-    if (base + lane < len) {
-      const int p = cache_page(a.c, bi, (base + lane) >> plog, a.status);
-      if (p >= 0) off = p * a.c.sp + j * a.c.sh + (int64_t)((base + lane) & pmask) * a.c.sr;
+  // (the cache, its table and lengths are inputs of the call: only the group
+  // means, the histogram and the status words are waited for)
+  const int want = __ldcg(a.c.seq_len + bi), len = min(max(want, 0), a.max_len);
+  const int per = (len + a.nsplit * kStage - 1) / (a.nsplit * kStage) * kStage;
+  const int k0 = min(len, (int)blockIdx.x * per), k1 = min(len, k0 + per);
+  const int passes = PACKED ? 1 : (a.NQ + kQueries - 1) / kQueries;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      sm100::mbar_init(&sh.full[i], 32);
+      sm100::mbar_init(&sh.empty[i], 4);
     }
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const int64_t ro = __shfl_sync(0xffffffffu, off, 8 * nt + g);
-#pragma unroll
-      for (int w = 0; w < KS; ++w) kw[nt][w] = 0u;
-      if (ro >= 0) {
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          const uint4 v = *reinterpret_cast<const uint4*>(a.c.k + ro + 16 * t4 + 64 * h);
-          kw[nt][4 * h] = v.x;
-          kw[nt][4 * h + 1] = v.y;
-          kw[nt][4 * h + 2] = v.z;
-          kw[nt][4 * h + 3] = v.w;
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  for (int i = tid; i < TOPK_HIST_BINS; i += kThreads) sh.hist[i] = 0u;
+  __syncthreads();
+  if (want != len && tid == 0) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
+
+  if (k0 >= k1) {
+    pdl_wait();
+    return;
+  }
+  if (warp == 4) {
+    load_rows<D>(a, sh, ring, lane, bi, j, k0, k1, passes);
+  } else {
+    pdl_wait();
+    const float* qg = a.Qg + row * a.NQ * D;
+    const int nst = (k1 - k0 + kStage - 1) / kStage;
+    const int gk = g ^ ((g & 1) << 2);  // operand row g (and g + 8) of a step is key gk (and gk + 8)
+    uint32_t qb[PACKED ? KS : 1][2];
+    bool alive = true;
+    for (int pass = 0; pass < passes && alive; ++pass) {
+      const int i0 = pass * kQueries, nq = min(kQueries, a.NQ - i0);
+      const int tiles = PACKED ? 1 : (nq + 7) / 8;
+      if (pass > 0) sm100::named_barrier_sync(1, 128);
+      // column d of group mean i: k-step ks of lane 4 (i % 8) + t, with chunk d / 16 = t + 4 (ks / 4) and
+      // word (d % 16) / 4 = ks % 4
+      for (int e = tid; e < (PACKED ? 4 : tiles * 8) * (D / 2); e += 128) {
+        const int i = e / (D / 2), d = 2 * (e % (D / 2));
+        float2 x = make_float2(0.f, 0.f);
+        if (i < nq) x = __ldcg(reinterpret_cast<const float2*>(qg + (int64_t)(i0 + i) * D + d));
+        x.x *= kQScale;
+        x.y *= kQScale;
+        const __half2 hi = __floats2half2_rn(x.x, x.y);
+        const float2 f = __half22float2(hi);
+        const __half2 lo = __floats2half2_rn(x.x - f.x, x.y - f.y);
+        const int ch = d >> 4, ks = 4 * (ch >> 2) + ((d & 15) >> 2), reg = (d >> 1) & 1;
+        uint4* q = qs + ((i >> 3) * KS + ks) * 32 + (ch & 3);
+        if (PACKED) {  // columns 0 .. 3 hi, 4 .. 7 lo
+          reinterpret_cast<__half2*>(q + 4 * i)[reg] = hi;
+          reinterpret_cast<__half2*>(q + 4 * (i + 4))[reg] = lo;
+        } else {
+          reinterpret_cast<__half2*>(q + 4 * (i & 7))[reg] = hi;
+          reinterpret_cast<__half2*>(q + 4 * (i & 7))[2 + reg] = lo;
         }
       }
-    }
-  }
-
-  float best[4][2];  // per n-tile: keys 2 t, 2 t + 1, over the lane's rows
-  float ss[4] = {0.f, 0.f, 0.f, 0.f};
+      sm100::named_barrier_sync(1, 128);
+      if (PACKED) {
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) best[nt][0] = best[nt][1] = -INFINITY;
-  const float* qg = a.Qg + row * a.NQ * D;
-  for (int i0 = 0; i0 < a.NQ; i0 += 16 * kTiles) {
-    const int tiles = min(kTiles, (a.NQ - i0 + 15) / 16);
-    if (i0 > 0) __syncthreads();
-    // column d of row i belongs to lane t = (d / 16) % 4, k-step 4 (d / 64) + (d % 16) / 4
-    for (int e = tid; e < tiles * 16 * (D / 2); e += kThreads) {
-      const int i = e / (D / 2), d = 2 * (e % (D / 2));
-      float2 x = make_float2(0.f, 0.f);
-      if (i0 + i < a.NQ) x = __ldcg(reinterpret_cast<const float2*>(qg + (int64_t)(i0 + i) * D + d));
-      x.x *= kQScale;
-      x.y *= kQScale;
-      const __half2 hi = __floats2half2_rn(x.x, x.y);
-      const float2 f = __half22float2(hi);
-      const __half2 lo = __floats2half2_rn(x.x - f.x, x.y - f.y);
-      const int ch = d >> 4, ks = 4 * (ch >> 2) + ((d & 15) >> 2), r = i & 15;
-      const int reg = ((d >> 1) & 1) * 2 + (r >> 3), ln = (r & 7) * 4 + (ch & 3);
-      reinterpret_cast<__half2*>(&qs[i >> 4][0][ks][ln])[reg] = hi;
-      reinterpret_cast<__half2*>(&qs[i >> 4][1][ks][ln])[reg] = lo;
-    }
-    __syncthreads();
-    float c[kTiles][4][4];
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) c[m][nt][0] = c[m][nt][1] = c[m][nt][2] = c[m][nt][3] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      uint32_t b0[4], b1[4];
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        b0[nt] = e4m3x2_to_f16x2((uint16_t)kw[nt][ks]);
-        b1[nt] = e4m3x2_to_f16x2((uint16_t)(kw[nt][ks] >> 16));
-        if (i0 == 0) ss[nt] = sq_add(sq_add(ss[nt], b0[nt]), b1[nt]);
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint2 q = *reinterpret_cast<const uint2*>(qs + ks * 32 + lane);
+          qb[ks % (PACKED ? KS : 1)][0] = q.x;
+          qb[ks % (PACKED ? KS : 1)][1] = q.y;
+        }
       }
+      for (int s = 0; s < nst; ++s) {
+        const int it = pass * nst + s, st = it % kStages;
+        if (!__all_sync(0xffffffffu, sm100::mbar_wait(&sh.full[st], (it / kStages) & 1, &sh.abort))) {
+          if (lane == 0) {
+            sh.abort = 1;
+            latch_status(a.status, 5 /* QUOKA_ERR_TIMEOUT */);
+            latch_where(a.status, 64);
+          }
+          alive = false;
+          break;
+        }
+        const uint8_t* stage = ring + st * kStage * D;
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        if (m < tiles) {
+        for (int m = 0; m < 2; ++m) {
+          const int r0 = warp * 32 + m * 16, key = k0 + s * kStage + r0 + gk;
+          uint32_t kw[2][KS];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint4 q = qs[m][half][ks][lane];
-            const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) mma_f16(c[m][nt], qa, b0[nt], b1[nt]);
+            for (int h = 0; h < D / 64; ++h) {
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + at_chunk<D>(r0 + gk + 8 * u, t4 + 4 * h));
+              kw[u][4 * h] = w.x;
+              kw[u][4 * h + 1] = w.y;
+              kw[u][4 * h + 2] = w.z;
+              kw[u][4 * h + 3] = w.w;
+            }
+          uint32_t ka[KS][4];
+          float n0[4] = {0.f, 0.f, 0.f, 0.f}, n1[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            ka[ks][0] = e4m3x2_to_f16x2((uint16_t)kw[0][ks]);
+            ka[ks][1] = e4m3x2_to_f16x2((uint16_t)kw[1][ks]);
+            ka[ks][2] = e4m3x2_to_f16x2((uint16_t)(kw[0][ks] >> 16));
+            ka[ks][3] = e4m3x2_to_f16x2((uint16_t)(kw[1][ks] >> 16));
+            mma_f16(n0, ka[ks], ka[ks][0], ka[ks][2]);
+            mma_f16(n1, ka[ks], ka[ks][1], ka[ks][3]);
+            if (PACKED) mma_f16(c, ka[ks], qb[ks % (PACKED ? KS : 1)][0], qb[ks % (PACKED ? KS : 1)][1]);
+          }
+          float x0 = -INFINITY, x1 = -INFINITY;  // the best of keys gk, gk + 8 over the lane's columns
+          if (PACKED) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) c[u] += __shfl_xor_sync(0xffffffffu, c[u], 2);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (2 * (t4 & 1) + u < a.NQ) {
+                x0 = fmaxf(x0, c[u]);
+                x1 = fmaxf(x1, c[2 + u]);
+              }
+          } else {
+            for (int nt = 0; nt < tiles; ++nt) {
+              c[0] = c[1] = c[2] = c[3] = 0.f;
+#pragma unroll
+              for (int ks = 0; ks < KS; ++ks) {
+                const uint4 q = qs[(nt * KS + ks) * 32 + lane];
+                mma_f16(c, ka[ks], q.x, q.y);
+                mma_f16(c, ka[ks], q.z, q.w);
+              }
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                if (8 * nt + 2 * t4 + u < nq) {
+                  x0 = fmaxf(x0, c[u]);
+                  x1 = fmaxf(x1, c[2 + u]);
+                }
+            }
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+          }
+          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+          if (t4 == (g >> 1)) {  // the lane that holds the diagonal's g-th element
+            const float q0 = g & 1 ? n0[1] : n0[0], q1 = g & 1 ? n1[3] : n1[2];
+            float* S = a.S_agg + row * a.max_len + key;
+            auto put = [&](int at, float x, float k2) {
+              if (key + at >= k1) return;
+              x = x * (1.f / kQScale) / fmaxf(sqrtf(k2), 1e-12f);
+              if (!PACKED && pass > 0) x = fmaxf(x, S[at]);  // (this thread's own score of the passes before)
+              S[at] = x;
+              if (pass == passes - 1) atomicAdd(&sh.hist[score_bin(x)], 1u);
+            };
+            put(0, x0, q0);
+            put(8, x1, q1);
           }
         }
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&sh.empty[st]);
       }
     }
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      const bool r0 = i0 + 16 * m + g < a.NQ, r1 = i0 + 16 * m + g + 8 < a.NQ;
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (r0) best[nt][u] = fmaxf(best[nt][u], c[m][nt][u]);
-          if (r1) best[nt][u] = fmaxf(best[nt][u], c[m][nt][2 + u]);
-        }
-    }
   }
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    // |k|^2 of key g over the quad; then the norms of keys 2 t, 2 t + 1
-    ss[nt] += __shfl_xor_sync(0xffffffffu, ss[nt], 1);
-    ss[nt] += __shfl_xor_sync(0xffffffffu, ss[nt], 2);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float x = best[nt][u];
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-      const float k2 = __shfl_sync(0xffffffffu, ss[nt], 4 * (2 * t4 + u));
-      const int key = base + 8 * nt + 2 * t4 + u;
-      if (g == 0 && key < len)
-        a.S_agg[row * a.max_len + key] = x * (1.f / kQScale) / fmaxf(sqrtf(k2), 1e-12f);
-    }
+  __syncthreads();
+  pdl_wait();  // (the loader's threads: the histogram's zeros)
+  uint32_t* hist = a.hist + row * TOPK_HIST_BINS;
+  for (int i = tid; i < TOPK_HIST_BINS; i += kThreads) {
+    const uint32_t n = sh.hist[i];
+    if (n != 0u) atomicAdd(hist + i, n);
   }
+}
+
+// One round of CTAs at three an SM, a range being at least 256 keys.
+constexpr int kSplitCTAs = 444, kSplitKeys = 256;
+
+template <int D>
+cudaError_t launch_typed(const CacheScoreArgs& args, cudaStream_t stream) {
+  CacheScoreArgs a = args;
+  const int64_t heads = (int64_t)a.b * a.c.nkv;
+  const int64_t want = (kSplitCTAs + heads - 1) / heads, most = (a.max_len + kSplitKeys - 1) / kSplitKeys;
+  a.nsplit = (int)(want < most ? want : most);
+  auto* kern = a.NQ <= kPacked ? cache_score_kernel<D, true> : cache_score_kernel<D, false>;
+  const size_t smem = smem_bytes<D>(a.NQ);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.nsplit, a.c.nkv, a.b);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;  // waits for the group means inside
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_score(int d, const CacheScoreArgs& a, cudaStream_t stream) {
   if (a.NQ < 1 || a.max_len < 1) return cudaErrorInvalidValue;
-  if (d != 64 && d != 128) return cudaErrorNotSupported;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.max_len + kKeys - 1) / kKeys, a.c.nkv, a.b);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;  // waits for the group means inside
-  return cudaLaunchKernelEx(&cfg, d == 128 ? cache_score_kernel<128> : cache_score_kernel<64>, a);
+  if (d == 128) return launch_typed<128>(a, stream);
+  if (d == 64) return launch_typed<64>(a, stream);
+  return cudaErrorNotSupported;
 }
 
 }  // namespace quoka

@@ -233,14 +233,17 @@ int cache_attn_splits(int64_t heads, int N);
 cudaError_t launch_cache_attn(bool bf16, int d, const CacheAttnArgs& a, cudaStream_t stream);
 
 // Step (d) over the cache's keys: S_agg (b, nkv, max_len); entries at and
-// past seq_len are not written (cache_score.cu).
+// past seq_len are not written. Adds the scores' value buckets to `hist`
+// (b * nkv, TOPK_HIST_BINS), zeroed beforehand (cache_score.cu).
 struct CacheScoreArgs {
   CacheView c;
   int b, max_len;
   const float* Qg;  // (b, nkv, NQ, d) fp32 group means
   int NQ;
   float* S_agg;
+  uint32_t* hist;
   int* status;
+  int nsplit = 1;  // ranges of a row's keys (set by the launcher)
 };
 cudaError_t launch_cache_score(int d, const CacheScoreArgs& a, cudaStream_t stream);
 

@@ -817,14 +817,15 @@ quoka_status quoka_cache_select(const quoka_tensor* Q, const quoka_cache* cache,
   float* qg = at<float>(ws, L.qgroup);
   int32_t* qidx = q_idx != nullptr ? q_idx : at<int32_t>(ws, L.qidx);
   a.status = at<int>(ws, L.status);
-  // (the status words are cleared by the kernel that makes the group means)
+  a.hist = at<uint32_t>(ws, L.hist);
+  // (the status words and the histogram are cleared by the kernel that makes the group means)
   cudaError_t e = cudaErrorNotSupported;
   if (bf && d == 128)
-    e = quoka::launch_qsel_group_fast(strided(Q), b, nq, nkv, BCP, NQ, qidx, qg, nullptr, nullptr, a.status, true, cs);
+    e = quoka::launch_qsel_group_fast(strided(Q), b, nq, nkv, BCP, NQ, qidx, qg, nullptr, a.hist, a.status, true, cs);
   if (e == cudaErrorNotSupported) {
     e = quoka::launch_qsel(bf, d, strided(Q), b, nq, BCP, NQ, at<float>(ws, L.qhat), qidx, true, cs);
     if (e != cudaSuccess) return cuda_status(e);
-    e = quoka::launch_qgroup(d, at<float>(ws, L.qhat), b, nq, nkv, NQ, qg, nullptr, nullptr, a.status, cs);
+    e = quoka::launch_qgroup(d, at<float>(ws, L.qhat), b, nq, nkv, NQ, qg, nullptr, a.hist, a.status, cs);
   }
   if (e != cudaSuccess) return cuda_status(e);
   a.b = b;
@@ -837,7 +838,7 @@ quoka_status quoka_cache_select(const quoka_tensor* Q, const quoka_cache* cache,
     if (e != cudaSuccess) return cuda_status(e);
   }
   if (bsa_eff > 0)
-    return cuda_status(quoka::launch_topk(a.S_agg, b, nkv, max_len, bsa_eff, nullptr, kv_idx, kv_count, a.status, true,
+    return cuda_status(quoka::launch_topk(a.S_agg, b, nkv, max_len, bsa_eff, a.hist, kv_idx, kv_count, a.status, true,
                                           cs, cache->seq_len));
   return cudaMemsetAsync(kv_count, 0, sizeof(int32_t) * b * nkv, cs) == cudaSuccess ? QUOKA_OK : QUOKA_ERR_CUDA;
 }

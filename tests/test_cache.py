@@ -757,7 +757,7 @@ def _cache(**kw):
 
 def test_entry_points_reject_bad_arguments_on_host(lib):  # noqa: F811
     """Every refusal comes before anything is enqueued (no GPU here)."""
-    B = ctypes.byref
+    B = lambda t: bytes(t) if isinstance(t, type(_view((1, 1, 1, 1)))) else ctypes.byref(t)
     ws, buf, out = (ctypes.c_void_p(x) for x in (0x100000, 0x200000, 0x300000))
     Q, K = _view((1, 4, 7, 128)), _view((1, 2, 7, 128), data=0x60000)
     big = 1 << 30
