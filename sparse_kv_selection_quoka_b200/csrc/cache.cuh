@@ -84,5 +84,25 @@ __device__ __forceinline__ int cache_page(const CacheView& c, int bi, int col, i
   return -1;
 }
 
+// c (16 x 8, fp32) += a (16 x 16, fp16) * b (16 x 8, fp16)
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte of chunk c (16 bytes) of row r of code rows in shared memory: the
+// layout of a tiled TMA load swizzled by 128 (d = 128) or 64 bytes (d = 64).
+template <int D>
+__device__ __forceinline__ int at_chunk(int r, int c) {
+  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Rows of a box of the pools' tensor maps: a run of keys that starts on a
+// multiple of 64 splits into boxes of one page each.
+__host__ __device__ __forceinline__ int box_log2(const CacheView& c) { return c.page_log2 < 6 ? c.page_log2 : 6; }
+
 }  // namespace cache
 }  // namespace quoka

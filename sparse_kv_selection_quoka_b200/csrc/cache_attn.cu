@@ -22,25 +22,32 @@
 // weights; with bf16 rows a weight is rounded to fp16 once (2^-11 of it, finer
 // than the bf16 output). Products accumulate in fp32.
 //
-// Work split. The keys of a (sequence, KV head) are cut into nsplit contiguous
-// ranges, one CTA each: a loader warp and four that compute. The loader looks
-// the rows up (list entry, page, scales: each one stage ahead of the next, so
-// that no lookup is waited for) and copies 64 keys at a time into a ring of
-// stages with cp.async, zeros in place of rows that are absent; rows of any
-// stride, whole pages and listed rows go the same way. The computing warps
-// share the 16-row query tiles and take a stage's four 16-key steps in turn.
+// Work split. The keys of every (sequence, KV head) are cut into ranges of
+// near equal length, so many in all as CTAs are resident at once, one CTA
+// each: every CTA reads all lengths and finds its own range. A loader warp
+// looks the rows up (list entry, page, scales: each a stage ahead of the next,
+// so that no lookup is waited for) and copies 128 keys at a time into a ring of
+// stages: listed rows with cp.async, runs of keys by boxes of up to 64 with
+// TMA; a row that is not there reads as zeros. Four warps compute. They
+// share the query tiles (8 rows, or 16 where there are more) and take a
+// stage's 32-key steps in turn.
+// Keys are the rows of the first product S^T = K Q^T, columns of the head those
+// of the second, O^T = V^T P^T, so that few query rows fill its 8 columns.
 // Codes go from shared memory straight into the operand layouts of mma.sync:
-// for Q K^T the columns of a k-step may be any 16 as long as Q is permuted
+// for K Q^T the columns of a k-step may be any 16 as long as Q is permuted
 // alike, so lane (g, t) reads the 16-byte chunks t and t + 4 of a key's row;
-// for P V a lane needs the 4 keys of its P fragment and may own any column per
-// n-tile, so lane (g, t) reads the columns [16 g, 16 g + 16) of four keys.
-// Chunk c of row r lies at c ^ (r & 7), and operand row n of a step stands for
-// key n ^ 4 (n & 1), so that neither read has a bank conflict (d = 128; d = 64
-// keeps a two-way one on V). A second kernel joins the ranges of every query
-// row and adds the chunk's own keys (at most 64) in fp32.
+// V^T needs 4 keys of a lane and any columns, so lane (g, t) reads the columns
+// [16 g, 16 g + 16) of four keys; P is transposed between the two by
+// movmatrix. Chunk c of row r lies at c ^ (r & 7), and operand row n of a step
+// stands for key n ^ 4 (n & 1), so that neither read has a bank conflict
+// (d = 128; d = 64 keeps a two-way one on V). A second kernel joins the ranges
+// of every query row and adds the chunk's own keys (at most 64) in fp32.
 // Bound by the cache's bytes, each read once per 64 query rows.
+#include <algorithm>
+
 #include "cache.cuh"
 #include "sm100.cuh"
+#include "tmap.cuh"
 
 namespace quoka {
 
@@ -49,23 +56,22 @@ namespace {
 using namespace cache;
 
 constexpr int kThreads = 160;      // four computing warps and the loader
-constexpr int kStep = 16;          // keys of one step of a warp
-constexpr int kStage = 64;         // keys of a stage of the ring
-constexpr int kStages = 4;
+constexpr int kStep = 32;          // keys of one step of a warp: two operand tiles
+constexpr int kStage = 128;        // keys of a stage of the ring
+constexpr int kStages = 2;
 // M is set kHead below the row maximum and may lag it by kLazy: weights then
 // stay below 2^15 (fp16 holds 65504), and one that fp16 holds as a subnormal
 // is off by at most 2^-25, 2^-32 of the row's largest.
 constexpr float kHead = 7.f, kLazy = 15.f;
+// One round of CTAs at three an SM, a range being at least kSplitKeys keys.
+#ifndef SPLIT_CTAS
+#define SPLIT_CTAS 444
+#endif
+#ifndef SPLIT_KEYS
+#define SPLIT_KEYS 128
+#endif
+constexpr int kSplitCTAs = SPLIT_CTAS, kSplitKeys = SPLIT_KEYS;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// c (16 x 8, fp32) += a (16 x 16, fp16) * b (16 x 8, fp16)
-__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -77,61 +83,118 @@ __device__ __forceinline__ uint32_t rest_h2(float lo, float hi, uint32_t h) {
   return pack_h2(lo - f.x, hi - f.y);
 }
 
-// Shared memory: the query fragments [tiles][SPLIT][D / 16][32 lanes] of 16
-// bytes and the rows' factors [tiles * 16]; the stages of codes (keys, then
-// values, then the 64 keys' scale exponents). After the loop the warps'
-// outputs [4][16][D] fp32 and their (M, l) [4][16][2] lie over the stages.
+// 8 x 8 halves, a row's pairs over four lanes: transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Shared memory: the query fragments [8-row tiles][D / 16][32 lanes] of two
+// words (four for fp32 rows: hi, lo) and the rows' factors, behind the stages of
+// codes (keys, then values; aligned to 1024 bytes). After the loop the warps'
+// outputs [4][8 RT][D] fp32 and their (M, l) [4][8 RT][2] lie over the stages.
 template <int D>
 struct Ring {
-  static constexpr int kBytes = kStage * D;                  // codes of a stage's keys (or values)
-  static constexpr int kPitch = 2 * kBytes + kStage * 4;     // a stage
+  static constexpr int kBytes = kStage * D;   // codes of a stage's keys (or values)
+  static constexpr int kPitch = 2 * kBytes;   // a stage
   static constexpr int kTotal = kStages * kPitch;
   static_assert(kTotal >= 4 * 16 * D * 4 + 4 * 16 * 2 * 4, "the join's scratch lies over the ring");
 };
 template <int D, int SPLIT>
-constexpr size_t smem_bytes(int tiles) {
-  return (size_t)tiles * SPLIT * (D / 16) * 512 + (size_t)tiles * 16 * 4 + Ring<D>::kTotal;
-}
-
-// Byte of chunk c (16 bytes) of row r of a stage.
-template <int D>
-__device__ __forceinline__ int at_chunk(int r, int c) {
-  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+constexpr size_t smem_bytes(int tiles8) {
+  return (size_t)tiles8 * (D / 16) * 32 * 8 * SPLIT + (size_t)tiles8 * 32 + Ring<D>::kTotal + 1024;
 }
 
 struct Shared {
   uint64_t full[kStages], empty[kStages];
+  uint32_t ex[kStages][kStage];  // scale exponents: ek + 64 in the low half, ev + 64 in the high
   int abort, fault, site;
+  int row, k0, k1;  // this CTA's range (row < 0: none)
 };
 
-// The loader warp: rows [k0, k1) of the (sequence, head), 64 at a time.
+// Keys of row `row` = sequence * nkv + head.
+template <bool IDX>
+__device__ __forceinline__ int row_keys(const CacheAttnArgs& a, int row) {
+  if (IDX) return min(max(__ldcg(a.kv_count + row), 0), a.N);
+  return min(max(__ldcg(a.c.seq_len + row / a.c.nkv), 0), a.max_len);
+}
+
+// The range of CTA `cta` (one warp): rows are cut into ranges of at most
+// `most` keys, total / target rounded up, each row into equal ones.
+template <bool IDX>
+__device__ __forceinline__ void find_range(const CacheAttnArgs& a, Shared& sh, int cta, int lane) {
+  const int rows = a.b * a.c.nkv;
+  int64_t total = 0;
+  for (int i = lane; i < rows; i += 32) total += row_keys<IDX>(a, i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  // (rows have at most 2^30 keys)
+  const int most = (int)min(max((int64_t)kSplitKeys, (total + a.target - 1) / a.target), (int64_t)1 << 30);
+  int before = 0;  // ranges of the rows before
+  if (lane == 0) sh.row = -1;
+  __syncwarp();
+  for (int i0 = 0; i0 < rows; i0 += 32) {
+    const int i = i0 + lane;
+    const int n = i < rows ? row_keys<IDX>(a, i) : 0;
+    const int parts = i < rows ? max(1, (n + most - 1) / most) : 0;
+    int incl = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int first = before + incl - parts;
+    if (cta >= first && cta < first + parts) {
+      const int per = ((n + parts - 1) / parts + 63) & ~63;  // (whole boxes)
+      sh.row = i;
+      sh.k0 = min(n, (cta - first) * per);
+      sh.k1 = min(n, sh.k0 + per);
+      if (cta == first) a.row_parts[i] = make_int2(first, parts);
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    if (before > cta) break;
+  }
+}
+
+struct Maps {
+  CUtensorMap k, v;  // the pools (only read without an index list)
+};
+
+// The loader warp: rows [k0, k1) of the (sequence, head), 128 at a time.
+// Listed rows are copied one by one with cp.async; without a list a run of keys
+// is copied by boxes of one page each with TMA (rows behind k1 then come along).
 template <int D, bool IDX>
-__device__ __forceinline__ void load_rows(const CacheAttnArgs& a, Shared& sh, uint8_t* ring, int lane, int bi, int j,
-                                          int len, int k0, int k1) {
+__device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& maps, Shared& sh, uint8_t* ring, int lane,
+                                          int bi, int j, int len, int k0, int k1) {
   using R = Ring<D>;
-  constexpr int CPR = D / 16;       // 16-byte chunks of a row
-  constexpr int RPI = 32 / CPR;     // rows a warp-wide copy covers
+  constexpr int CPR = D / 16;           // 16-byte chunks of a row
+  constexpr int RPI = 32 / CPR;         // rows a warp-wide copy covers
+  constexpr int NU = IDX ? 4 : 1;       // keys (or boxes) a lane looks up
   const int64_t kvrow = (int64_t)bi * a.c.nkv + j;
-  const int plog = a.c.page_log2, pmask = (1 << plog) - 1;
+  const int plog = a.c.page_log2, pmask = (1 << plog) - 1, blog = box_log2(a.c);
   const int32_t* table = a.c.page_table + (int64_t)bi * a.c.table_stride;
   const int nst = (k1 - k0 + kStage - 1) / kStage;
   bool bad = false;
-  // key (-1: absent) of this lane's slot u (lane + 32 u) of stage s
+  // this lane's slot u of stage s: key lane + 32 u of a list; without a list,
+  // the first key of box `lane`. -1: absent.
+  auto key_of = [&](int s, int u) { return k0 + s * kStage + (IDX ? lane + 32 * u : lane << blog); };
+  auto here = [&](int s, int u) { return key_of(s, u) < k1 && (IDX || (lane << blog) < kStage); };
   auto tau_of = [&](int s, int u) {
-    const int key = k0 + s * kStage + lane + 32 * u;
-    if (key >= k1) return -1;
-    if constexpr (IDX) return __ldcg(a.kv_idx + kvrow * a.N + key);
-    return key;
+    if (!here(s, u)) return -1;
+    if constexpr (IDX) return __ldcg(a.kv_idx + kvrow * a.N + key_of(s, u));
+    return key_of(s, u);
   };
   auto page_of = [&](int tau) {
     if (tau < 0 || tau >= len) return -1;
     return __ldcg(table + (tau >> plog));
   };
   auto held = [&](int p) { return p >= 0 && p < a.c.npages; };
-  int tau[3][2], pg[2][2];
-  float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
+  int tau[3][NU], pg[2][NU];
+  float ks[NU], vs[NU];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < NU; ++u) {
+    ks[u] = vs[u] = 1.f;
 #pragma unroll
     for (int i = 0; i < 3; ++i) tau[i][u] = tau_of(i, u);
     pg[0][u] = page_of(tau[0][u]);
@@ -141,12 +204,14 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, Shared& sh, ui
       vs[u] = __ldcg(a.c.v_scale + (int64_t)pg[0][u] * a.c.nkv + j);
     }
   }
-  for (int s = 0; s < nst; ++s) {
+  int s = 0;
+  for (; s < nst; ++s) {
     // the lookups of the stages to come
-    int tau3[2], pg2[2];
-    float ks1[2] = {1.f, 1.f}, vs1[2] = {1.f, 1.f};
+    int tau3[NU], pg2[NU];
+    float ks1[NU], vs1[NU];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < NU; ++u) {
+      ks1[u] = vs1[u] = 1.f;
       tau3[u] = tau_of(s + 3, u);
       pg2[u] = page_of(tau[2][u]);
       if (held(pg[1][u])) {
@@ -163,41 +228,57 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, Shared& sh, ui
       }
       break;
     }
-    uint8_t* stage = ring + st * R::kPitch;
-    int64_t off[2];
+    const uint32_t dst = sm100::smem_u32(ring + st * R::kPitch);
+    uint32_t* ex = sh.ex[st];
+    uint32_t e[NU];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int key = k0 + s * kStage + lane + 32 * u;
-      off[u] = -1;
+    for (int u = 0; u < NU; ++u) {
       int ek = 0, ev = 0;
-      if (key < k1) {
-        if (held(pg[0][u])) {
-          off[u] = pg[0][u] * a.c.sp + (int64_t)(tau[0][u] & pmask) * a.c.sr;
-          ek = scale_exp(ks[u], &bad);
-          ev = scale_exp(vs[u], &bad);
-        } else {
-          bad = true;  // reads as zeros
-        }
+      if (held(pg[0][u])) {
+        ek = scale_exp(ks[u], &bad);
+        ev = scale_exp(vs[u], &bad);
+      } else {
+        bad |= here(s, u);  // reads as zeros
       }
-      reinterpret_cast<uint32_t*>(stage + 2 * R::kBytes)[lane + 32 * u] = (uint32_t)(ek + 64) | (uint32_t)(ev + 64) << 16;
+      e[u] = (uint32_t)(ek + 64) | (uint32_t)(ev + 64) << 16;
     }
-    const uint32_t dst = sm100::smem_u32(stage);
-    const int c = lane % CPR, r0 = lane / CPR;
-    const uint8_t* kb = a.c.k + j * a.c.sh + 16 * c;
-    const uint8_t* vb = a.c.v + j * a.c.sh + 16 * c;
+    if constexpr (IDX) {
+      int64_t off[NU];
 #pragma unroll
-    for (int i = 0; i < kStage / RPI; ++i) {
-      const int r = i * RPI + r0;
-      const int64_t o = __shfl_sync(0xffffffffu, off[i * RPI / 32], r & 31);
-      const int64_t so = o >= 0 ? o : 0;
-      const uint32_t n = o >= 0 ? 16u : 0u, at = at_chunk<D>(r, c);
-      sm100::cp_async_16(dst + at, kb + so, n);
-      sm100::cp_async_16(dst + R::kBytes + at, vb + so, n);
+      for (int u = 0; u < NU; ++u) {
+        ex[lane + 32 * u] = e[u];
+        off[u] = held(pg[0][u]) ? pg[0][u] * a.c.sp + (int64_t)(tau[0][u] & pmask) * a.c.sr : -1;
+      }
+      const int c = lane % CPR, r0 = lane / CPR;
+      const uint8_t* kb = a.c.k + j * a.c.sh + 16 * c;
+      const uint8_t* vb = a.c.v + j * a.c.sh + 16 * c;
+#pragma unroll
+      for (int i = 0; i < kStage / RPI; ++i) {
+        const int r = i * RPI + r0;
+        const int64_t o = __shfl_sync(0xffffffffu, off[i * RPI / 32], r & 31);
+        const int64_t so = o >= 0 ? o : 0;
+        const uint32_t n = o >= 0 ? 16u : 0u, at = at_chunk<D>(r, c);
+        sm100::cp_async_16(dst + at, kb + so, n);
+        sm100::cp_async_16(dst + R::kBytes + at, vb + so, n);
+      }
+      sm100::cp_async_arrive_noinc(&sh.full[st]);
+      sm100::mbar_arrive(&sh.full[st]);  // (releases the exponents)
+    } else {
+#pragma unroll
+      for (int i = 0; i < kStage / 32; ++i) ex[lane + 32 * i] = __shfl_sync(0xffffffffu, e[0], (lane + 32 * i) >> blog);
+      if (here(s, 0)) {
+        const uint32_t at = dst + ((lane << blog) * D);
+        // (a page that is not there lies out of bounds: zeros)
+        const int p = held(pg[0][0]) ? pg[0][0] : a.c.npages, r = tau[0][0] & pmask;
+        sm100::mbar_arrive_expect_tx(&sh.full[st], 2u * D << blog);
+        sm100::tma_load_4d(at, &maps.k, &sh.full[st], 0, r, j, p);
+        sm100::tma_load_4d(at + R::kBytes, &maps.v, &sh.full[st], 0, r, j, p);
+      } else {
+        sm100::mbar_arrive(&sh.full[st]);
+      }
     }
-    sm100::cp_async_arrive_noinc(&sh.full[st]);
-    sm100::mbar_arrive(&sh.full[st]);  // (releases the exponents)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < NU; ++u) {
       tau[0][u] = tau[1][u];
       tau[1][u] = tau[2][u];
       tau[2][u] = tau3[u];
@@ -207,59 +288,66 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, Shared& sh, ui
       vs[u] = vs1[u];
     }
   }
-  sm100::cp_async_commit();
-  sm100::cp_async_wait<0>();
+  if constexpr (IDX) {
+    sm100::cp_async_commit();
+    sm100::cp_async_wait<0>();
+  } else if (s < nst) {  // gave up: no copy may be in flight when the CTA goes on
+    for (int i = max(0, s - kStages); i < s; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
+  }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && sh.fault == 0) sh.fault = 6;  // QUOKA_ERR_BOUNDS
 }
 
-// grid (nsplit, nkv, b)
-template <typename T, int D, bool IDX>
-__global__ void __launch_bounds__(kThreads, 3) cache_slice_kernel(const CacheAttnArgs a) {
+// One CTA per range. RT: 8-row query tiles of a warp.
+template <typename T, int D, bool IDX, int RT>
+__global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
   constexpr int SPLIT = sizeof(T) == 2 ? 1 : 2;
-  constexpr int KS = D / 16;  // k-steps of Q K^T
-  constexpr int NT = D / 8;   // n-tiles of P V
+  constexpr int KS = D / 16;  // k-steps of K Q^T, and row tiles of O^T
   using Rg = Ring<D>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int s = blockIdx.x, j = blockIdx.y, bi = blockIdx.z;
   const int G = a.nq / a.c.nkv, R = G * a.BCP;
-  const int tiles = R <= 16 ? 1 : R <= 32 ? 2 : 4;  // (a third tile alone would leave a warp idle as well)
-  uint4* qs = reinterpret_cast<uint4*>(smem);
-  float* rowf = reinterpret_cast<float*>(smem + (size_t)tiles * SPLIT * KS * 512);
-  uint8_t* ring = smem + (size_t)tiles * SPLIT * KS * 512 + (size_t)tiles * 16 * 4;
+  const int tiles = RT == 1 || R <= 16 ? 1 : R <= 32 ? 2 : 4;  // (a third tile alone would leave a warp idle as well)
+  uint8_t* ring = sm100::align_smem_1024(smem);
+  uint32_t* qs = reinterpret_cast<uint32_t*>(ring + Rg::kTotal);
+  float* rowf = reinterpret_cast<float*>(ring + Rg::kTotal + (size_t)tiles * RT * KS * 32 * 8 * SPLIT);
   pdl_trigger();
   clear_status(a.status);  // (the faults of this kernel are latched by the next)
-
-  const int64_t kvrow = (int64_t)bi * a.c.nkv + j;
-  const int want = __ldcg(a.c.seq_len + bi), len = min(max(want, 0), a.max_len);
-  const int n = IDX ? min(max(__ldcg(a.kv_count + kvrow), 0), a.N) : len;
-  const int per = ((n + a.nsplit * kStep - 1) / (a.nsplit * kStep)) * kStep;  // keys of a range
-  const int k0 = min(n, s * per), k1 = min(n, k0 + per);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      sm100::mbar_init(&sh.full[i], 64);
+      sm100::mbar_init(&sh.full[i], IDX ? 64 : 32);
       sm100::mbar_init(&sh.empty[i], 4);
     }
-    sh.abort = 0;
-    sh.fault = want != len ? 6 : 0;  // QUOKA_ERR_BOUNDS
-    sh.site = 0;
+    sh.abort = sh.fault = sh.site = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 4) find_range<IDX>(a, sh, blockIdx.x, lane);
   __syncthreads();
+  const int row = sh.row, k0 = sh.k0, k1 = sh.k1;
+  if (row < 0) return;
+  const int bi = row / a.c.nkv, j = row % a.c.nkv;
 
-  float o[NT][4];
+  float o[RT][KS][4];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int i = 0; i < KS; ++i) o[rt][i][0] = o[rt][i][1] = o[rt][i][2] = o[rt][i][3] = 0.f;
+  float m[RT][2], l[RT][2];  // query rows 2 t, 2 t + 1 of each tile
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt][0] = m[rt][1] = -INFINITY;
+    l[rt][0] = l[rt][1] = 0.f;
+  }
   const int kgroups = 4 / tiles, tile = warp % tiles, kg = warp / tiles;  // (computing warps)
 
   if (warp == 4) {
-    load_rows<D, IDX>(a, sh, ring, lane, bi, j, len, k0, k1);
+    const int want = __ldcg(a.c.seq_len + bi), len = min(max(want, 0), a.max_len);
+    if (want != len && lane == 0) sh.fault = 6;  // QUOKA_ERR_BOUNDS
+    load_rows<D, IDX>(a, maps, sh, ring, lane, bi, j, len, k0, k1);
   } else {
     // ---- query rows: row r is head j G + r / BCP, chunk position r % BCP; a
     // warp takes a row at a time
-    for (int r = warp; r < tiles * 16; r += 4) {
+    for (int r = warp; r < tiles * RT * 8; r += 4) {
       float x[D / 32];
       float top = 0.f;
       const T* q = static_cast<const T*>(a.Q.data) + bi * a.Q.sb + (int64_t)(j * G + r / a.BCP) * a.Q.sh +
@@ -280,144 +368,170 @@ __global__ void __launch_bounds__(kThreads, 3) cache_slice_kernel(const CacheAtt
       for (int i = 0; i < D / 32; i += 2) {
         const int d = D / 32 * lane + i;
         // column d belongs to chunk d / 16 = t + 4 * (ks / 4), word (d % 16) / 4 = ks % 4 of it
-        const int ch = d >> 4, ks = 4 * (ch >> 2) + ((d & 15) >> 2);
-        const int reg = ((d >> 1) & 1) * 2 + ((r & 15) >> 3);
-        uint32_t* dst =
-            reinterpret_cast<uint32_t*>(qs + (((r >> 4) * SPLIT) * KS + ks) * 32 + (r & 7) * 4 + (ch & 3)) + reg;
+        const int ch = d >> 4, ks = 4 * (ch >> 2) + ((d & 15) >> 2), reg = (d >> 1) & 1;
+        uint32_t* dst = qs + (((r >> 3) * KS + ks) * 32 + (r & 7) * 4 + (ch & 3)) * (2 * SPLIT) + reg;
         const uint32_t hi = pack_h2(x[i] * f, x[i + 1] * f);
         *dst = hi;
-        if constexpr (SPLIT == 2) dst[KS * 32 * 4] = rest_h2(x[i] * f, x[i + 1] * f, hi);
+        if constexpr (SPLIT == 2) dst[2] = rest_h2(x[i] * f, x[i + 1] * f, hi);
       }
     }
     sm100::named_barrier_sync(1, 128);
-    const float f0 = rowf[tile * 16 + g], f1 = rowf[tile * 16 + g + 8];
-    const uint4* qt = qs + (size_t)tile * SPLIT * KS * 32 + lane;
-    const int gk = g ^ ((g & 1) << 2);               // this lane's key of a step (and gk + 8)
-    const int v0 = 2 * t4, v1 = (2 * t4 + 1) ^ 4;    // its keys of P V: v0, v1, v0 + 8, v1 + 8
+    float f[RT][2];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      f[rt][0] = rowf[(tile * RT + rt) * 8 + 2 * t4];
+      f[rt][1] = rowf[(tile * RT + rt) * 8 + 2 * t4 + 1];
+    }
+    const uint32_t* qt = qs + ((size_t)tile * RT * KS * 32 + lane) * (2 * SPLIT);
+    const int gk = g ^ ((g & 1) << 2);             // this lane's key of an operand tile (and gk + 8)
+    const int v0 = 2 * t4, v1 = (2 * t4 + 1) ^ 4;  // its keys of V^T P^T: v0, v1, v0 + 8, v1 + 8
 
-    auto compute = [&](const uint8_t* stage, int row, int left) {
-      const uint8_t* kr = stage + row * D;
+    auto compute = [&](const uint8_t* stage, const uint32_t* exs, int row0, int left) {
+      const uint8_t* kr = stage + row0 * D;
       const uint8_t* vr = kr + Rg::kBytes;
-      const uint32_t* ex = reinterpret_cast<const uint32_t*>(stage + 2 * Rg::kBytes) + row;
-      float c[2][4];
+      const uint32_t* ex = exs + row0;
+      // ---- S^T: c[y][rt]: keys gk, gk + 8 of tile y by rows 2 t, 2 t + 1
+      float c[2][RT][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.f;
-      uint32_t kw[2][KS];
+      for (int y = 0; y < 2; ++y)
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+        for (int rt = 0; rt < RT; ++rt) c[y][rt][0] = c[y][rt][1] = c[y][rt][2] = c[y][rt][3] = 0.f;
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          const uint4 w = *reinterpret_cast<const uint4*>(kr + at_chunk<D>(gk + 8 * nt, t4 + 4 * h));
-          kw[nt][4 * h] = w.x;
-          kw[nt][4 * h + 1] = w.y;
-          kw[nt][4 * h + 2] = w.z;
-          kw[nt][4 * h + 3] = w.w;
-        }
-      uint32_t vw[4][D / 32];
+      for (int h = 0; h < D / 64; ++h) {
+        uint4 kw[2][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = (i & 1 ? v1 : v0) + 8 * (i >> 1);
-        if constexpr (D == 128) {
-          const uint4 w = *reinterpret_cast<const uint4*>(vr + at_chunk<D>(r, g));
-          vw[i][0] = w.x;
-          vw[i][1] = w.y;
-          vw[i][2] = w.z;
-          vw[i][3] = w.w;
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(vr + at_chunk<D>(r, g >> 1) + 8 * (g & 1));
-          vw[i][0] = w.x;
-          vw[i][1] = w.y;
-        }
-      }
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const uint4 q0 = qt[ks * 32];
-        const uint32_t qa[4] = {q0.x, q0.y, q0.z, q0.w};
-        uint32_t qb[4];
-        if constexpr (SPLIT == 2) {
-          const uint4 q1 = qt[(KS + ks) * 32];
-          qb[0] = q1.x; qb[1] = q1.y; qb[2] = q1.z; qb[3] = q1.w;
-        }
+          for (int u = 0; u < 2; ++u)
+            kw[y][u] = *reinterpret_cast<const uint4*>(kr + at_chunk<D>(16 * y + gk + 8 * u, t4 + 4 * h));
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const uint32_t w = kw[nt][ks];
-          const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)w), b1 = e4m3x2_to_f16x2((uint16_t)(w >> 16));
-          mma_f16(c[nt], qa, b0, b1);
-          if constexpr (SPLIT == 2) mma_f16(c[nt], qb, b0, b1);
+        for (int w = 0; w < 4; ++w) {
+          uint32_t qb[RT][2 * SPLIT];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            const uint32_t* q = qt + (rt * KS + 4 * h + w) * 32 * (2 * SPLIT);
+            if constexpr (SPLIT == 2) {
+              const uint4 x = *reinterpret_cast<const uint4*>(q);
+              qb[rt][0] = x.x; qb[rt][1] = x.y; qb[rt][2] = x.z; qb[rt][3] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(q);
+              qb[rt][0] = x.x; qb[rt][1] = x.y;
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t w0 = reinterpret_cast<const uint32_t*>(&kw[y][0])[w];
+            const uint32_t w1 = reinterpret_cast<const uint32_t*>(&kw[y][1])[w];
+            const uint32_t ka[4] = {e4m3x2_to_f16x2((uint16_t)w0), e4m3x2_to_f16x2((uint16_t)w1),
+                                    e4m3x2_to_f16x2((uint16_t)(w0 >> 16)), e4m3x2_to_f16x2((uint16_t)(w1 >> 16))};
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              mma_f16(c[y][rt], ka, qb[rt][0], qb[rt][1]);
+              if constexpr (SPLIT == 2) mma_f16(c[y][rt], ka, qb[rt][2], qb[rt][3]);
+            }
+          }
         }
       }
-      // scores in log2 units, with the value scale's exponent added
-      float x0 = -INFINITY, x1 = -INFINITY;
-      float inv[4];  // 2^-ev of the lane's four keys
+      // ---- scores in log2 units, with the value scale's exponent added
+      float x[RT][2], inv[2][2];  // row maxima; 2^-ev of the lane's keys
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = (i & 1 ? v1 : v0) + 8 * (i >> 1);
-        const uint32_t e = ex[key];
-        const float ks = exp2i((int)(e & 0xFFFFu) - 64);
-        const int ev = (int)(e >> 16) - 64;
-        inv[i] = exp2i(-ev);
-        const bool there = key < left;
-        float& a0 = c[i >> 1][i & 1];
-        float& a1 = c[i >> 1][2 + (i & 1)];
-        a0 = there ? fmaf(a0, f0 * ks, (float)ev) : -INFINITY;
-        a1 = there ? fmaf(a1, f1 * ks, (float)ev) : -INFINITY;
-        x0 = fmaxf(x0, a0);
-        x1 = fmaxf(x1, a1);
-      }
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-      if (__any_sync(0xffffffffu, x0 > m0 + kLazy || x1 > m1 + kLazy)) {
-        const float n0 = fmaxf(m0, x0 - kHead), n1 = fmaxf(m1, x1 - kHead);
-        const float r0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0), r1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= r0;
-        l1 *= r1;
+      for (int rt = 0; rt < RT; ++rt) x[rt][0] = x[rt][1] = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          o[i][0] *= r0;
-          o[i][1] *= r0;
-          o[i][2] *= r1;
-          o[i][3] *= r1;
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = 16 * y + gk + 8 * u;
+          const uint32_t e = ex[key];
+          const float ks = exp2i((int)(e & 0xFFFFu) - 64);
+          const int ev = (int)(e >> 16) - 64;
+          inv[y][u] = exp2i(-ev);
+          const bool there = key < left;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& s_ = c[y][rt][2 * u + i];
+              s_ = there ? fmaf(s_, f[rt][i] * ks, (float)ev) : -INFINITY;
+              x[rt][i] = fmaxf(x[rt][i], s_);
+            }
         }
-      }
-      const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-      float p[2][4];
+      bool rise = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p0 = sm100::ex2(c[i >> 1][i & 1] - b0), p1 = sm100::ex2(c[i >> 1][2 + (i & 1)] - b1);
-        l0 = fmaf(p0, inv[i], l0);
-        l1 = fmaf(p1, inv[i], l1);
-        p[i >> 1][i & 1] = p0;
-        p[i >> 1][2 + (i & 1)] = p1;
-      }
-      uint32_t pa[4], pb[4];
-      pa[0] = pack_h2(p[0][0], p[0][1]);
-      pa[1] = pack_h2(p[0][2], p[0][3]);
-      pa[2] = pack_h2(p[1][0], p[1][1]);
-      pa[3] = pack_h2(p[1][2], p[1][3]);
-      if constexpr (SPLIT == 2) {
-        pb[0] = rest_h2(p[0][0], p[0][1], pa[0]);
-        pb[1] = rest_h2(p[0][2], p[0][3], pa[1]);
-        pb[2] = rest_h2(p[1][0], p[1][1], pa[2]);
-        pb[3] = rest_h2(p[1][2], p[1][3], pa[3]);
-      }
-      // O += P V: n-tile 4 w + u multiplies byte u of every lane's word w
+      for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        uint32_t lo[2], hi[2];
-        lo[0] = __byte_perm(vw[0][w], vw[1][w], 0x5140);
-        lo[1] = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-        hi[0] = __byte_perm(vw[2][w], vw[3][w], 0x5140);
-        hi[1] = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const uint32_t b0_ = e4m3x2_to_f16x2((uint16_t)(lo[u >> 1] >> (16 * (u & 1))));
-          const uint32_t b1_ = e4m3x2_to_f16x2((uint16_t)(hi[u >> 1] >> (16 * (u & 1))));
-          mma_f16(o[4 * w + u], pa, b0_, b1_);
-          if constexpr (SPLIT == 2) mma_f16(o[4 * w + u], pb, b0_, b1_);
+          for (int d = 4; d < 32; d <<= 1) x[rt][i] = fmaxf(x[rt][i], __shfl_xor_sync(0xffffffffu, x[rt][i], d));
+          rise = rise || x[rt][i] > m[rt][i] + kLazy;
+        }
+      if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float n = fmaxf(m[rt][i], x[rt][i] - kHead);
+            const float r = m[rt][i] == -INFINITY ? 0.f : exp2f(m[rt][i] - n);
+            m[rt][i] = n;
+            l[rt][i] *= r;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              o[rt][k][i] *= r;
+              o[rt][k][2 + i] *= r;
+            }
+          }
+      }
+      // ---- P^T as the second product's operand
+      uint32_t pb[2][RT][2 * SPLIT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float b0 = m[rt][0] == -INFINITY ? 0.f : m[rt][0], b1 = m[rt][1] == -INFINITY ? 0.f : m[rt][1];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float p0 = sm100::ex2(c[y][rt][2 * u] - b0), p1 = sm100::ex2(c[y][rt][2 * u + 1] - b1);
+            l[rt][0] = fmaf(p0, inv[y][u], l[rt][0]);
+            l[rt][1] = fmaf(p1, inv[y][u], l[rt][1]);
+            const uint32_t hi = pack_h2(p0, p1);
+            pb[y][rt][u] = transpose_8x8(hi);
+            if constexpr (SPLIT == 2) pb[y][rt][2 + u] = transpose_8x8(rest_h2(p0, p1, hi));
+          }
+      }
+      // ---- O^T += V^T P^T: row tile i holds columns 2 i, 2 i + 1 of every lane's chunk
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t vw[4][D / 32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * y + (i & 1 ? v1 : v0) + 8 * (i >> 1);
+          if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vr + at_chunk<D>(r, g));
+            vw[i][0] = w.x;
+            vw[i][1] = w.y;
+            vw[i][2] = w.z;
+            vw[i][3] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(vr + at_chunk<D>(r, g >> 1) + 8 * (g & 1));
+            vw[i][0] = w.x;
+            vw[i][1] = w.y;
+          }
+          if (!IDX && left < kStep && r >= left) {  // (a row behind the range may hold a NaN)
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) vw[i][w] = 0u;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t sel = k & 1 ? 0x7362 : 0x5140;  // bytes 2 (k % 2), 2 (k % 2) + 1 of both keys
+          const uint32_t lo = __byte_perm(vw[0][k >> 1], vw[1][k >> 1], sel);
+          const uint32_t hi = __byte_perm(vw[2][k >> 1], vw[3][k >> 1], sel);
+          const uint32_t va[4] = {e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
+                                  e4m3x2_to_f16x2((uint16_t)hi), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            mma_f16(o[rt][k], va, pb[y][rt][0], pb[y][rt][1]);
+            if constexpr (SPLIT == 2) mma_f16(o[rt][k], va, pb[y][rt][2], pb[y][rt][3]);
+          }
         }
       }
     };
@@ -434,71 +548,65 @@ __global__ void __launch_bounds__(kThreads, 3) cache_slice_kernel(const CacheAtt
         break;
       }
       const int left = k1 - k0 - i * kStage;
-      for (int row = kg * kStep; row < min(left, kStage); row += kgroups * kStep)
-        compute(ring + st * Rg::kPitch, row, left - row);
+      for (int r = kg * kStep; r < min(left, kStage); r += kgroups * kStep)
+        compute(ring + st * Rg::kPitch, sh.ex[st], r, left - r);
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&sh.empty[st]);
     }
   }
 
   // ---- join the warps of each query tile
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-  l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-  l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
   __syncthreads();  // the ring is no longer read, and no copy into it is in flight
-  float* os = reinterpret_cast<float*>(ring);  // [4 warps][16][D]
-  float* ml = os + 4 * 16 * D;                 // [4][16][2]
+  constexpr int TR = 8 * RT;                   // rows of a warp's tile
+  float* os = reinterpret_cast<float*>(ring);  // [4 warps][TR][D]
+  float* ml = os + 4 * TR * D;                 // [4][TR][2]
   if (warp < 4) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = g + 8 * hf;
-      if (t4 == 0) {
-        ml[(warp * 16 + r) * 2] = hf ? m1 : m0;
-        ml[(warp * 16 + r) * 2 + 1] = hf ? l1 : l0;
-      }
-      if (tile * 16 + r < R) {
-        // n-tile i of lane (g, t): columns D/8 * 2t + i and D/8 * (2t + 1) + i
-        float4* row = reinterpret_cast<float4*>(os + (warp * 16 + r) * D + D / 4 * t4);
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int i = 0; i < NT; i += 4) {
-          row[i / 4] = make_float4(o[i][2 * hf], o[i + 1][2 * hf], o[i + 2][2 * hf], o[i + 3][2 * hf]);
-          row[D / 32 + i / 4] =
-              make_float4(o[i][2 * hf + 1], o[i + 1][2 * hf + 1], o[i + 2][2 * hf + 1], o[i + 3][2 * hf + 1]);
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[rt][i] += __shfl_xor_sync(0xffffffffu, l[rt][i], d);
+        const int r = 8 * rt + 2 * t4 + i;
+        if (g == 0) {
+          ml[(warp * TR + r) * 2] = m[rt][i];
+          ml[(warp * TR + r) * 2 + 1] = l[rt][i];
+        }
+        if (tile * TR + r < R) {  // columns [D / 8 * g, + D / 8)
+          float4* dst = reinterpret_cast<float4*>(os + (warp * TR + r) * D + D / 8 * g);
+#pragma unroll
+          for (int k = 0; k < KS; k += 2)
+            dst[k / 2] = make_float4(o[rt][k][i], o[rt][k][2 + i], o[rt][k + 1][i], o[rt][k + 1][2 + i]);
         }
       }
-    }
   }
   __syncthreads();
-  const int64_t rows = (int64_t)a.b * a.nq * a.BCP;
   for (int e = tid; e < R * (D / 4); e += kThreads) {
     const int r = e / (D / 4), c4 = e % (D / 4);
-    const int tl = r >> 4, rr = r & 15;
+    const int tl = r / TR, rr = r % TR;
     float M = -INFINITY;
-    for (int k = 0; k < kgroups; ++k) M = fmaxf(M, ml[((k * tiles + tl) * 16 + rr) * 2]);
+    for (int k = 0; k < kgroups; ++k) M = fmaxf(M, ml[((k * tiles + tl) * TR + rr) * 2]);
     float L = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < kgroups; ++k) {
       const int w = k * tiles + tl;
-      const float lw = ml[(w * 16 + rr) * 2 + 1];
+      const float lw = ml[(w * TR + rr) * 2 + 1];
       if (lw == 0.f) continue;  // the warp saw no key (not so for NaN scores: they come through)
-      const float f = exp2f(ml[(w * 16 + rr) * 2] - M);
-      const float4 y = *reinterpret_cast<const float4*>(os + (w * 16 + rr) * D + 4 * c4);
-      L = fmaf(f, lw, L);
-      x.x = fmaf(f, y.x, x.x);
-      x.y = fmaf(f, y.y, x.y);
-      x.z = fmaf(f, y.z, x.z);
-      x.w = fmaf(f, y.w, x.w);
+      const float fw = exp2f(ml[(w * TR + rr) * 2] - M);
+      const float4 y = *reinterpret_cast<const float4*>(os + (w * TR + rr) * D + 4 * c4);
+      L = fmaf(fw, lw, L);
+      x.x = fmaf(fw, y.x, x.x);
+      x.y = fmaf(fw, y.y, x.y);
+      x.z = fmaf(fw, y.z, x.z);
+      x.w = fmaf(fw, y.w, x.w);
     }
     const float inv = L != 0.f ? 1.f / L : 0.f;
-    const int h = j * G + r / a.BCP, t = r % a.BCP;
-    const int64_t row = ((int64_t)bi * a.nq + h) * a.BCP + t;
-    *reinterpret_cast<float4*>(a.O_parts + ((int64_t)s * rows + row) * D + 4 * c4) =
-        make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    const int64_t at = (int64_t)blockIdx.x * R + r;
+    *reinterpret_cast<float4*>(a.O_parts + at * D + 4 * c4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     // log2 of the range's partition function (-inf: no key)
-    if (c4 == 0) a.lse_parts[(int64_t)s * rows + row] = L != 0.f ? M + log2f(L) : -INFINITY;
+    if (c4 == 0) a.lse_parts[at] = L != 0.f ? M + log2f(L) : -INFINITY;
   }
-  if (tid == 0) a.faults[kvrow * a.nsplit + s] = sh.fault | sh.site << 8;
+  if (tid == 0) a.faults[blockIdx.x] = sh.fault | sh.site << 8;
 }
 
 // Joins the ranges of one query row, adds the chunk's own keys s <= t, and
@@ -527,10 +635,10 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
   constexpr int C4 = D / 4, kGroups = kMergeThreads / C4;
   __shared__ float4 acc[kGroups][C4];
   __shared__ float sc[kCacheMaxRows];
-  const int64_t row = blockIdx.x, rows = (int64_t)a.b * a.nq * a.BCP;
+  const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c4 = tid % C4, grp = tid / C4;
   const int t = (int)(row % a.BCP), h = (int)(row / a.BCP % a.nq), bi = (int)(row / a.BCP / a.nq);
-  const int j = h / (a.nq / a.c.nkv);
+  const int G = a.nq / a.c.nkv, j = h / G, R = G * a.BCP;
   const int nc = a.chunk ? t + 1 : 0;
   const T* vc = static_cast<const T*>(a.Vc.data) + bi * a.Vc.sb + j * a.Vc.sh;
   if (nc > 0) {  // (inputs of the call: read before the partials are waited for)
@@ -561,9 +669,22 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     __syncthreads();
   }
   pdl_wait();
-  const float* lp = a.lse_parts + row;
-  float M = -INFINITY;
-  for (int s = lane; s < a.nsplit; s += 32) M = fmaxf(M, __ldcg(lp + (int64_t)s * rows));
+  const int2 parts = __ldcg(a.row_parts + bi * a.c.nkv + j);  // first range and their number
+  const int64_t at = (int64_t)parts.x * R + (h - j * G) * a.BCP + t;
+  const float* lp = a.lse_parts + at;
+  const float* op = a.O_parts + at * D;
+  // the first 32 ranges' outputs and sums are fetched together
+  constexpr int kOwn = 32 / kGroups;
+  float4 own[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int s = i * kGroups + grp;
+    own[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s < parts.y) own[i] = __ldcg(reinterpret_cast<const float4*>(op + (int64_t)s * R * D) + c4);
+  }
+  const float x0 = lane < parts.y ? __ldcg(lp + (int64_t)lane * R) : -INFINITY;
+  float M = x0;
+  for (int s = 32 + lane; s < parts.y; s += 32) M = fmaxf(M, __ldcg(lp + (int64_t)s * R));
   for (int k = lane; k < nc; k += 32) M = fmaxf(M, sc[k]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -576,16 +697,18 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     o.z = fmaf(w, x.z, o.z);
     o.w = fmaf(w, x.w, o.w);
   };
-  for (int s0 = 0; s0 < a.nsplit; s0 += 32) {
-    // (a range without keys has a weight of 0 and a zero output)
-    const float w = s0 + lane < a.nsplit ? exp2f(__ldcg(lp + (int64_t)(s0 + lane) * rows) - ref) : 0.f;
+  // (a range without keys has a weight of 0 and a zero output)
+  for (int s0 = 0; s0 < parts.y; s0 += 32) {
+    const float x = s0 == 0 ? x0 : s0 + lane < parts.y ? __ldcg(lp + (int64_t)(s0 + lane) * R) : -INFINITY;
+    const float w = exp2f(x - ref);
     L += w;
 #pragma unroll
-    for (int i = 0; i < 32 / kGroups; ++i) {
+    for (int i = 0; i < kOwn; ++i) {
       const int s = i * kGroups + grp;
       const float ws = __shfl_sync(0xffffffffu, w, s);
-      if (s0 + s < a.nsplit)
-        add(ws, __ldcg(reinterpret_cast<const float4*>(a.O_parts + ((int64_t)(s0 + s) * rows + row) * D) + c4));
+      if (s0 > 0 && s0 + s < parts.y)
+        own[i] = __ldcg(reinterpret_cast<const float4*>(op + (int64_t)(s0 + s) * R * D) + c4);
+      if (s0 + s < parts.y) add(ws, own[i]);
     }
   }
   for (int k = lane; k < nc; k += 32) L += exp2f(sc[k] - ref);
@@ -601,9 +724,8 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     if (a.lse != nullptr && tid == 0) a.lse[row] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
   }
   if (warp == 1) {
-    const int* f = a.faults + ((int64_t)bi * a.c.nkv + j) * a.nsplit;
-    for (int s = lane; s < a.nsplit; s += 32) {
-      const int x = __ldcg(f + s);
+    for (int s = lane; s < parts.y; s += 32) {
+      const int x = __ldcg(a.faults + parts.x + s);
       if (x != 0) {
         latch_status(a.status, x & 255);
         if (x >> 8) latch_where(a.status, x >> 8);
@@ -612,54 +734,63 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int RT>
 cudaError_t launch_typed(const CacheAttnArgs& a, cudaStream_t stream) {
   const int R = (a.nq / a.c.nkv) * a.BCP;
-  const int tiles = R <= 16 ? 1 : R <= 32 ? 2 : 4;
-  const size_t smem = smem_bytes<D, sizeof(T) == 2 ? 1 : 2>(tiles);
-  auto* kern = a.kv_idx != nullptr ? cache_slice_kernel<T, D, true> : cache_slice_kernel<T, D, false>;
+  const int tiles8 = RT == 1 ? 1 : R <= 16 ? 2 : R <= 32 ? 4 : 8;
+  const size_t smem = smem_bytes<D, sizeof(T) == 2 ? 1 : 2>(tiles8);
+  auto* kern = a.kv_idx != nullptr ? cache_slice_kernel<T, D, true, RT> : cache_slice_kernel<T, D, false, RT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  Maps maps = {};
+  const int page = 1 << a.c.page_log2, box = 1 << box_log2(a.c);
+  if (a.kv_idx == nullptr && (!encode_codes_4d(&maps.k, a.c.k, D, page, a.c.nkv, a.c.npages, a.c.sr, a.c.sh, a.c.sp, box) ||
+                              !encode_codes_4d(&maps.v, a.c.v, D, page, a.c.nkv, a.c.npages, a.c.sr, a.c.sh, a.c.sp, box)))
+    return cudaErrorNotSupported;
+  cudaLaunchConfig_t cfg = {};  // (clears the status words: behind everything before)
+  cfg.gridDim = dim3(a.ranges);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  e = cudaLaunchKernelEx(&cfg, kern, maps, a);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.nsplit, a.c.nkv, a.b);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 0;  // (clears the status words: behind everything before)
-  e = cudaLaunchKernelEx(&cfg, kern, a);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t mc = {};
   mc.gridDim = dim3((unsigned)((int64_t)a.b * a.nq * a.BCP));
   mc.blockDim = dim3(kMergeThreads);
   mc.stream = stream;
   mc.attrs = attr;
-  mc.numAttrs = 1;  // waits for the slices inside
+  mc.numAttrs = 1;  // waits for the ranges inside
   return cudaLaunchKernelEx(&mc, cache_merge_kernel<T, D>, a);
 }
 
-// One round of CTAs at three an SM, a range being at least 128 keys. (Decode
-// steps of 32 sequences of up to 8192 keys, d = 128: 79.9 us with 296 or 444
-// CTAs, 81.9 with 888, 86.0 with 1776; one sequence of 4096 listed keys the
-// same with 128 and 256 keys at least, blocks of 1500 keys 2 us slower with 256.)
-constexpr int kSplitCTAs = 444, kSplitKeys = 128;
+// Ranges to cut all keys into, before rounding up row by row.
+int64_t range_target(int64_t rows) { return std::max<int64_t>(kSplitCTAs - rows / 2, kSplitCTAs / 2); }
 
 }  // namespace
 
-int cache_attn_splits(int64_t heads, int N) {
-  const int64_t want = (kSplitCTAs + heads - 1) / heads, most = (N + kSplitKeys - 1) / kSplitKeys;
-  return (int)(want < 1 ? 1 : want < most ? want : most < 1 ? 1 : most);
+int64_t cache_attn_ranges(int64_t rows, int N) {
+  // sum over rows of max(1, ceil(n / most)) <= target + rows, and <= rows * ceil(N / kSplitKeys)
+  return std::min<int64_t>(range_target(rows) + rows, rows * std::max(1, (N + kSplitKeys - 1) / kSplitKeys));
 }
 
-cudaError_t launch_cache_attn(bool is_bf16, int d, const CacheAttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_cache_attn(bool is_bf16, int d, const CacheAttnArgs& args, cudaStream_t stream) {
+  CacheAttnArgs a = args;
   const int R = (a.nq / a.c.nkv) * a.BCP;
-  if (R < 1 || R > kCacheMaxRows || a.nsplit < 1) return cudaErrorInvalidValue;
-  if (d == 128) return is_bf16 ? launch_typed<bf16, 128>(a, stream) : launch_typed<float, 128>(a, stream);
-  if (d == 64) return is_bf16 ? launch_typed<bf16, 64>(a, stream) : launch_typed<float, 64>(a, stream);
-  return cudaErrorNotSupported;
+  const int64_t rows = (int64_t)a.b * a.c.nkv, ranges = cache_attn_ranges(rows, a.N);
+  if (R < 1 || R > kCacheMaxRows) return cudaErrorInvalidValue;
+  if (ranges > 0x7FFFFFFF || (int64_t)a.b * a.nq * a.BCP > 0x7FFFFFFF) return cudaErrorNotSupported;
+  a.target = (int)range_target(rows);
+  a.ranges = (int)ranges;
+  if (d != 64 && d != 128) return cudaErrorNotSupported;
+  if (R <= 8) {
+    if (d == 128) return is_bf16 ? launch_typed<bf16, 128, 1>(a, stream) : launch_typed<float, 128, 1>(a, stream);
+    return is_bf16 ? launch_typed<bf16, 64, 1>(a, stream) : launch_typed<float, 64, 1>(a, stream);
+  }
+  if (d == 128) return is_bf16 ? launch_typed<bf16, 128, 2>(a, stream) : launch_typed<float, 128, 2>(a, stream);
+  return is_bf16 ? launch_typed<bf16, 64, 2>(a, stream) : launch_typed<float, 64, 2>(a, stream);
 }
 
 }  // namespace quoka

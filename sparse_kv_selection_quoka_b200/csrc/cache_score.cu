@@ -13,8 +13,8 @@
 //
 // Work split. The keys of a (sequence, KV head) are cut into nsplit contiguous
 // ranges, one CTA each: a loader warp copies 128 code rows at a time into a
-// ring of stages (cp.async, zeros for a page that is not there; the page
-// table is read a stage ahead), four warps take 32 of them each. Keys are the
+// ring of stages (TMA, boxes of up to 64 rows of one page; the page table is
+// read two stages ahead), four warps take 32 of them each. Keys are the
 // rows of the product and group means its 8 columns: up to 4 group means put
 // hi and lo side by side into one tile, kept in registers, and a 16 x 16 step
 // costs three products; more go through shared memory, 64 at a time. The
@@ -25,6 +25,7 @@
 // Bound by the codes' bytes for few group means.
 #include "cache.cuh"
 #include "sm100.cuh"
+#include "tmap.cuh"
 
 namespace quoka {
 
@@ -39,20 +40,6 @@ constexpr int kQueries = 64;      // group means in shared memory at a time
 constexpr int kPacked = 4;        // up to this many fit one tile as hi and lo
 constexpr float kQScale = 4096.f;
 
-__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Byte of chunk c (16 bytes) of row r of a stage.
-template <int D>
-__device__ __forceinline__ int at_chunk(int r, int c) {
-  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
-}
-
 struct Shared {
   uint64_t full[kStages], empty[kStages];
   int abort;
@@ -64,27 +51,25 @@ struct Shared {
 template <int D>
 constexpr size_t smem_bytes(int NQ) {
   const int nt = NQ <= kPacked ? 1 : ((NQ < kQueries ? NQ : kQueries) + 7) / 8;
-  return (size_t)kStages * kStage * D + (size_t)nt * (D / 16) * 512;
+  return (size_t)kStages * kStage * D + (size_t)nt * (D / 16) * 512 + 1024;
 }
 
-// The loader warp: code rows [k0, k1) of the (sequence, head), `passes` times.
+// The loader warp: code rows [k0, k1) of the (sequence, head), `passes` times, by
+// boxes of one page each (rows behind k1 come along, and are not used).
 template <int D>
-__device__ __forceinline__ void load_rows(const CacheScoreArgs& a, Shared& sh, uint8_t* ring, int lane, int bi, int j,
-                                          int k0, int k1, int passes) {
-  constexpr int CPR = D / 16, RPI = 32 / CPR;  // chunks of a row, rows of a warp-wide copy
-  const int plog = a.c.page_log2, pmask = (1 << plog) - 1;
+__device__ __forceinline__ void load_rows(const CacheScoreArgs& a, const CUtensorMap& map, Shared& sh, uint8_t* ring,
+                                          int lane, int bi, int j, int k0, int k1, int passes) {
+  const int plog = a.c.page_log2, pmask = (1 << plog) - 1, blog = box_log2(a.c);
   const int32_t* table = a.c.page_table + (int64_t)bi * a.c.table_stride;
   const int nst = (k1 - k0 + kStage - 1) / kStage, total = nst * passes;
   bool bad = false;
-  // the page of this lane's 16 keys (lane % 8) of the it-th stage
-  auto page_of = [&](int it) {
-    const int key = k0 + it % nst * kStage + 16 * (lane & 7);
-    return it < total && key < k1 ? __ldcg(table + (key >> plog)) : -1;
-  };
-  int p0 = page_of(0), p1 = page_of(1);
-  for (int it = 0; it < total; ++it) {
-    const int p2 = page_of(it + 2);
-    const int st = it % kStages, base = k0 + it % nst * kStage;
+  // this lane's box of the it-th stage: its first key, whether there is one, its page
+  auto key_of = [&](int it) { return k0 + it % nst * kStage + (lane << blog); };
+  auto here = [&](int it) { return it < total && (lane << blog) < kStage && key_of(it) < k1; };
+  auto page_of = [&](int it) { return here(it) ? __ldcg(table + (key_of(it) >> plog)) : -1; };
+  int p0 = page_of(0), p1 = page_of(1), it = 0;
+  for (; it < total; ++it) {
+    const int p2 = page_of(it + 2), st = it % kStages;
     if (it >= kStages && !__all_sync(0xffffffffu, sm100::mbar_wait(&sh.empty[st], (it / kStages - 1) & 1, &sh.abort))) {
       if (lane == 0) {
         sh.abort = 1;
@@ -93,37 +78,31 @@ __device__ __forceinline__ void load_rows(const CacheScoreArgs& a, Shared& sh, u
       }
       break;
     }
-    const bool held = p0 >= 0 && p0 < a.c.npages;
-    bad |= !held && base + 16 * (lane & 7) < k1;
-    const int pg = held ? p0 : -1;
-    const uint32_t dst = sm100::smem_u32(ring + st * kStage * D);
-    const int c = lane % CPR, r0 = lane / CPR;
-    const uint8_t* kb = a.c.k + j * a.c.sh + 16 * c;
-#pragma unroll
-    for (int i = 0; i < kStage / RPI; ++i) {
-      const int r = i * RPI + r0;
-      const int p = __shfl_sync(0xffffffffu, pg, i * RPI / 16);  // (a copy's rows lie in one group of 16)
-      const bool there = p >= 0 && base + r < k1;
-      const int64_t off = there ? p * a.c.sp + (int64_t)((base + r) & pmask) * a.c.sr : 0;
-      sm100::cp_async_16(dst + at_chunk<D>(r, c), kb + off, there ? 16u : 0u);
+    if (here(it)) {
+      const bool held = p0 >= 0 && p0 < a.c.npages;
+      bad |= !held;  // (a page that is not there lies out of bounds: zeros)
+      sm100::mbar_arrive_expect_tx(&sh.full[st], (uint32_t)D << blog);
+      sm100::tma_load_4d(sm100::smem_u32(ring + st * kStage * D) + (lane << blog) * D, &map, &sh.full[st], 0,
+                         key_of(it) & pmask, j, held ? p0 : a.c.npages);
+    } else {
+      sm100::mbar_arrive(&sh.full[st]);
     }
-    sm100::cp_async_arrive_noinc(&sh.full[st]);
     p0 = p1;
     p1 = p2;
   }
-  sm100::cp_async_commit();
-  sm100::cp_async_wait<0>();
+  if (it < total)  // gave up: no copy may be in flight when the CTA ends
+    for (int i = max(0, it - kStages); i < it; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
   if (bad) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
 }
 
 // grid (nsplit, nkv, b). PACKED: NQ <= kPacked.
 template <int D, bool PACKED>
-__global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const CacheScoreArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const __grid_constant__ CUtensorMap map, const CacheScoreArgs a) {
   constexpr int KS = D / 16;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
-  uint8_t* ring = smem;
-  uint4* qs = reinterpret_cast<uint4*>(smem + kStages * kStage * D);
+  uint8_t* ring = sm100::align_smem_1024(smem);
+  uint4* qs = reinterpret_cast<uint4*>(ring + kStages * kStage * D);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int j = blockIdx.y, bi = blockIdx.z;
   const int64_t row = (int64_t)bi * a.c.nkv + j;
@@ -151,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const CacheSco
     return;
   }
   if (warp == 4) {
-    load_rows<D>(a, sh, ring, lane, bi, j, k0, k1, passes);
+    load_rows<D>(a, map, sh, ring, lane, bi, j, k0, k1, passes);
   } else {
     pdl_wait();
     const float* qg = a.Qg + row * a.NQ * D;
@@ -303,6 +282,9 @@ cudaError_t launch_typed(const CacheScoreArgs& args, cudaStream_t stream) {
   const size_t smem = smem_bytes<D>(a.NQ);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  CUtensorMap map;
+  if (!encode_codes_4d(&map, a.c.k, D, 1 << a.c.page_log2, a.c.nkv, a.c.npages, a.c.sr, a.c.sh, a.c.sp, 1 << box_log2(a.c)))
+    return cudaErrorNotSupported;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -313,7 +295,7 @@ cudaError_t launch_typed(const CacheScoreArgs& args, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;  // waits for the group means inside
-  return cudaLaunchKernelEx(&cfg, kern, a);
+  return cudaLaunchKernelEx(&cfg, kern, map, a);
 }
 
 }  // namespace

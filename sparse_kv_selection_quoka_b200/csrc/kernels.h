@@ -221,15 +221,17 @@ struct CacheAttnArgs {
   int N;                    // most keys of a row
   int chunk;                // 1: the chunk's own keys too
   float scale;
-  float* O_parts;           // (nsplit, b, nq, BCP, d) fp32
-  float* lse_parts;         // (nsplit, b, nq, BCP) fp32, in log2 units
-  int* faults;              // (b, nkv, nsplit): what a range's CTA has to latch
-  int nsplit;               // cache_attn_splits(b * nkv, N)
+  float* O_parts;           // (ranges, G * BCP, d) fp32
+  float* lse_parts;         // (ranges, G * BCP) fp32, in log2 units
+  int2* row_parts;          // (b, nkv): a row's first range and their number
+  int* faults;              // (ranges): what a range's CTA has to latch
+  int ranges, target;       // set by the launcher
   void* O;
   float* lse;
   int* status;
 };
-int cache_attn_splits(int64_t heads, int N);
+// Ranges that launch_cache_attn cuts `rows` = b * nkv rows of at most N keys into, at most.
+int64_t cache_attn_ranges(int64_t rows, int N);
 cudaError_t launch_cache_attn(bool bf16, int d, const CacheAttnArgs& a, cudaStream_t stream);
 
 // Step (d) over the cache's keys: S_agg (b, nkv, max_len); entries at and

@@ -491,8 +491,7 @@ bool overlaps(const void* a, size_t na, const quoka_tensor* t) {
 // their counts and the partials of the tensor-core attention.
 struct CacheAttnWs {
   bool few;
-  int nsplit;
-  size_t o_parts, lse_parts, faults, ksel, vsel, count, aparts, aparts_bytes, total;
+  size_t o_parts, lse_parts, row_parts, faults, ksel, vsel, count, aparts, aparts_bytes, total;
 };
 
 CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t BCP, int64_t N, quoka_dtype dtype,
@@ -506,11 +505,11 @@ CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t
   };
   w.few = (nq / nkv) * BCP <= quoka::kCacheMaxRows;
   if (w.few) {
-    w.nsplit = quoka::cache_attn_splits(b * nkv, (int)N);
-    const int64_t rows = w.nsplit * b * nq * BCP;
+    const int64_t ranges = quoka::cache_attn_ranges(b * nkv, (int)N), rows = ranges * (nq / nkv) * BCP;
     w.o_parts = take((size_t)(rows * d) * 4);
     w.lse_parts = take((size_t)rows * 4);
-    w.faults = take((size_t)(b * nkv * w.nsplit) * 4);
+    w.row_parts = take((size_t)(b * nkv) * 8);
+    w.faults = take((size_t)ranges * 4);
   } else {
     w.ksel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
     w.vsel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
@@ -870,7 +869,7 @@ quoka_status quoka_cache_gather(const quoka_cache* cache, int max_len, const int
 }
 
 size_t quoka_cache_attn_workspace_size(int b, int nq, int nkv, int d, int BCP, int N, quoka_dtype dtype) {
-  if (b < 1 || nq < 1 || nkv < 1 || BCP < 1 || N < 0 || nq % nkv != 0 || !supported_d(d)) return 0;
+  if (b < 1 || nq < 1 || nkv < 1 || BCP < 1 || N < 0 || N > (1 << 30) || nq % nkv != 0 || !supported_d(d)) return 0;
   if (dtype != QUOKA_F32 && dtype != QUOKA_BF16) return 0;
   return std::max(cache_attn_ws(b, nq, nkv, d, BCP, N, dtype, false).total,
                   cache_attn_ws(b, nq, nkv, d, BCP, N, dtype, true).total);
@@ -896,7 +895,7 @@ quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, i
     return QUOKA_ERR_INVALID_ARG;
   if (kv_idx == nullptr && N != max_len) return QUOKA_ERR_INVALID_ARG;
   if (O == nullptr || !aligned16(O) || !(scale > 0.f)) return QUOKA_ERR_INVALID_ARG;
-  if (nq > kMaxHeads || BCP > kMaxBCP) return QUOKA_ERR_UNSUPPORTED;
+  if (nq > kMaxHeads || BCP > kMaxBCP || N > (1 << 30)) return QUOKA_ERR_UNSUPPORTED;
   const bool no_chunk = Kc == nullptr, bf = Q->dtype == QUOKA_BF16;
   const CacheAttnWs w = cache_attn_ws(b, nq, nkv, d, BCP, N, Q->dtype, no_chunk);
   st = check_ws(ws, ws_bytes, w.total);
@@ -920,10 +919,10 @@ quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, i
     a.scale = scale;
     a.O_parts = at<float>(ws, w.o_parts);
     a.lse_parts = at<float>(ws, w.lse_parts);
-    a.nsplit = w.nsplit;
     a.O = O;
     a.lse = lse;
     a.status = status;
+    a.row_parts = at<int2>(ws, w.row_parts);
     a.faults = at<int>(ws, w.faults);
     return cuda_status(quoka::launch_cache_attn(bf, (int)d, a, cs));
   }
