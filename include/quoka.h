@@ -422,7 +422,7 @@ typedef struct {
  *   the codes the page holds are brought to it. Codes are rounded to nearest
  *   even and saturate at 448 (infinities too); NaN stays NaN.
  *   new_len (b) int32 or NULL: new tokens of each sequence, in [0, BCP] (NULL:
- *   BCP each). Tokens past it are neither read nor written, in any output.
+ *   BCP each). Tokens past it have no effect and are not written, in any output.
  *   Kr (b, nkv, BCP, d) or NULL, Qr (b, nq, BCP, d, with Q): out, contiguous,
  *   the rotated keys and queries rounded to their dtype. They must not
  *   overlap K, V or Q (QUOKA_ERR_INVALID_ARG).

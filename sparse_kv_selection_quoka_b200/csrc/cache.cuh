@@ -67,23 +67,6 @@ __device__ __forceinline__ int scale_exp_for(float amax) {
   return min(max(e, kCacheMinExp), kCacheMaxExp);
 }
 
-// Tokens a kernel may read of sequence bi: seq_len, kept to [0, max_len].
-// A length outside that range is latched.
-__device__ __forceinline__ int cache_len(const CacheView& c, int bi, int max_len, int* status) {
-  const int n = __ldcg(c.seq_len + bi);
-  if ((n < 0 || n > max_len) && status != nullptr) latch_status(status, 6 /* QUOKA_ERR_BOUNDS */);
-  return min(max(n, 0), max_len);
-}
-
-// The page of table column `col` of sequence bi, or -1 (latched) when the
-// entry names none.
-__device__ __forceinline__ int cache_page(const CacheView& c, int bi, int col, int* status) {
-  const int p = __ldcg(c.page_table + (int64_t)bi * c.table_stride + col);
-  if (p >= 0 && p < c.npages) return p;
-  if (status != nullptr) latch_status(status, 6 /* QUOKA_ERR_BOUNDS */);
-  return -1;
-}
-
 // c (16 x 8, fp32) += a (16 x 16, fp16) * b (16 x 8, fp16)
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(

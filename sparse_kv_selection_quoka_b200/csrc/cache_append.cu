@@ -19,10 +19,12 @@
 // whose rows stay in registers between the maximum and the quantisation; a
 // page has one writer, so nothing is atomic and the result does not depend on
 // the order of the CTAs. The queries are rotated by further CTAs of the same
-// launch, each over a few heads of 256 * 8 / d tokens, so that a token's
-// cosines are read once for several heads.
+// launch, each over a few heads of the same tokens, so that a token's cosines
+// are read once for several heads. A thread owns two 8-column chunks of a row,
+// the two halves of its pairs, and issues all its loads before it computes.
 // Bound by bytes: every row is read once and written once as codes (and once
-// rotated).
+// rotated); a chunk of few tokens by the chain length, page, scale, and takes
+// small CTAs so that all of them are resident at once.
 #include "cache.cuh"
 
 namespace quoka {
@@ -31,7 +33,6 @@ namespace {
 
 using namespace cache;
 
-constexpr int kThreads = 256;
 constexpr int kQHeads = 4;  // query heads of one rotating CTA
 
 struct RotArgs {
@@ -39,6 +40,31 @@ struct RotArgs {
   const float* sin;  // (npos, rot / 2)
   int rot, interleaved;
 };
+
+// 8 elements as they lie in memory.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(const T* p, Raw8<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+}
+__device__ __forceinline__ void to_floats(const Raw8<bf16>& r, float (&v)[8]) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(h[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void to_floats(const Raw8<float>& r, float (&v)[8]) {
+  const float* f = reinterpret_cast<const float*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = f[i];
+}
 
 __device__ __forceinline__ void store8(bf16* p, const float (&v)[8]) {
   uint4 o;
@@ -51,47 +77,43 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-
-// cos / sin of the 8 columns from 8 * c of a row at position `pos`, ready for
-// out[u] = x[u] * cs[u] + y[u] * sn[u] with y the partner columns (sn carries
-// the sign). Columns past `rot` are left alone by the caller.
-__device__ __forceinline__ void load_angles(const RotArgs& r, int pos, int c, float (&cs)[8], float (&sn)[8]) {
-  const int half = r.rot >> 1;
-  if (r.interleaved) {  // pairs (2i, 2i + 1): this chunk holds pairs 4c .. 4c + 3
-    const float4 a = __ldg(reinterpret_cast<const float4*>(r.cos + (int64_t)pos * half + 4 * c));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(r.sin + (int64_t)pos * half + 4 * c));
-    cs[0] = cs[1] = a.x; cs[2] = cs[3] = a.y; cs[4] = cs[5] = a.z; cs[6] = cs[7] = a.w;
-    sn[1] = b.x; sn[3] = b.y; sn[5] = b.z; sn[7] = b.w;
-    sn[0] = -b.x; sn[2] = -b.y; sn[4] = -b.z; sn[6] = -b.w;
-  } else {  // pairs (i, i + rot / 2)
-    const bool second = 8 * c >= half;
-    const int i = 8 * c - (second ? half : 0);
-    load8(r.cos + (int64_t)pos * half + i, cs);
-    load8(r.sin + (int64_t)pos * half + i, sn);
-    if (!second) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u) sn[u] = -sn[u];
-    }
-  }
+__device__ __forceinline__ uint2 quantise8(const float (&v)[8], float f) {
+  uint2 o;
+  o.x = f32x2_to_e4m3x2(v[0] * f, v[1] * f) | (uint32_t)f32x2_to_e4m3x2(v[2] * f, v[3] * f) << 16;
+  o.y = f32x2_to_e4m3x2(v[4] * f, v[5] * f) | (uint32_t)f32x2_to_e4m3x2(v[6] * f, v[7] * f) << 16;
+  return o;
 }
 
-// The rotated 8 columns from 8 * c of the row at `p`. (x * c + y * (-s) and
-// x * c - y * s round alike.)
-template <typename T>
-__device__ __forceinline__ void load_rotated(const T* p, const RotArgs& r, int c, const float (&cs)[8],
-                                             const float (&sn)[8], float (&x)[8]) {
-  load8(p + 8 * c, x);
-  if (8 * c >= r.rot) return;
-  float y[8];
+// The two chunks of thread i (of D / 16) of a row: with pairs (c, c + rot / 2)
+// the halves of 8 pairs, else two neighbouring chunks.
+__device__ __forceinline__ void chunks_of(const RotArgs& r, int i, int* c0, int* c1) {
+  const bool split = !r.interleaved && 16 * i < r.rot;
+  *c0 = split ? i : 2 * i;
+  *c1 = split ? i + (r.rot >> 4) : 2 * i + 1;
+}
+
+// Rotates the two chunks x, y of thread i by the angles of a position, cs and
+// sn being the 8 cosines and sines from 8 i of its row of the tables.
+__device__ __forceinline__ void rotate(const RotArgs& r, const float (&cs)[8], const float (&sn)[8], float (&x)[8],
+                                       float (&y)[8]) {
   if (r.interleaved) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) y[u] = x[u ^ 1];
+    for (int u = 0; u < 4; ++u) {
+      const float a = x[2 * u], z = x[2 * u + 1];
+      x[2 * u] = __fsub_rn(__fmul_rn(a, cs[u]), __fmul_rn(z, sn[u]));
+      x[2 * u + 1] = __fadd_rn(__fmul_rn(z, cs[u]), __fmul_rn(a, sn[u]));
+      const float b = y[2 * u], w = y[2 * u + 1];
+      y[2 * u] = __fsub_rn(__fmul_rn(b, cs[4 + u]), __fmul_rn(w, sn[4 + u]));
+      y[2 * u + 1] = __fadd_rn(__fmul_rn(w, cs[4 + u]), __fmul_rn(b, sn[4 + u]));
+    }
   } else {
-    const int half = r.rot >> 1;
-    load8(p + 8 * c + (8 * c < half ? half : -half), y);
-  }
 #pragma unroll
-  for (int u = 0; u < 8; ++u) x[u] = __fadd_rn(__fmul_rn(x[u], cs[u]), __fmul_rn(y[u], sn[u]));
+    for (int u = 0; u < 8; ++u) {
+      const float a = x[u], z = y[u];
+      x[u] = __fsub_rn(__fmul_rn(a, cs[u]), __fmul_rn(z, sn[u]));
+      y[u] = __fadd_rn(__fmul_rn(z, cs[u]), __fmul_rn(a, sn[u]));
+    }
+  }
 }
 
 // New tokens of sequence bi: positions [start, end). Lengths and counts out
@@ -113,14 +135,15 @@ __device__ __forceinline__ void new_range(const CacheAppendArgs& a, int bi, int*
   if (bad && a.status != nullptr) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
 }
 
-// Grid: nkvu key / value CTAs, then the query CTAs. NP: passes of
-// 256 * 8 / D rows that cover a page.
-template <typename T, int D, int NP>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheAppendArgs a, int npt, int nkvu) {
-  constexpr int CPR = D / 8;           // 8-column chunks per row
-  constexpr int RPP = kThreads / CPR;  // rows per pass
-  const int tid = threadIdx.x, c = tid % CPR, rr = tid / CPR;
+// Grid: nkvu key / value CTAs, then the query CTAs. NT threads; NP passes of
+// NT * 16 / D rows that cover the new tokens of a page.
+template <typename T, int D, int NT, int NP>
+__global__ void __launch_bounds__(NT) cache_append_kernel(const CacheAppendArgs a, int npt, int nkvu) {
+  constexpr int TPR = D / 16;    // threads of a row
+  constexpr int RPP = NT / TPR;  // rows of a pass
+  const int tid = threadIdx.x, i = tid % TPR, rr = tid / TPR;
   const RotArgs rot{a.cos, a.sin, a.rot, a.interleaved};
+  const int half = a.rot >> 1;
   pdl_wait();
 
   if ((int)blockIdx.x >= nkvu) {
@@ -131,27 +154,41 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheAppen
     const int h0 = (u % hgroups) * kQHeads;
     if (g >= (int64_t)a.b * a.BCP) return;
     const int bi = (int)(g / a.BCP), t = (int)(g % a.BCP);
+    int c0, c1;
+    chunks_of(rot, i, &c0, &c1);
+    const T* q = static_cast<const T*>(a.Q.data) + bi * a.Q.sb + (int64_t)t * a.Q.st;
+    Raw8<T> rx[kQHeads], ry[kQHeads];
+#pragma unroll
+    for (int k = 0; k < kQHeads; ++k)
+      if (h0 + k < a.nq) {
+        load_raw(q + (h0 + k) * a.Q.sh + 8 * c0, rx[k]);
+        load_raw(q + (h0 + k) * a.Q.sh + 8 * c1, ry[k]);
+      }
     int start, end;
     new_range(a, bi, &start, &end);
     if (start + t >= end) return;
+    const bool turn = 16 * i < a.rot;
     float cs[8], sn[8];
-    if (8 * c < a.rot) load_angles(rot, start + t, c, cs, sn);
-    const T* q = static_cast<const T*>(a.Q.data) + bi * a.Q.sb + t * a.Q.st;
-    T* o = static_cast<T*>(a.Qr) + ((int64_t)bi * a.nq * a.BCP + t) * D + 8 * c;
-#pragma unroll
-    for (int i = 0; i < kQHeads; ++i) {
-      const int h = h0 + i;
-      if (h < a.nq) {
-        float x[8];
-        load_rotated(q + h * a.Q.sh, rot, c, cs, sn, x);
-        store8(o + (int64_t)h * a.BCP * D, x);
-      }
+    if (turn) {
+      load8(a.cos + (int64_t)(start + t) * half + 8 * i, cs);
+      load8(a.sin + (int64_t)(start + t) * half + 8 * i, sn);
     }
+    T* o = static_cast<T*>(a.Qr) + ((int64_t)bi * a.nq * a.BCP + t) * D;
+#pragma unroll
+    for (int k = 0; k < kQHeads; ++k)
+      if (h0 + k < a.nq) {
+        float x[8], y[8];
+        to_floats(rx[k], x);
+        to_floats(ry[k], y);
+        if (turn) rotate(rot, cs, sn, x, y);
+        store8(o + (int64_t)(h0 + k) * a.BCP * D + 8 * c0, x);
+        store8(o + (int64_t)(h0 + k) * a.BCP * D + 8 * c1, y);
+      }
     return;
   }
 
   // ------------------------------------------------------------ keys, values
-  __shared__ uint32_t wmax[kThreads / 32];
+  __shared__ uint32_t wmax[NT / 32];
   const int nkv = a.c.nkv;
   const bool is_v = blockIdx.x & 1;
   const int j = (blockIdx.x >> 1) % nkv;
@@ -163,43 +200,64 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheAppen
   const int p0 = col << a.c.page_log2;
   const int t0 = max(start, p0), t1 = min(end, p0 + (1 << a.c.page_log2));
   if (t0 >= t1) return;  // (the same for the whole CTA)
+  const int pid = __ldcg(a.c.page_table + (int64_t)bi * a.c.table_stride + col);
   const Strided X = is_v ? a.V : a.K;
   const T* x0 = static_cast<const T*>(X.data) + bi * X.sb + j * X.sh;
-  const int page = cache_page(a.c, bi, col, a.status);
+  int c0 = 2 * i, c1 = 2 * i + 1;
+  const bool turn = !is_v && 16 * i < a.rot;
+  if (turn) chunks_of(rot, i, &c0, &c1);
 
-  float x[NP][8];
+  float x[NP][8], y[NP][8];
   uint32_t top = 0u;  // bits of the largest finite magnitude
+  {
+    Raw8<T> rx[NP], ry[NP];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int t = t0 + i * RPP + rr;
-    if (t < t1) {
-      const T* row = x0 + (int64_t)(t - start) * X.st;
-      if (is_v) {
-        load8(row + 8 * c, x[i]);
-      } else {
+    for (int k = 0; k < NP; ++k) {
+      const int t = t0 + k * RPP + rr;
+      if (t < t1) {
+        load_raw(x0 + (int64_t)(t - start) * X.st + 8 * c0, rx[k]);
+        load_raw(x0 + (int64_t)(t - start) * X.st + 8 * c1, ry[k]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int t = t0 + k * RPP + rr;
+      if (t >= t1) continue;
+      to_floats(rx[k], x[k]);
+      to_floats(ry[k], y[k]);
+      if (turn) {
         float cs[8], sn[8];
-        if (8 * c < a.rot) load_angles(rot, t, c, cs, sn);
-        load_rotated(row, rot, c, cs, sn, x[i]);
-        if (a.Kr != nullptr)
-          store8(static_cast<T*>(a.Kr) + (((int64_t)bi * nkv + j) * a.BCP + (t - start)) * D + 8 * c, x[i]);
+        load8(a.cos + (int64_t)t * half + 8 * i, cs);
+        load8(a.sin + (int64_t)t * half + 8 * i, sn);
+        rotate(rot, cs, sn, x[k], y[k]);
+      }
+      if (!is_v && a.Kr != nullptr) {
+        T* o = static_cast<T*>(a.Kr) + (((int64_t)bi * nkv + j) * a.BCP + (t - start)) * D;
+        store8(o + 8 * c0, x[k]);
+        store8(o + 8 * c1, y[k]);
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const uint32_t m = __float_as_uint(x[i][u]) & 0x7FFFFFFFu;
-        if (m < 0x7F800000u) top = max(top, m);
+        const uint32_t mx = __float_as_uint(x[k][u]) & 0x7FFFFFFFu, my = __float_as_uint(y[k][u]) & 0x7FFFFFFFu;
+        if (mx < 0x7F800000u) top = max(top, mx);
+        if (my < 0x7F800000u) top = max(top, my);
       }
     }
   }
+  const bool held = pid >= 0 && pid < a.c.npages;
+  if (!held) {  // (the same for the whole CTA)
+    if (tid == 0 && a.status != nullptr) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
+    return;
+  }
   top = __reduce_max_sync(0xffffffffu, top);
   if ((tid & 31) == 0) wmax[tid >> 5] = top;
-  float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + (int64_t)max(page, 0) * nkv + j;
-  const float old = page >= 0 && t0 > p0 ? __ldcg(scale) : 0.f;
+  float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + (int64_t)pid * nkv + j;
+  const float old = t0 > p0 ? __ldcg(scale) : 0.f;
   __syncthreads();  // (the old scale is read by all before it is replaced below)
-  if (page < 0) return;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) top = max(top, wmax[w]);
+  for (int w = 0; w < NT / 32; ++w) top = max(top, wmax[w]);
   int e = scale_exp_for(__uint_as_float(top));
-  uint8_t* dst = (is_v ? a.c.v : a.c.k) + page * a.c.sp + j * a.c.sh;
+  uint8_t* dst = (is_v ? a.c.v : a.c.k) + pid * a.c.sp + j * a.c.sh;
   if (t0 > p0) {  // the page holds earlier tokens
     bool bad = false;
     const int eo = scale_exp(old, &bad);
@@ -207,15 +265,15 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheAppen
     if (e > eo) {
       const float f = exp2i(eo - e);
       for (int r = rr; r < t0 - p0; r += RPP) {
-        uint2* p = reinterpret_cast<uint2*>(dst + r * a.c.sr + 8 * c);
-        const uint2 w = *p;
-        float v[8];
+        uint4* p = reinterpret_cast<uint4*>(dst + r * a.c.sr + 16 * i);
+        const uint4 w = *p;
+        float v[8], z[8];
         e4m3x4_to_f32(w.x, v);
         e4m3x4_to_f32(w.y, v + 4);
-        uint2 o;
-        o.x = f32x2_to_e4m3x2(v[0] * f, v[1] * f) | (uint32_t)f32x2_to_e4m3x2(v[2] * f, v[3] * f) << 16;
-        o.y = f32x2_to_e4m3x2(v[4] * f, v[5] * f) | (uint32_t)f32x2_to_e4m3x2(v[6] * f, v[7] * f) << 16;
-        *p = o;
+        e4m3x4_to_f32(w.z, z);
+        e4m3x4_to_f32(w.w, z + 4);
+        const uint2 lo = quantise8(v, f), hi = quantise8(z, f);
+        *p = make_uint4(lo.x, lo.y, hi.x, hi.y);
       }
     } else {
       e = eo;
@@ -223,41 +281,47 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheAppen
   }
   const float f = exp2i(-e);
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int t = t0 + i * RPP + rr;
+  for (int k = 0; k < NP; ++k) {
+    const int t = t0 + k * RPP + rr;
     if (t < t1) {
-      uint2 o;
-      o.x = f32x2_to_e4m3x2(x[i][0] * f, x[i][1] * f) | (uint32_t)f32x2_to_e4m3x2(x[i][2] * f, x[i][3] * f) << 16;
-      o.y = f32x2_to_e4m3x2(x[i][4] * f, x[i][5] * f) | (uint32_t)f32x2_to_e4m3x2(x[i][6] * f, x[i][7] * f) << 16;
-      *reinterpret_cast<uint2*>(dst + (int64_t)(t - p0) * a.c.sr + 8 * c) = o;
+      uint8_t* o = dst + (int64_t)(t - p0) * a.c.sr;
+      *reinterpret_cast<uint2*>(o + 8 * c0) = quantise8(x[k], f);
+      *reinterpret_cast<uint2*>(o + 8 * c1) = quantise8(y[k], f);
     }
   }
   if (tid == 0) *scale = exp2i(e);
 }
 
-template <typename T, int D>
-cudaError_t launch_typed(const CacheAppendArgs& a, bool pdl, cudaStream_t stream) {
-  constexpr int RPP = kThreads * 8 / D;
+template <typename T, int D, int NT, int NP>
+cudaError_t launch_grid(const CacheAppendArgs& a, bool pdl, cudaStream_t stream) {
+  constexpr int RPP = NT * 16 / D;
   const int page = 1 << a.c.page_log2;
   const int npt = (a.BCP + 2 * page - 2) / page;  // pages a run of BCP tokens can touch
   const int64_t nkvu = (int64_t)a.b * npt * a.c.nkv * 2;
   const int64_t nqu = a.Qr != nullptr ? ((int64_t)a.b * a.BCP + RPP - 1) / RPP * ((a.nq + kQHeads - 1) / kQHeads) : 0;
   if (nkvu + nqu > 0x7FFFFFFF) return cudaErrorNotSupported;
-  const int np = (page + RPP - 1) / RPP;
-  auto* kern = np <= 1   ? cache_append_kernel<T, D, 1>
-               : np <= 2 ? cache_append_kernel<T, D, 2>
-               : np <= 4 ? cache_append_kernel<T, D, 4>
-                         : cache_append_kernel<T, D, 8>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(nkvu + nqu));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(NT);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, a, npt, (int)nkvu);
+  return cudaLaunchKernelEx(&cfg, cache_append_kernel<T, D, NT, NP>, a, npt, (int)nkvu);
+}
+
+// CTAs of 64 threads while one pass of theirs covers the new tokens of a page,
+// else of 256.
+template <typename T, int D>
+cudaError_t launch_typed(const CacheAppendArgs& a, bool pdl, cudaStream_t stream) {
+  const int page = 1 << a.c.page_log2, rows = a.BCP < page ? a.BCP : page;
+  if (rows <= 1024 / D) return launch_grid<T, D, 64, 1>(a, pdl, stream);
+  const int np = (rows + 4096 / D - 1) / (4096 / D);
+  if (np <= 1) return launch_grid<T, D, 256, 1>(a, pdl, stream);
+  if (np <= 2) return launch_grid<T, D, 256, 2>(a, pdl, stream);
+  return launch_grid<T, D, 256, 4>(a, pdl, stream);  // (pages have at most 128 rows)
 }
 
 }  // namespace
