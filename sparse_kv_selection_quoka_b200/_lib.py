@@ -3,7 +3,8 @@
 Argument marshalling only: torch tensors are turned into the C ABI's strided
 views (device pointer, dtype, shape, element strides) and the call is
 enqueued on the current CUDA stream. Every step of the computation runs in
-the library's CUDA kernels. Output and workspace buffers the caller does not
+the library's CUDA kernels. (The cache calls are marshalled by a compiled
+module, csrc/cache_binding.cpp.) Output and workspace buffers the caller does not
 pass are allocated with torch (the library itself never allocates).
 
 The library must have been built (python -m sparse_kv_selection_quoka_b200.build);
@@ -12,9 +13,8 @@ there is no fallback: a missing library raises at load time.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
-import struct
 import threading
 from typing import Optional
 
@@ -22,6 +22,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libquoka.so")
+BINDING_PATH = os.path.join(_PKG, "_cache_binding.so")
 
 QUOKA_F32 = 0
 QUOKA_BF16 = 1
@@ -110,7 +111,6 @@ _lock = threading.Lock()
 _P = ctypes.c_void_p
 _T = ctypes.POINTER(quoka_tensor)
 _C = ctypes.POINTER(quoka_cache)
-_B = ctypes.c_char_p  # a packed quoka_tensor
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
@@ -172,15 +172,15 @@ def load() -> ctypes.CDLL:
         lib.quoka_debug_set_wait_hooks.restype = _I
         lib.quoka_debug_set_wait_hooks.argtypes = [ctypes.c_uint64, ctypes.c_uint32]
         lib.quoka_cache_append.restype = _I
-        lib.quoka_cache_append.argtypes = [_C, _B, _B, _B, _P, _P, _I64, _I, ctypes.c_uint32, _P, _P, _P, _P, _SZ, _P]
+        lib.quoka_cache_append.argtypes = [_C, _T, _T, _T, _P, _P, _I64, _I, ctypes.c_uint32, _P, _P, _P, _P, _SZ, _P]
         lib.quoka_cache_select.restype = _I
-        lib.quoka_cache_select.argtypes = [_B, _C, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]
+        lib.quoka_cache_select.argtypes = [_T, _C, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]
         lib.quoka_cache_gather.restype = _I
         lib.quoka_cache_gather.argtypes = [_C, _I, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]
         lib.quoka_cache_attn_workspace_size.restype = _SZ
         lib.quoka_cache_attn_workspace_size.argtypes = [_I, _I, _I, _I, _I, _I, _I]
         lib.quoka_cache_attn.restype = _I
-        lib.quoka_cache_attn.argtypes = [_B, _C, _I, _P, _P, _I, _B, _B, _F, _P, _P, _P, _SZ, _P]
+        lib.quoka_cache_attn.argtypes = [_T, _C, _I, _P, _P, _I, _T, _T, _F, _P, _P, _P, _SZ, _P]
         lib.quoka_combine_partials.restype = _I
         lib.quoka_combine_partials.argtypes = [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]
         _lib = lib
@@ -221,10 +221,6 @@ def _stream(stream) -> ctypes.c_void_p:
 def _check(status: int, where: str) -> None:
     if status != 0:
         raise QuokaError(status, where)
-
-
-# the address of a device's current stream
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _code(dtype) -> int:
@@ -609,75 +605,49 @@ class QuokaCache:
         self._view = quoka_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), npages, nkv, page,
                                  d, k.stride(0), k.stride(1), k.stride(2), page_table.data_ptr(),
                                  max(page_table.stride(0), max_pages), b, max_pages, seq_len.data_ptr())
-        self._ref = ctypes.byref(self._view)
+        self._handle = ctypes.addressof(self._view)
+        self._device = k.device.index if k.is_cuda else -1
 
 
-# The cache calls serve decode steps, whose kernels take a few microseconds:
-# their arguments are checked and packed in as little host time as they allow
-# (a packed view is one struct.pack, a workspace size is looked up once per
-# shape).
-_CODES = {torch.float32: QUOKA_F32, torch.bfloat16: QUOKA_BF16}
-_pack_view = struct.Struct("Pi4x8q").pack  # quoka_tensor
-assert struct.calcsize("Pi4x8q") == ctypes.sizeof(quoka_tensor)
+_cache = None
+
+
+def _binding():
+    """The compiled binding of the cache calls (csrc/cache_binding.cpp), bound
+    to the loaded library: it checks a call's tensors and allocates what was
+    not given in a fraction of the host time that this module would take, which
+    for a decode step is the larger part."""
+    global _cache
+    lib = load()
+    with _lock:
+        if _cache is None:
+            if not os.path.exists(BINDING_PATH):
+                raise ImportError(f"{BINDING_PATH} is missing: build it with "
+                                  "`python -m sparse_kv_selection_quoka_b200.build`")
+            spec = importlib.util.spec_from_file_location("_cache_binding", BINDING_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind(*(ctypes.cast(f, _P).value for f in (
+                lib.quoka_cache_append, lib.quoka_cache_select, lib.quoka_cache_gather, lib.quoka_cache_attn,
+                lib.quoka_select_workspace_size, lib.quoka_cache_attn_workspace_size)))
+            _cache = module
+    return _cache
 
 
 def _expect(t, name, dtype, shape, device) -> None:
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
-        return
-    if t.dtype is not dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, not {t.device}")
-    raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _rows(x, name, shape, device, dtype):
-    """The packed view of rows x, which must have this shape and dtype (any strides)."""
-    if x.shape != shape or x.device != device:
-        raise ValueError(f"{name} must be {tuple(shape)} on {device}, not {tuple(x.shape)} on {x.device}")
-    if x.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {x.dtype}")
-    return _pack_view(x.data_ptr(), _CODES[dtype], *shape, *x.stride())
-
-
-def _row_shape(x, name, cache):
-    """heads, rows of x (b, heads, rows, d)."""
-    if x.dtype not in _CODES:
-        raise TypeError(f"unsupported dtype {x.dtype}")
-    if x.dim() != 4 or x.shape[0] != cache.b or x.shape[3] != cache.d:
-        raise ValueError(f"{name} must be ({cache.b}, heads, rows, {cache.d}), not {tuple(x.shape)}")
-    return x.shape[1], x.shape[2]
-
-
-def _here(cache, stream) -> bool:
-    """Whether a call can go to the current stream of the current device as it is."""
-    if cache.device.type != "cuda":
-        raise ValueError("the cache must be on a CUDA device")
-    return stream is None and cache.device.index == torch.cuda.current_device()
-
-
-def _there(cache, stream):
-    """The context of a call that goes elsewhere, so that what it allocates belongs there."""
-    if stream is None:
-        return torch.cuda.device(cache.device)
+def _on(cache, stream):
+    """The context of a call on a given stream: what it allocates belongs there."""
     if stream.device != cache.device:
         raise ValueError(f"the stream must be on the cache's device {cache.device}")
     return torch.cuda.stream(stream)
-
-
-def _workspace(ws, cache):
-    if ws is None:
-        return None, 0
-    if ws.device != cache.device or not ws.is_contiguous():
-        raise ValueError(f"ws must be contiguous on {cache.device}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-ROTATE_NEIGHBOURS = 1  # quoka_cache_append flag: pairs are neighbouring columns
 
 
 def quoka_cache_append(cache, K, V, Q=None, cos=None, sin=None, *, interleaved=False, new_len=None, Kr=None, Qr=None,
@@ -690,51 +660,15 @@ def quoka_cache_append(cache, K, V, Q=None, cos=None, sin=None, *, interleaved=F
     their dtype. Tokens from new_len (b) int32 on (None: BCP) are left out;
     their rows of Kr and Qr stay as they were (zeros when made here).
     cache.seq_len stays: advance it when the chunk is done."""
-    lib, b, nkv, d, dev = load(), cache.b, cache.nkv, cache.d, cache.device
-    BCP, dtype = _row_shape(K, "K", cache)[1], K.dtype
-    shape = (b, nkv, BCP, d)
-    kv, vv = _rows(K, "K", shape, dev, dtype), _rows(V, "V", shape, dev, dtype)
-    qv = None
-    if Q is not None:
-        qshape = (b, _row_shape(Q, "Q", cache)[0], BCP, d)
-        qv = _rows(Q, "Q", qshape, dev, dtype)
-        if Qr is not None:
-            _expect(Qr, "Qr", dtype, qshape, dev)
-    elif Qr is not None:
-        raise ValueError("Qr without Q")
-    rot = npos = 0
-    if cos is not None and sin is not None:
-        if cos.dim() != 2:
-            raise ValueError("cos and sin must be (npos, rot / 2)")
-        npos, half = cos.shape
-        rot = 2 * half
-        _expect(cos, "cos", torch.float32, (npos, half), dev)
-        _expect(sin, "sin", torch.float32, (npos, half), dev)
-    elif cos is not None or sin is not None:
-        raise ValueError("cos and sin go together")
-    if new_len is not None:
-        _expect(new_len, "new_len", torch.int32, (b,), dev)
-    if Kr is not None:
-        _expect(Kr, "Kr", dtype, shape, dev)
-    wp, wn = _workspace(ws, cache)
-    if not _here(cache, stream):
-        with _there(cache, stream):
+    if stream is not None:
+        with _on(cache, stream):
             return quoka_cache_append(cache, K, V, Q, cos, sin, interleaved=interleaved, new_len=new_len, Kr=Kr, Qr=Qr,
                                       want_Kr=want_Kr, ws=ws)
-    if Kr is None and want_Kr:
-        Kr = K.new_zeros(shape) if new_len is not None else K.new_empty(shape)
-    if Qr is None and Q is not None:
-        Qr = Q.new_zeros(qshape) if new_len is not None else Q.new_empty(qshape)
-    st = lib.quoka_cache_append(cache._ref, kv, vv, qv, _addr(cos), _addr(sin), npos, rot,
-                                ROTATE_NEIGHBOURS if interleaved else 0, _addr(new_len), _addr(Kr), _addr(Qr), wp, wn,
-                                _raw_stream(dev.index))
-    _check(st, "quoka_cache_append")
-    return Kr, Qr
-
-
-@functools.lru_cache(maxsize=4096)
-def _cache_select_ws(b, nq, nkv, d, max_len, BCP, NQ, BSA, code) -> int:
-    return max(256, load().quoka_select_workspace_size(b, nq, nkv, d, max_len, BCP, NQ, BSA, code))
+    r = (_cache or _binding()).append(cache._handle, cache._device, K, V, Q, cos, sin, bool(interleaved), new_len, Kr, Qr,
+                                      bool(want_Kr), ws)
+    if type(r) is int:
+        raise QuokaError(r, "quoka_cache_append")
+    return r
 
 
 def quoka_cache_select(Q, cache, max_len: int, NQ: int, BSA: int, *, kv_idx=None, kv_count=None, q_idx=None,
@@ -743,56 +677,15 @@ def quoka_cache_select(Q, cache, max_len: int, NQ: int, BSA: int, *, kv_idx=None
     min(BSA, max_len)) int32 ascending, kv_count (b, nkv) int32, q_idx or
     None, s_agg (b, nkv, max_len) or None); max_len bounds cache.seq_len.
     Entries past a count, and scores past a sequence's end, are not written."""
-    lib, b, nkv, d, dev = load(), cache.b, cache.nkv, cache.d, cache.device
-    nq, BCP = _row_shape(Q, "Q", cache)
-    qv = _rows(Q, "Q", (b, nq, BCP, d), dev, Q.dtype)
-    n = max(0, min(BSA, max_len))
-    if kv_idx is not None:
-        _expect(kv_idx, "kv_idx", torch.int32, (b, nkv, n), dev)
-    if kv_count is not None:
-        _expect(kv_count, "kv_count", torch.int32, (b, nkv), dev)
-    if q_idx is not None:
-        _expect(q_idx, "q_idx", torch.int32, (b, nq, NQ), dev)
-    if s_agg is not None:
-        _expect(s_agg, "s_agg", torch.float32, (b, nkv, max_len), dev)
-    wp, wn = _workspace(ws, cache)
-    if not _here(cache, stream):
-        with _there(cache, stream):
+    if stream is not None:
+        with _on(cache, stream):
             return quoka_cache_select(Q, cache, max_len, NQ, BSA, kv_idx=kv_idx, kv_count=kv_count, q_idx=q_idx,
                                       s_agg=s_agg, want_q_idx=want_q_idx, want_s_agg=want_s_agg, ws=ws)
-    if kv_idx is None:
-        kv_idx = cache.seq_len.new_empty((b, nkv, n))
-    if kv_count is None:
-        kv_count = cache.seq_len.new_empty((b, nkv))
-    if q_idx is None and want_q_idx:
-        q_idx = cache.seq_len.new_empty((b, nq, NQ))
-    if s_agg is None and want_s_agg:
-        s_agg = cache.k_scale.new_empty((b, nkv, max_len))
-    if ws is None:
-        wn = _cache_select_ws(b, nq, nkv, d, max_len, BCP, max(1, NQ), max(0, BSA), _CODES[Q.dtype])
-        ws = cache.seq_len.new_empty((wn + 3) // 4)
-        wp = ws.data_ptr()
-    st = lib.quoka_cache_select(qv, cache._ref, max_len, NQ, BSA, kv_idx.data_ptr() if n else None,
-                                kv_count.data_ptr(), _addr(q_idx), _addr(s_agg) if max_len else None, wp, wn,
-                                _raw_stream(dev.index))
-    _check(st, "quoka_cache_select")
-    return kv_idx, kv_count, q_idx, s_agg
-
-
-def _index_list(cache, max_len, kv_idx, kv_count):
-    """The rows N of an index list (b, nkv, N) with counts, or max_len without
-    one, and the list's address (not null for an empty list)."""
-    if kv_idx is None:
-        if kv_count is not None:
-            raise ValueError("kv_idx and kv_count go together")
-        return max_len, None, None
-    if kv_count is None or kv_idx.dim() != 3:
-        raise ValueError("kv_idx must be (b, nkv, N), with kv_count")
-    n = kv_idx.shape[2]
-    _expect(kv_idx, "kv_idx", torch.int32, (cache.b, cache.nkv, n), cache.device)
-    _expect(kv_count, "kv_count", torch.int32, (cache.b, cache.nkv), cache.device)
-    cp = kv_count.data_ptr()
-    return n, kv_idx.data_ptr() if n else cp, cp
+    r = (_cache or _binding()).select(cache._handle, cache._device, Q, max_len, NQ, BSA, kv_idx, kv_count, q_idx, s_agg,
+                                      bool(want_q_idx), bool(want_s_agg), ws)
+    if type(r) is int:
+        raise QuokaError(r, "quoka_cache_select")
+    return r
 
 
 def quoka_cache_gather(cache, max_len: int, kv_idx=None, kv_count=None, *, dtype=torch.bfloat16, Ksel=None, Vsel=None,
@@ -801,36 +694,20 @@ def quoka_cache_gather(cache, max_len: int, kv_idx=None, kv_count=None, *, dtype
     (bfloat16 or float32): the rows of the index list kv_idx (b, nkv, N) with
     kv_count (b, nkv), or, without one, all rows below each seq_len (N =
     max_len). Rows past the count are zeros."""
-    lib, dev = load(), cache.device
-    n, ip, cp = _index_list(cache, max_len, kv_idx, kv_count)
-    if dtype not in _CODES:
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError(f"unsupported dtype {dtype}")
-    shape = (cache.b, cache.nkv, n, cache.d)
-    if Ksel is not None:
-        _expect(Ksel, "Ksel", dtype, shape, dev)
-    if Vsel is not None:
-        _expect(Vsel, "Vsel", dtype, shape, dev)
-    wp, wn = _workspace(ws, cache)
-    if not _here(cache, stream):
-        with _there(cache, stream):
+    if stream is not None:
+        with _on(cache, stream):
             return quoka_cache_gather(cache, max_len, kv_idx, kv_count, dtype=dtype, Ksel=Ksel, Vsel=Vsel, ws=ws)
-    if Ksel is None:
-        Ksel = torch.empty(shape, dtype=dtype, device=dev)
-    if Vsel is None:
-        Vsel = torch.empty(shape, dtype=dtype, device=dev)
-    st = lib.quoka_cache_gather(cache._ref, max_len, ip, cp, n, _CODES[dtype], Ksel.data_ptr() if n else None,
-                                Vsel.data_ptr() if n else None, wp, wn, _raw_stream(dev.index))
-    _check(st, "quoka_cache_gather")
-    return Ksel, Vsel
+    r = (_cache or _binding()).gather(cache._handle, cache._device, max_len, kv_idx, kv_count, dtype is torch.float32,
+                                      Ksel, Vsel, ws)
+    if type(r) is int:
+        raise QuokaError(r, "quoka_cache_gather")
+    return r
 
 
 def quoka_cache_attn_workspace_size(b, nq, nkv, d, BCP, N, dtype) -> int:
     return int(load().quoka_cache_attn_workspace_size(b, nq, nkv, d, BCP, N, _code(dtype)))
-
-
-@functools.lru_cache(maxsize=4096)
-def _cache_attn_ws(b, nq, nkv, d, BCP, N, code) -> int:
-    return max(256, quoka_cache_attn_workspace_size(b, nq, nkv, d, BCP, N, code))
 
 
 def quoka_cache_attn(Q, cache, max_len: int, kv_idx=None, kv_count=None, Kc=None, Vc=None, scale=None, *, O=None,
@@ -841,35 +718,12 @@ def quoka_cache_attn(Q, cache, max_len: int, kv_idx=None, kv_count=None, Kc=None
     (O (b, nq, BCP, d), lse (b, nq, BCP) or None); a row that sees no key gives
     0 and -inf. `ws` defaults to a new workspace of
     quoka_cache_attn_workspace_size bytes."""
-    lib, b, nkv, d, dev = load(), cache.b, cache.nkv, cache.d, cache.device
-    nq, BCP = _row_shape(Q, "Q", cache)
-    shape, dtype = (b, nq, BCP, d), Q.dtype
-    qv = _rows(Q, "Q", shape, dev, dtype)
-    n, ip, cp = _index_list(cache, max_len, kv_idx, kv_count)
-    kcv = vcv = None
-    if Kc is not None and Vc is not None:
-        kcv = _rows(Kc, "Kc", (b, nkv, BCP, d), dev, dtype)
-        vcv = _rows(Vc, "Vc", (b, nkv, BCP, d), dev, dtype)
-    elif Kc is not None or Vc is not None:
-        raise ValueError("Kc and Vc go together")
-    if O is not None:
-        _expect(O, "O", dtype, shape, dev)
-    if lse is not None:
-        _expect(lse, "lse", torch.float32, shape[:3], dev)
-    wp, wn = _workspace(ws, cache)
-    if not _here(cache, stream):
-        with _there(cache, stream):
+    if stream is not None:
+        with _on(cache, stream):
             return quoka_cache_attn(Q, cache, max_len, kv_idx, kv_count, Kc, Vc, scale, O=O, lse=lse,
                                     want_lse=want_lse, ws=ws)
-    if O is None:
-        O = Q.new_empty(shape)
-    if lse is None and want_lse:
-        lse = cache.k_scale.new_empty(shape[:3])
-    if ws is None:
-        wn = _cache_attn_ws(b, nq, nkv, d, BCP, n, _CODES[dtype])
-        ws = cache.seq_len.new_empty((wn + 3) // 4)
-        wp = ws.data_ptr()
-    st = lib.quoka_cache_attn(qv, cache._ref, max_len, ip, cp, n, kcv, vcv, d ** -0.5 if scale is None else scale,
-                              O.data_ptr(), _addr(lse), wp, wn, _raw_stream(dev.index))
-    _check(st, "quoka_cache_attn")
-    return O, lse
+    r = (_cache or _binding()).attn(cache._handle, cache._device, Q, max_len, kv_idx, kv_count, Kc, Vc,
+                                    cache.d ** -0.5 if scale is None else scale, O, lse, bool(want_lse), ws)
+    if type(r) is int:
+        raise QuokaError(r, "quoka_cache_attn")
+    return r

@@ -4,7 +4,9 @@
 
 Each csrc/*.cu is compiled to an object under _build/ (in parallel) and the
 objects are linked into sparse_kv_selection_quoka_b200/libquoka.so. The CUDA
-runtime is linked statically. No GPU is needed to build.
+runtime is linked statically. The Python binding of the cache calls
+(csrc/cache_binding.cpp, against torch's headers) is compiled alongside into
+_cache_binding.so. No GPU is needed to build.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libquoka.so")
+BINDING_SRC = os.path.join(CSRC, "cache_binding.cpp")
+BINDING = os.path.join(PKG, "_cache_binding.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -50,11 +55,34 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _newer(out: str, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
+
+
+def _binding_deps():
+    return [BINDING_SRC, os.path.join(INCLUDE, "quoka.h")]
+
+
+def _build_binding(force: bool) -> None:
+    if not force and _newer(BINDING, _binding_deps()):
+        return
+    import torch
+    home = os.path.dirname(torch.__file__)
+    paths = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+             os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           *[x for p in paths for x in ("-isystem", p)], BINDING_SRC, "-o", tmp,
+           "-L" + os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps()) and _newer(BINDING, _binding_deps())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -64,7 +92,9 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        binding = ex.submit(_build_binding, force)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -739,6 +739,10 @@ def test_calls_refuse_bad_tensors(lib):  # noqa: F811
         with pytest.raises(ValueError):
             call()
     for call in (lambda: m.quoka_cache_append(c, K, K, new_len=torch.zeros(3)),
+                 lambda: m.quoka_cache_append(c, K, None),
+                 lambda: m.quoka_cache_append(c, K, K, Q=3),
+                 lambda: m.quoka_cache_select(Q, c, 10.5, 1, 1),
+                 lambda: m.quoka_cache_attn(Q, c, 10, scale="x"),
                  lambda: m.quoka_cache_append(c, K.half(), K.half()),
                  lambda: m.quoka_cache_gather(c, 10, dtype=torch.float16),
                  lambda: m.quoka_cache_attn(Q, c, 10, lse=torch.zeros(3, 4, 7, dtype=torch.float64))):
@@ -757,7 +761,7 @@ def _cache(**kw):
 
 def test_entry_points_reject_bad_arguments_on_host(lib):  # noqa: F811
     """Every refusal comes before anything is enqueued (no GPU here)."""
-    B = lambda t: bytes(t) if isinstance(t, type(_view((1, 1, 1, 1)))) else ctypes.byref(t)
+    B = ctypes.byref
     ws, buf, out = (ctypes.c_void_p(x) for x in (0x100000, 0x200000, 0x300000))
     Q, K = _view((1, 4, 7, 128)), _view((1, 2, 7, 128), data=0x60000)
     big = 1 << 30
