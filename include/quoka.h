@@ -446,7 +446,7 @@ quoka_status quoka_cache_append(const quoka_cache* cache, const quoka_tensor* K,
  *   q_idx (b, nq, NQ) or NULL and s_agg (b, nkv, max_len) or NULL as in
  *   quoka_select; entries of kv_idx past the count and of s_agg past seq_len
  *   are left as they were. After a device fault kv_count is 0. A key whose
- *   codes are all zero scores 0.
+ *   codes are all zero scores 0, one with a NaN code -inf.
  *   ws at least quoka_select_workspace_size(b, nq, nkv, d, max_len, BCP, NQ,
  *   BSA, dtype of Q) bytes. */
 quoka_status quoka_cache_select(const quoka_tensor* Q, const quoka_cache* cache,

@@ -83,6 +83,61 @@ __device__ __forceinline__ int at_chunk(int r, int c) {
   return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
 
+// ---- Ranges: the keys of all rows (sequence, KV head) cut into runs of near
+// equal length, one CTA each. Lengths are known on the device only, so the
+// grid is an upper bound and every CTA finds its own range.
+
+struct Range {
+  int row, k0, k1;   // keys [k0, k1) of row; row < 0: none
+  int first, parts;  // the row's first range and their number
+};
+
+// Ranges asked for (before rounding up row by row), and the grid that holds
+// them: sum over rows of max(1, ceil(n / most)) <= target + rows with
+// most >= total / target, and <= rows * ceil(N / least).
+__host__ __device__ __forceinline__ int64_t range_target(int64_t rows, int ctas) {
+  return ctas - rows / 2 > ctas / 2 ? ctas - rows / 2 : ctas / 2;
+}
+__host__ __forceinline__ int64_t range_grid(int64_t rows, int N, int ctas, int least) {
+  const int64_t a = range_target(rows, ctas) + rows, b = rows * (N > least ? (N + least - 1) / least : 1);
+  return a < b ? a : b;
+}
+
+// Range `cta` (called by one warp; written to *out). keys(row): a row's keys, at
+// most 2^30. Rows are cut into equal runs of at most max(least, total / target)
+// keys, rounded up to `step`.
+template <typename Keys>
+__device__ __forceinline__ void find_range(int rows, int target, int least, int step, int cta, int lane, Keys&& keys,
+                                           Range* out) {
+  int64_t total = 0;
+  for (int i = lane; i < rows; i += 32) total += keys(i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int most = (int)min(max((int64_t)least, (total + target - 1) / target), (int64_t)1 << 30);
+  int before = 0;  // ranges of the rows before
+  if (lane == 0) out->row = -1;
+  __syncwarp();
+  for (int i0 = 0; i0 < rows; i0 += 32) {
+    const int i = i0 + lane;
+    const int n = i < rows ? keys(i) : 0;
+    const int parts = i < rows ? max(1, (n + most - 1) / most) : 0;
+    int incl = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int first = before + incl - parts;
+    if (cta >= first && cta < first + parts) {
+      const int per = ((n + parts - 1) / parts + step - 1) & ~(step - 1);
+      const int k0 = (int)min((int64_t)n, (int64_t)(cta - first) * per);
+      *out = Range{i, k0, min(n, k0 + per), first, parts};
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    if (before > cta) break;
+  }
+}
+
 // Rows of a box of the pools' tensor maps: a run of keys that starts on a
 // multiple of 64 splits into boxes of one page each.
 __host__ __device__ __forceinline__ int box_log2(const CacheView& c) { return c.page_log2 < 6 ? c.page_log2 : 6; }

@@ -64,13 +64,7 @@ constexpr int kStages = 2;
 // is off by at most 2^-25, 2^-32 of the row's largest.
 constexpr float kHead = 7.f, kLazy = 15.f;
 // One round of CTAs at three an SM, a range being at least kSplitKeys keys.
-#ifndef SPLIT_CTAS
-#define SPLIT_CTAS 444
-#endif
-#ifndef SPLIT_KEYS
-#define SPLIT_KEYS 128
-#endif
-constexpr int kSplitCTAs = SPLIT_CTAS, kSplitKeys = SPLIT_KEYS;
+constexpr int kSplitCTAs = 444, kSplitKeys = 128;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -110,7 +104,7 @@ struct Shared {
   uint64_t full[kStages], empty[kStages];
   uint32_t ex[kStages][kStage];  // scale exponents: ek + 64 in the low half, ev + 64 in the high
   int abort, fault, site;
-  int row, k0, k1;  // this CTA's range (row < 0: none)
+  Range range;  // this CTA's
 };
 
 // Keys of row `row` = sequence * nkv + head.
@@ -118,43 +112,6 @@ template <bool IDX>
 __device__ __forceinline__ int row_keys(const CacheAttnArgs& a, int row) {
   if (IDX) return min(max(__ldcg(a.kv_count + row), 0), a.N);
   return min(max(__ldcg(a.c.seq_len + row / a.c.nkv), 0), a.max_len);
-}
-
-// The range of CTA `cta` (one warp): rows are cut into ranges of at most
-// `most` keys, total / target rounded up, each row into equal ones.
-template <bool IDX>
-__device__ __forceinline__ void find_range(const CacheAttnArgs& a, Shared& sh, int cta, int lane) {
-  const int rows = a.b * a.c.nkv;
-  int64_t total = 0;
-  for (int i = lane; i < rows; i += 32) total += row_keys<IDX>(a, i);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  // (rows have at most 2^30 keys)
-  const int most = (int)min(max((int64_t)kSplitKeys, (total + a.target - 1) / a.target), (int64_t)1 << 30);
-  int before = 0;  // ranges of the rows before
-  if (lane == 0) sh.row = -1;
-  __syncwarp();
-  for (int i0 = 0; i0 < rows; i0 += 32) {
-    const int i = i0 + lane;
-    const int n = i < rows ? row_keys<IDX>(a, i) : 0;
-    const int parts = i < rows ? max(1, (n + most - 1) / most) : 0;
-    int incl = parts;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    const int first = before + incl - parts;
-    if (cta >= first && cta < first + parts) {
-      const int per = ((n + parts - 1) / parts + 63) & ~63;  // (whole boxes)
-      sh.row = i;
-      sh.k0 = min(n, (cta - first) * per);
-      sh.k1 = min(n, sh.k0 + per);
-      if (cta == first) a.row_parts[i] = make_int2(first, parts);
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
-    if (before > cta) break;
-  }
 }
 
 struct Maps {
@@ -321,10 +278,13 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
     sh.abort = sh.fault = sh.site = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 4) find_range<IDX>(a, sh, blockIdx.x, lane);
+  if (warp == 4)
+    find_range(a.b * a.c.nkv, a.target, kSplitKeys, 64, blockIdx.x, lane, [&](int row) { return row_keys<IDX>(a, row); },
+               &sh.range);
   __syncthreads();
-  const int row = sh.row, k0 = sh.k0, k1 = sh.k1;
+  const int row = sh.range.row, k0 = sh.range.k0, k1 = sh.range.k1;
   if (row < 0) return;
+  if (tid == 0 && (int)blockIdx.x == sh.range.first) a.row_parts[row] = make_int2(sh.range.first, sh.range.parts);
   const int bi = row / a.c.nkv, j = row % a.c.nkv;
 
   float o[RT][KS][4];
@@ -346,33 +306,41 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
     load_rows<D, IDX>(a, maps, sh, ring, lane, bi, j, len, k0, k1);
   } else {
     // ---- query rows: row r is head j G + r / BCP, chunk position r % BCP; a
-    // warp takes a row at a time
-    for (int r = warp; r < tiles * RT * 8; r += 4) {
-      float x[D / 32];
-      float top = 0.f;
-      const T* q = static_cast<const T*>(a.Q.data) + bi * a.Q.sb + (int64_t)(j * G + r / a.BCP) * a.Q.sh +
-                   (int64_t)(r % a.BCP) * a.Q.st;
-      // lane: columns [D / 32 * lane, + D / 32)
+    // warp takes four rows at a time, their loads together
+    for (int r4 = warp; r4 < tiles * RT * 8; r4 += 16) {
+      float x[4][D / 32];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        x[i] = r < R ? to_f32(q[D / 32 * lane + i]) : 0.f;
-        top = fmaxf(top, fabsf(x[i]));
+      for (int y = 0; y < 4; ++y) {
+        const int r = r4 + 4 * y;
+        const T* q = static_cast<const T*>(a.Q.data) + bi * a.Q.sb + (int64_t)(j * G + r / a.BCP) * a.Q.sh +
+                     (int64_t)(r % a.BCP) * a.Q.st;
+        // lane: columns [D / 32 * lane, + D / 32)
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) x[y][i] = r < R ? to_f32(q[D / 32 * lane + i]) : 0.f;
       }
 #pragma unroll
-      for (int o_ = 16; o_ > 0; o_ >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o_));
-      int e = (int)(__float_as_uint(top) >> 23) - 127 - 13;  // top * 2^-e lies in [2^13, 2^14)
-      e = min(max(e, -100), 100);                            // (zero, tiny, infinite rows)
-      const float f = exp2i(-e);
-      if (lane == 0) rowf[r] = exp2i(e) * a.scale * kLog2e;
+      for (int y = 0; y < 4; ++y) {
+        const int r = r4 + 4 * y;
+        if (r >= tiles * RT * 8) break;
+        float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < D / 32; i += 2) {
-        const int d = D / 32 * lane + i;
-        // column d belongs to chunk d / 16 = t + 4 * (ks / 4), word (d % 16) / 4 = ks % 4 of it
-        const int ch = d >> 4, ks = 4 * (ch >> 2) + ((d & 15) >> 2), reg = (d >> 1) & 1;
-        uint32_t* dst = qs + (((r >> 3) * KS + ks) * 32 + (r & 7) * 4 + (ch & 3)) * (2 * SPLIT) + reg;
-        const uint32_t hi = pack_h2(x[i] * f, x[i + 1] * f);
-        *dst = hi;
-        if constexpr (SPLIT == 2) dst[2] = rest_h2(x[i] * f, x[i + 1] * f, hi);
+        for (int i = 0; i < D / 32; ++i) top = fmaxf(top, fabsf(x[y][i]));
+#pragma unroll
+        for (int o_ = 16; o_ > 0; o_ >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o_));
+        int e = (int)(__float_as_uint(top) >> 23) - 127 - 13;  // top * 2^-e lies in [2^13, 2^14)
+        e = min(max(e, -100), 100);                            // (zero, tiny, infinite rows)
+        const float f = exp2i(-e);
+        if (lane == 0) rowf[r] = exp2i(e) * a.scale * kLog2e;
+#pragma unroll
+        for (int i = 0; i < D / 32; i += 2) {
+          const int d = D / 32 * lane + i;
+          // column d belongs to chunk d / 16 = t + 4 * (ks / 4), word (d % 16) / 4 = ks % 4 of it
+          const int ch = d >> 4, ks = 4 * (ch >> 2) + ((d & 15) >> 2), reg = (d >> 1) & 1;
+          uint32_t* dst = qs + (((r >> 3) * KS + ks) * 32 + (r & 7) * 4 + (ch & 3)) * (2 * SPLIT) + reg;
+          const uint32_t hi = pack_h2(x[y][i] * f, x[y][i + 1] * f);
+          *dst = hi;
+          if constexpr (SPLIT == 2) dst[2] = rest_h2(x[y][i] * f, x[y][i + 1] * f, hi);
+        }
       }
     }
     sm100::named_barrier_sync(1, 128);
@@ -766,15 +734,9 @@ cudaError_t launch_typed(const CacheAttnArgs& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&mc, cache_merge_kernel<T, D>, a);
 }
 
-// Ranges to cut all keys into, before rounding up row by row.
-int64_t range_target(int64_t rows) { return std::max<int64_t>(kSplitCTAs - rows / 2, kSplitCTAs / 2); }
-
 }  // namespace
 
-int64_t cache_attn_ranges(int64_t rows, int N) {
-  // sum over rows of max(1, ceil(n / most)) <= target + rows, and <= rows * ceil(N / kSplitKeys)
-  return std::min<int64_t>(range_target(rows) + rows, rows * std::max(1, (N + kSplitKeys - 1) / kSplitKeys));
-}
+int64_t cache_attn_ranges(int64_t rows, int N) { return range_grid(rows, N, kSplitCTAs, kSplitKeys); }
 
 cudaError_t launch_cache_attn(bool is_bf16, int d, const CacheAttnArgs& args, cudaStream_t stream) {
   CacheAttnArgs a = args;
@@ -782,7 +744,7 @@ cudaError_t launch_cache_attn(bool is_bf16, int d, const CacheAttnArgs& args, cu
   const int64_t rows = (int64_t)a.b * a.c.nkv, ranges = cache_attn_ranges(rows, a.N);
   if (R < 1 || R > kCacheMaxRows) return cudaErrorInvalidValue;
   if (ranges > 0x7FFFFFFF || (int64_t)a.b * a.nq * a.BCP > 0x7FFFFFFF) return cudaErrorNotSupported;
-  a.target = (int)range_target(rows);
+  a.target = (int)range_target(rows, kSplitCTAs);
   a.ranges = (int)ranges;
   if (d != 64 && d != 128) return cudaErrorNotSupported;
   if (R <= 8) {

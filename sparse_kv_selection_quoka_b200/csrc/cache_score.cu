@@ -11,8 +11,8 @@
 // diagonal of K K^T, whose operands are the registers already there: its
 // products are exact too.
 //
-// Work split. The keys of a (sequence, KV head) are cut into nsplit contiguous
-// ranges, one CTA each: a loader warp copies 128 code rows at a time into a
+// Work split. The keys of every (sequence, KV head) are cut into ranges of near
+// equal length, one CTA each (cache.cuh): a loader warp copies 128 code rows at a time into a
 // ring of stages (TMA, boxes of up to 64 rows of one page; the page table is
 // read two stages ahead), four warps take 32 of them each. Keys are the
 // rows of the product and group means its 8 columns: up to 4 group means put
@@ -39,10 +39,13 @@ constexpr int kStages = 3;
 constexpr int kQueries = 64;      // group means in shared memory at a time
 constexpr int kPacked = 4;        // up to this many fit one tile as hi and lo
 constexpr float kQScale = 4096.f;
+// One round of CTAs at three an SM, a range being at least 256 keys.
+constexpr int kSplitCTAs = 444, kSplitKeys = 256;
 
 struct Shared {
   uint64_t full[kStages], empty[kStages];
   int abort;
+  Range range;
   uint32_t hist[TOPK_HIST_BINS];
 };
 
@@ -95,7 +98,7 @@ __device__ __forceinline__ void load_rows(const CacheScoreArgs& a, const CUtenso
   if (bad) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
 }
 
-// grid (nsplit, nkv, b). PACKED: NQ <= kPacked.
+// One CTA per range. PACKED: NQ <= kPacked.
 template <int D, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const __grid_constant__ CUtensorMap map, const CacheScoreArgs a) {
   constexpr int KS = D / 16;
@@ -104,14 +107,9 @@ __global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const __grid_c
   uint8_t* ring = sm100::align_smem_1024(smem);
   uint4* qs = reinterpret_cast<uint4*>(ring + kStages * kStage * D);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int j = blockIdx.y, bi = blockIdx.z;
-  const int64_t row = (int64_t)bi * a.c.nkv + j;
   pdl_trigger();
   // (the cache, its table and lengths are inputs of the call: only the group
   // means, the histogram and the status words are waited for)
-  const int want = __ldcg(a.c.seq_len + bi), len = min(max(want, 0), a.max_len);
-  const int per = (len + a.nsplit * kStage - 1) / (a.nsplit * kStage) * kStage;
-  const int k0 = min(len, (int)blockIdx.x * per), k1 = min(len, k0 + per);
   const int passes = PACKED ? 1 : (a.NQ + kQueries - 1) / kQueries;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -122,9 +120,21 @@ __global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const __grid_c
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   for (int i = tid; i < TOPK_HIST_BINS; i += kThreads) sh.hist[i] = 0u;
+  if (warp == 4)
+    find_range(a.b * a.c.nkv, a.target, kSplitKeys, kStage, blockIdx.x, lane,
+               [&](int i) { return min(max(__ldcg(a.c.seq_len + i / a.c.nkv), 0), a.max_len); }, &sh.range);
   __syncthreads();
-  if (want != len && tid == 0) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
-
+  const int k0 = sh.range.k0, k1 = sh.range.k1;
+  if (sh.range.row < 0) {
+    pdl_wait();
+    return;
+  }
+  const int64_t row = sh.range.row;
+  const int bi = sh.range.row / a.c.nkv, j = sh.range.row % a.c.nkv;
+  if (tid == 0) {
+    const int want = __ldcg(a.c.seq_len + bi);
+    if (want < 0 || want > a.max_len) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
+  }
   if (k0 >= k1) {
     pdl_wait();
     return;
@@ -184,76 +194,115 @@ __global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const __grid_c
           break;
         }
         const uint8_t* stage = ring + st * kStage * D;
+        const int r0 = warp * 32, key = k0 + s * kStage + r0 + gk;
+        float x[2][2];   // the best of keys gk, gk + 8 of both 16-key tiles over the lane's columns
+        float k2[2][2];  // |k|^2 of the keys whose diagonal element this lane holds
+        if (PACKED) {
+          // both tiles side by side: six independent chains of products
+          float n0[2][4], n1[2][4], c[2][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int r0 = warp * 32 + m * 16, key = k0 + s * kStage + r0 + gk;
-          uint32_t kw[2][KS];
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 4; ++u) n0[m][u] = n1[m][u] = c[m][u] = 0.f;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            uint4 kw[2][2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+                kw[m][u] = *reinterpret_cast<const uint4*>(stage + at_chunk<D>(r0 + 16 * m + gk + 8 * u, t4 + 4 * h));
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int ks = (4 * h + w) % (PACKED ? KS : 1);
+#pragma unroll
+              for (int m = 0; m < 2; ++m) {
+                const uint32_t w0 = reinterpret_cast<const uint32_t*>(&kw[m][0])[w];
+                const uint32_t w1 = reinterpret_cast<const uint32_t*>(&kw[m][1])[w];
+                const uint32_t ka[4] = {e4m3x2_to_f16x2((uint16_t)w0), e4m3x2_to_f16x2((uint16_t)w1),
+                                        e4m3x2_to_f16x2((uint16_t)(w0 >> 16)), e4m3x2_to_f16x2((uint16_t)(w1 >> 16))};
+                mma_f16(c[m], ka, qb[ks][0], qb[ks][1]);
+                mma_f16(n0[m], ka, ka[0], ka[2]);
+                mma_f16(n1[m], ka, ka[1], ka[3]);
+              }
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) c[m][u] += __shfl_xor_sync(0xffffffffu, c[m][u], 2);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const bool one = 2 * (t4 & 1) < a.NQ, two = 2 * (t4 & 1) + 1 < a.NQ;
+              x[m][v] = fmaxf(one ? c[m][2 * v] : -INFINITY, two ? c[m][2 * v + 1] : -INFINITY);
+            }
+            k2[m][0] = g & 1 ? n0[m][1] : n0[m][0];
+            k2[m][1] = g & 1 ? n1[m][3] : n1[m][2];
+          }
+        } else {
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint32_t ka[KS][4];
+            float n0[4] = {0.f, 0.f, 0.f, 0.f}, n1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
-              const uint4 w = *reinterpret_cast<const uint4*>(stage + at_chunk<D>(r0 + gk + 8 * u, t4 + 4 * h));
-              kw[u][4 * h] = w.x;
-              kw[u][4 * h + 1] = w.y;
-              kw[u][4 * h + 2] = w.z;
-              kw[u][4 * h + 3] = w.w;
-            }
-          uint32_t ka[KS][4];
-          float n0[4] = {0.f, 0.f, 0.f, 0.f}, n1[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
+              const uint4 w0 = *reinterpret_cast<const uint4*>(stage + at_chunk<D>(r0 + 16 * m + gk, t4 + 4 * h));
+              const uint4 w1 = *reinterpret_cast<const uint4*>(stage + at_chunk<D>(r0 + 16 * m + gk + 8, t4 + 4 * h));
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            ka[ks][0] = e4m3x2_to_f16x2((uint16_t)kw[0][ks]);
-            ka[ks][1] = e4m3x2_to_f16x2((uint16_t)kw[1][ks]);
-            ka[ks][2] = e4m3x2_to_f16x2((uint16_t)(kw[0][ks] >> 16));
-            ka[ks][3] = e4m3x2_to_f16x2((uint16_t)(kw[1][ks] >> 16));
-            mma_f16(n0, ka[ks], ka[ks][0], ka[ks][2]);
-            mma_f16(n1, ka[ks], ka[ks][1], ka[ks][3]);
-            if (PACKED) mma_f16(c, ka[ks], qb[ks % (PACKED ? KS : 1)][0], qb[ks % (PACKED ? KS : 1)][1]);
-          }
-          float x0 = -INFINITY, x1 = -INFINITY;  // the best of keys gk, gk + 8 over the lane's columns
-          if (PACKED) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) c[u] += __shfl_xor_sync(0xffffffffu, c[u], 2);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              if (2 * (t4 & 1) + u < a.NQ) {
-                x0 = fmaxf(x0, c[u]);
-                x1 = fmaxf(x1, c[2 + u]);
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t v0 = reinterpret_cast<const uint32_t*>(&w0)[w], v1 = reinterpret_cast<const uint32_t*>(&w1)[w];
+                uint32_t* k = ka[4 * h + w];
+                k[0] = e4m3x2_to_f16x2((uint16_t)v0);
+                k[1] = e4m3x2_to_f16x2((uint16_t)v1);
+                k[2] = e4m3x2_to_f16x2((uint16_t)(v0 >> 16));
+                k[3] = e4m3x2_to_f16x2((uint16_t)(v1 >> 16));
+                mma_f16(n0, k, k[0], k[2]);
+                mma_f16(n1, k, k[1], k[3]);
               }
-          } else {
+            }
+            x[m][0] = x[m][1] = -INFINITY;
             for (int nt = 0; nt < tiles; ++nt) {
-              c[0] = c[1] = c[2] = c[3] = 0.f;
+              float c[2][4] = {};  // hi and lo apart: two chains
 #pragma unroll
               for (int ks = 0; ks < KS; ++ks) {
                 const uint4 q = qs[(nt * KS + ks) * 32 + lane];
-                mma_f16(c, ka[ks], q.x, q.y);
-                mma_f16(c, ka[ks], q.z, q.w);
+                mma_f16(c[0], ka[ks], q.x, q.y);
+                mma_f16(c[1], ka[ks], q.z, q.w);
               }
 #pragma unroll
               for (int u = 0; u < 2; ++u)
                 if (8 * nt + 2 * t4 + u < nq) {
-                  x0 = fmaxf(x0, c[u]);
-                  x1 = fmaxf(x1, c[2 + u]);
+                  x[m][0] = fmaxf(x[m][0], c[0][u] + c[1][u]);
+                  x[m][1] = fmaxf(x[m][1], c[0][2 + u] + c[1][2 + u]);
                 }
             }
-            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+            k2[m][0] = g & 1 ? n0[1] : n0[0];
+            k2[m][1] = g & 1 ? n1[3] : n1[2];
           }
-          x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-          if (t4 == (g >> 1)) {  // the lane that holds the diagonal's g-th element
-            const float q0 = g & 1 ? n0[1] : n0[0], q1 = g & 1 ? n1[3] : n1[2];
-            float* S = a.S_agg + row * a.max_len + key;
-            auto put = [&](int at, float x, float k2) {
-              if (key + at >= k1) return;
-              x = x * (1.f / kQScale) / fmaxf(sqrtf(k2), 1e-12f);
-              if (!PACKED && pass > 0) x = fmaxf(x, S[at]);  // (this thread's own score of the passes before)
-              S[at] = x;
-              if (pass == passes - 1) atomicAdd(&sh.hist[score_bin(x)], 1u);
-            };
-            put(0, x0, q0);
-            put(8, x1, q1);
-          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) x[m][v] = fmaxf(x[m][v], __shfl_xor_sync(0xffffffffu, x[m][v], 2));
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) x[m][v] = fmaxf(x[m][v], __shfl_xor_sync(0xffffffffu, x[m][v], 1));
+        if (t4 == (g >> 1)) {  // the lane that holds the diagonal's g-th element
+          float* S = a.S_agg + row * a.max_len + key;
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const int at = 16 * m + 8 * v;
+              if (key + at >= k1) continue;
+              // (rsqrt is within 2^-22; a key of zeros scores 0, one with a NaN -inf)
+              const float n = k2[m][v];
+              float y = n > 0.f ? x[m][v] * (1.f / kQScale) * rsqrtf(n) : n == 0.f ? 0.f : -INFINITY;
+              if (!PACKED && pass > 0) y = fmaxf(y, S[at]);  // (this thread's own score of the passes before)
+              S[at] = y;
+              if (pass == passes - 1) atomicAdd(&sh.hist[score_bin(y)], 1u);
+            }
         }
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&sh.empty[st]);
@@ -269,15 +318,12 @@ __global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const __grid_c
   }
 }
 
-// One round of CTAs at three an SM, a range being at least 256 keys.
-constexpr int kSplitCTAs = 444, kSplitKeys = 256;
-
 template <int D>
 cudaError_t launch_typed(const CacheScoreArgs& args, cudaStream_t stream) {
   CacheScoreArgs a = args;
-  const int64_t heads = (int64_t)a.b * a.c.nkv;
-  const int64_t want = (kSplitCTAs + heads - 1) / heads, most = (a.max_len + kSplitKeys - 1) / kSplitKeys;
-  a.nsplit = (int)(want < most ? want : most);
+  const int64_t rows = (int64_t)a.b * a.c.nkv, ranges = range_grid(rows, a.max_len, kSplitCTAs, kSplitKeys);
+  if (ranges > 0x7FFFFFFF) return cudaErrorNotSupported;
+  a.target = (int)range_target(rows, kSplitCTAs);
   auto* kern = a.NQ <= kPacked ? cache_score_kernel<D, true> : cache_score_kernel<D, false>;
   const size_t smem = smem_bytes<D>(a.NQ);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -289,7 +335,7 @@ cudaError_t launch_typed(const CacheScoreArgs& args, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.nsplit, a.c.nkv, a.b);
+  cfg.gridDim = dim3((unsigned)ranges);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

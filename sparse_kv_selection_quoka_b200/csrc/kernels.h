@@ -245,7 +245,7 @@ struct CacheScoreArgs {
   float* S_agg;
   uint32_t* hist;
   int* status;
-  int nsplit = 1;  // ranges of a row's keys (set by the launcher)
+  int target = 1;  // ranges asked for (set by the launcher)
 };
 cudaError_t launch_cache_score(int d, const CacheScoreArgs& a, cudaStream_t stream);
 

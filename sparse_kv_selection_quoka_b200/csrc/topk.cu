@@ -31,6 +31,8 @@
 // the cluster through distributed shared memory.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -45,6 +47,7 @@ constexpr int TOPK_WARPS = TOPK_THREADS / 32;
 constexpr int TOPK_MAX_CLUSTER = 8;
 constexpr int TOPK_MAX_SLICE = 36 * 1024;  // keys per CTA (144 KiB of shared memory; 208 KiB in all)
 constexpr int TOPK_SLICE_TARGET = 4096;    // keys per CTA while the cluster can spread them
+constexpr int TOPK_SMS = 148;
 constexpr int TOPK_LIST_MAX = 4096;        // candidates gathered in every CTA
 constexpr int TOPK_BINS = 4096;            // widest digit: 12 bits
 static_assert(TOPK_BINS / TOPK_THREADS <= 4, "bins per thread in a pick");
@@ -603,6 +606,11 @@ cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, 
   // reach; `status` is only read, to skip the select after an earlier fault)
   if (bsa <= 0 || T <= 0 || bsa > T || T > topk_max_T()) return cudaErrorInvalidValue;
   int C = (int)((T + TOPK_SLICE_TARGET - 1) / TOPK_SLICE_TARGET);
+  // no more CTAs than SMs while the slices allow it: two on an SM only slow
+  // each other's phases (issue- and barrier-bound)
+  const int64_t rows = (int64_t)b * nkv;
+  const int fit = std::max(rows < TOPK_SMS ? (int)(TOPK_SMS / rows) : 1, (int)((T + TOPK_MAX_SLICE - 1) / TOPK_MAX_SLICE));
+  if (C > fit) C = fit;
   if (C > TOPK_MAX_CLUSTER) C = TOPK_MAX_CLUSTER;
   if (C < 1) C = 1;
   const int slice = (int)((T + C - 1) / C);
