@@ -90,10 +90,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
 // MMA warp; one elected lane issues.
 
 // S[:, 0:128) = Q K^T for a 128-row Q tile and a 128-key K tile, both in
-// shared memory in the 128-byte-swizzled K-major layout (two 64-column atoms).
+// shared memory in the 128-byte-swizzled K-major layout (two 64-column atoms;
+// head dim HD = 64: the first).
+template <int HD = D>
 __device__ __forceinline__ void issue_qk(uint32_t tmem_s, uint32_t q_smem, uint32_t k_smem) {
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
+  for (int kk = 0; kk < HD / 16; ++kk) {
     const uint32_t koff = (kk >> 2) * ATOM_BYTES + (kk & 3) * 32;
     umma_bf16_ss_warp(tmem_s, sw128_desc(q_smem + koff, 16, 1024), sw128_desc(k_smem + koff, 16, 1024), IDESC_QK,
                  kk > 0 ? 1u : 0u);
@@ -111,14 +113,15 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint32_t tmem_p, uint3
 
 // Part `part` of O (+)= P V when the 128 keys are released in PARTS
 // equal parts: the K = 16 steps of keys [part * N / PARTS, (part + 1) * N / PARTS).
-template <int PARTS>
+template <int PARTS, int HD = D>
 __device__ __forceinline__ void issue_pv_part(uint32_t tmem_o, uint32_t tmem_p, uint32_t v_smem, int part,
                                               bool accumulate) {
   constexpr int KK = N / 16 / PARTS;
+  constexpr uint32_t IDESC = idesc_bf16_f32(128, HD, 0, 1);
 #pragma unroll
   for (int q = 0; q < KK; ++q) {
     const int kk = part * KK + q;
-    umma_bf16_ts_warp(tmem_o, tmem_p + kk * 8, sw128_desc(v_smem + kk * 2048, ATOM_BYTES, 1024), IDESC_PV,
+    umma_bf16_ts_warp(tmem_o, tmem_p + kk * 8, sw128_desc(v_smem + kk * 2048, ATOM_BYTES, 1024), IDESC,
                  (accumulate || kk > 0) ? 1u : 0u);
   }
 }
@@ -137,7 +140,7 @@ __device__ __forceinline__ void issue_pv_part(uint32_t tmem_o, uint32_t tmem_p, 
 // product of the first keys runs while the later ones are still being
 // exponentiated. Updates m and l. TMEM accesses are warp-collective: no
 // per-row branch surrounds one.
-template <int PARTS>
+template <int PARTS, int HD = D>
 __device__ __forceinline__ void softmax_tile_split(uint32_t S, uint32_t O, bool have_o, int base_n, int lim,
                                                    float qscale, float& m, float& l, uint64_t* p_part) {
   constexpr int CPP = 4 / PARTS;  // 32-key chunks per part
@@ -165,7 +168,7 @@ __device__ __forceinline__ void softmax_tile_split(uint32_t S, uint32_t O, bool 
   // warp-uniform condition: the rescale's TMEM traffic is collective
   if (have_o && __any_sync(0xffffffffu, corr != 1.f)) {
 #pragma unroll 1
-    for (int c4 = 0; c4 < 4; ++c4) {
+    for (int c4 = 0; c4 < HD / 32; ++c4) {
       float o[32];
       tmem_ld32(O + 32 * c4, o);
       tmem_wait_ld();

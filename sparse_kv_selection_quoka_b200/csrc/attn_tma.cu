@@ -22,6 +22,10 @@
 // softmax. After the last tile the two partial results of every row are in
 // the same SM's TMEM and are combined there.
 //
+// Head dim 64 (a.d = 64, only for callers that ask for it) is the same kernel
+// on the first 64-column atom of every tile: 4 k-steps of Q K^T, 64 columns of
+// O, half the bytes.
+//
 // Split key ranges: when the query tiles alone leave most SMs idle (short
 // chunks, few heads), each query tile's key tiles are cut into nsplit
 // contiguous ranges and the grid runs one CTA per (tile, range). Such a CTA
@@ -92,11 +96,12 @@ struct __align__(1024) Smem {
   uint64_t wait_ns;  // bound of every wait
 };
 
-// TMA boxes of one 128-row tile (two 64-column atoms).
+// TMA boxes of one 128-row tile (HD / 64 atoms of 64 columns).
+template <int HD>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int y, int j, int bi) {
-  mbar_arrive_expect_tx(bar, TILE_BYTES);
+  mbar_arrive_expect_tx(bar, HD / 64 * ATOM_BYTES);
   tma_load_4d(dst, m, bar, 0, y, j, bi);
-  tma_load_4d(dst + ATOM_BYTES, m, bar, 64, y, j, bi);
+  if constexpr (HD == 128) tma_load_4d(dst + ATOM_BYTES, m, bar, 64, y, j, bi);
 }
 
 // Waits, bounded, until the last copy into each stage of a ring has landed
@@ -118,7 +123,7 @@ __device__ __forceinline__ void drain_ring(Smem& sm, uint64_t* full, int nload, 
 // next one, so both come before the QK^T of tile kt - 1: the loads never
 // wait on a product that waits on a later load. With a thread per ring, a K
 // load never queues behind a V stage that is released later.
-template <bool IS_V>
+template <bool IS_V, int HD>
 __device__ __forceinline__ void load_kv(Smem& sm, const Maps& maps, int nT, int kt_base, int ntile_sel, int j,
                                         int bi, int* status) {
   constexpr int ST = IS_V ? VST : KST;
@@ -133,7 +138,7 @@ __device__ __forceinline__ void load_kv(Smem& sm, const Maps& maps, int nT, int 
       break;
     }
     const CUtensorMap* m = IS_V ? (sel_tile ? &maps.vs : &maps.vc) : (sel_tile ? &maps.ks : &maps.kc);
-    load_tile(smem_u32(IS_V ? sm.v[s] : sm.k[s]), m, &full[s],
+    load_tile<HD>(smem_u32(IS_V ? sm.v[s] : sm.k[s]), m, &full[s],
               (sel_tile ? kt_base + kt : kt_base + kt - ntile_sel) * N, j, bi);
     nl = kt + 1;
   }
@@ -141,6 +146,7 @@ __device__ __forceinline__ void load_kv(Smem& sm, const Maps& maps, int nT, int 
   if (!IS_V && !mbar_drain(&sm.q_full, 0, sm.wait_ns)) record_abort(sm, status, 13);
 }
 
+template <int HD>
 __global__ void __launch_bounds__(THREADS, 1)
 attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -193,9 +199,7 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     tma_prefetch_desc(&maps.kc);
     tma_prefetch_desc(&maps.vc);
     tma_prefetch_desc(&maps.o);
-    mbar_arrive_expect_tx(&sm.q_full, TILE_BYTES);
-    tma_load_4d(smem_u32(sm.q), &maps.q, &sm.q_full, 0, t0, h, bi);
-    tma_load_4d(smem_u32(sm.q) + ATOM_BYTES, &maps.q, &sm.q_full, 64, t0, h, bi);
+    load_tile<HD>(smem_u32(sm.q), &maps.q, &sm.q_full, t0, h, bi);
   }
 
   pdl_wait();  // the gathered rows and their counts come from the previous kernel
@@ -211,10 +215,10 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
 
   if (warp == LOAD_WARP) {
     // ------------------------------------------------------------ TMA loads
-    if (lane == 0) load_kv<false>(sm, maps, nT, kt_base, ntile_sel, j, bi, a.status);
+    if (lane == 0) load_kv<false, HD>(sm, maps, nT, kt_base, ntile_sel, j, bi, a.status);
     __syncwarp();
   } else if (warp == VLOAD_WARP) {
-    if (lane == 0) load_kv<true>(sm, maps, nT, kt_base, ntile_sel, j, bi, a.status);
+    if (lane == 0) load_kv<true, HD>(sm, maps, nT, kt_base, ntile_sel, j, bi, a.status);
     __syncwarp();
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issue
@@ -227,7 +231,7 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
       const int ks = kt % KST;
       if (!mbar_wait_warp(&sm.k_full[ks], (kt / KST) & 1, &sm.abort, sm.wait_ns)) return false;
       tc_fence_after();
-      issue_qk(tmem + 128u * w, q0, smem_u32(sm.k[ks]));
+      issue_qk<HD>(tmem + 128u * w, q0, smem_u32(sm.k[ks]));
       umma_commit_warp(&sm.s_full[w]);
       umma_commit_warp(&sm.k_empty[ks]);
       return true;
@@ -241,7 +245,7 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
       for (int c = 0; c < PV_PARTS; ++c) {
         if (!mbar_wait_warp(&sm.p_part[w][c], i & 1, &sm.abort, sm.wait_ns)) return false;
         tc_fence_after();
-        issue_pv_part<PV_PARTS>(tmem + 256u + 128u * w, tmem + 128u * w, smem_u32(sm.v[vs]), c, i > 0);
+        issue_pv_part<PV_PARTS, HD>(tmem + 256u + 128u * w, tmem + 128u * w, smem_u32(sm.v[vs]), c, i > 0);
       }
       umma_commit_warp(&sm.v_empty[vs]);
       return true;
@@ -303,7 +307,7 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
       // p < nchunk with p <= t
       const int base_n = (sel_tile ? kt : kt - sel_rel) * N;
       const int lim = sel_tile ? nsel_rel : min(nchunk, t + 1);
-      softmax_tile_split<PV_PARTS>(S, tmem + lane_off + 256u + 128u * w, i > 0, base_n, lim,
+      softmax_tile_split<PV_PARTS, HD>(S, tmem + lane_off + 256u + 128u * w, i > 0, base_n, lim,
                                                      qscale, m, l, sm.p_part[w]);
     }
 
@@ -327,14 +331,14 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     const float L = f0 * l0 + f1 * l1;
     const float inv = L > 0.f ? 1.f / L : 0.f;  // no visible key: O = 0, lse = -inf
     // warpgroup w combines, normalises and stages output columns
-    // [64w, 64w + 64) of its rows, bf16, in the 128-byte-swizzled layout the
+    // [HD / 2 w, + HD / 2) of its rows, bf16, in the 128-byte-swizzled layout the
     // TMA store reads (the Q area: every MMA is done); a key range of a split
     // tile stores them to its partial output instead
-    const uint32_t O0 = tmem + lane_off + 256u + 64u * w;
-    const uint32_t O1 = tmem + lane_off + 384u + 64u * w;
+    const uint32_t O0 = tmem + lane_off + 256u + HD / 2 * w;
+    const uint32_t O1 = tmem + lane_off + 384u + HD / 2 * w;
     const bool part = a.nsplit > 1;
 #pragma unroll 1
-    for (int c2 = 0; c2 < 2; ++c2) {
+    for (int c2 = 0; c2 < HD / 64; ++c2) {
       float o[32], p[32];
       if (have0) tmem_ld32(O0 + 32 * c2, o);
       if (have1) tmem_ld32(O1 + 32 * c2, p);
@@ -354,7 +358,7 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         pk.y = pack_bf16x2((o[u + 2] * f0 + p[u + 2] * f1) * inv, (o[u + 3] * f0 + p[u + 3] * f1) * inv);
         pk.z = pack_bf16x2((o[u + 4] * f0 + p[u + 4] * f1) * inv, (o[u + 5] * f0 + p[u + 5] * f1) * inv);
         pk.w = pack_bf16x2((o[u + 6] * f0 + p[u + 6] * f1) * inv, (o[u + 7] * f0 + p[u + 7] * f1) * inv);
-        *reinterpret_cast<uint4*>(sm.q + sw128_offset(r, (64 * w + 32 * c2 + u) >> 3, 128)) = pk;
+        *reinterpret_cast<uint4*>(sm.q + sw128_offset(r, (HD / 2 * w + 32 * c2 + u) >> 3, 128)) = pk;
       }
     }
     if (w == 0 && t < a.BCP) {
@@ -373,7 +377,7 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
       const CUtensorMap* om = part ? &maps.op : &maps.o;
       const int zb = part ? split * a.b + bi : bi;
       tma_store_4d(om, smem_u32(sm.q), 0, t0, h, zb);
-      tma_store_4d(om, smem_u32(sm.q) + ATOM_BYTES, 64, t0, h, zb);
+      if constexpr (HD == 128) tma_store_4d(om, smem_u32(sm.q) + ATOM_BYTES, 64, t0, h, zb);
       bulk_commit_group();
       bulk_wait_group_read_0();  // the staging may go once the copy has read it
     }
@@ -392,14 +396,15 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
 // row with none gives O = 0, lse = -inf.
 constexpr int kMergeThreads = 256;
 
+template <int HD>
 __global__ void __launch_bounds__(kMergeThreads)
 attn_split_merge_kernel(const bf16* __restrict__ O_parts, const float* __restrict__ lse_parts, int nsplit,
                         int64_t rows, bf16* __restrict__ O, float* __restrict__ lse) {
   pdl_wait();  // the partials come from the attention kernel
   const int64_t g = (int64_t)blockIdx.x * kMergeThreads + threadIdx.x;
-  if (g >= rows * (D / 8)) return;
-  const int64_t row = g / (D / 8);
-  const int c0 = (int)(g % (D / 8)) * 8;
+  if (g >= rows * (HD / 8)) return;
+  const int64_t row = g / (HD / 8);
+  const int c0 = (int)(g % (HD / 8)) * 8;
   float ls[4];
   float M = -INFINITY;
 #pragma unroll
@@ -414,7 +419,7 @@ attn_split_merge_kernel(const bf16* __restrict__ O_parts, const float* __restric
     if (ls[s] == -INFINITY) continue;
     const float wgt = __expf(ls[s] - M);
     L += wgt;
-    const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(O_parts + ((int64_t)s * rows + row) * D + c0));
+    const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(O_parts + ((int64_t)s * rows + row) * HD + c0));
     const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -428,7 +433,7 @@ attn_split_merge_kernel(const bf16* __restrict__ O_parts, const float* __restric
   pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
   pk.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
   pk.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-  *reinterpret_cast<uint4*>(O + row * D + c0) = pk;
+  *reinterpret_cast<uint4*>(O + row * HD + c0) = pk;
   if (c0 == 0 && lse != nullptr) lse[row] = L > 0.f ? M + __logf(L) : -INFINITY;
 }
 
@@ -441,10 +446,10 @@ int attn_splits(int64_t tiles, int nt) {
   return s < 2 ? 1 : s;
 }
 
-cudaError_t launch_attn_tc(const AttnArgs& args, bool pdl, cudaStream_t stream) {
-  if (args.d != D) return cudaErrorNotSupported;
-  // rows gathered by index while loading: the other kernel
-  if (args.kv_idx != nullptr && args.bsa > 0) return launch_attn_tc_gather(args, stream);
+namespace {
+
+template <int HD>
+cudaError_t launch_tma(const AttnArgs& args, bool pdl, cudaStream_t stream) {
   AttnArgs a = args;
   if (a.nsplit < 1 || a.nsplit > 4 || (a.nsplit > 1 && (a.O_parts == nullptr || a.lse_parts == nullptr)))
     return cudaErrorInvalidValue;
@@ -452,29 +457,29 @@ cudaError_t launch_attn_tc(const AttnArgs& args, bool pdl, cudaStream_t stream) 
   a.wait_ns = hooks.wait_ns;
   a.inject = hooks.inject == INJECT_ATTN_TMA ? 1 : 0;
   Maps maps;
-  const int64_t oh = (int64_t)a.BCP * D, ob = (int64_t)a.nq * oh;  // O is contiguous
-  if (!encode_bf16_4d(&maps.q, a.Q.data, D, a.BCP, a.nq, a.b, a.Q.st, a.Q.sh, a.Q.sb, 128) ||
-      !encode_bf16_4d(&maps.kc, a.Kc.data, D, a.BCP, a.nkv, a.b, a.Kc.st, a.Kc.sh, a.Kc.sb, 128) ||
-      !encode_bf16_4d(&maps.vc, a.Vc.data, D, a.BCP, a.nkv, a.b, a.Vc.st, a.Vc.sh, a.Vc.sb, 128) ||
-      !encode_bf16_4d(&maps.o, a.O, D, a.BCP, a.nq, a.b, D, oh, ob, 128))
+  const int64_t oh = (int64_t)a.BCP * HD, ob = (int64_t)a.nq * oh;  // O is contiguous
+  if (!encode_bf16_4d(&maps.q, a.Q.data, HD, a.BCP, a.nq, a.b, a.Q.st, a.Q.sh, a.Q.sb, 128) ||
+      !encode_bf16_4d(&maps.kc, a.Kc.data, HD, a.BCP, a.nkv, a.b, a.Kc.st, a.Kc.sh, a.Kc.sb, 128) ||
+      !encode_bf16_4d(&maps.vc, a.Vc.data, HD, a.BCP, a.nkv, a.b, a.Vc.st, a.Vc.sh, a.Vc.sb, 128) ||
+      !encode_bf16_4d(&maps.o, a.O, HD, a.BCP, a.nq, a.b, HD, oh, ob, 128))
     return cudaErrorNotSupported;
   if (a.nsplit > 1) {
-    if (!encode_bf16_4d(&maps.op, a.O_parts, D, a.BCP, a.nq, (uint64_t)a.nsplit * a.b, D, oh, ob, 128))
+    if (!encode_bf16_4d(&maps.op, a.O_parts, HD, a.BCP, a.nq, (uint64_t)a.nsplit * a.b, HD, oh, ob, 128))
       return cudaErrorNotSupported;
   } else {
     maps.op = maps.o;  // never written
   }
   if (a.bsa > 0) {
     // the gathered selected rows (b, nkv, bsa, d)
-    if (!encode_bf16_4d(&maps.ks, a.K.data, D, a.bsa, a.nkv, a.b, a.K.st, a.K.sh, a.K.sb, 128) ||
-        !encode_bf16_4d(&maps.vs, a.V.data, D, a.bsa, a.nkv, a.b, a.V.st, a.V.sh, a.V.sb, 128))
+    if (!encode_bf16_4d(&maps.ks, a.K.data, HD, a.bsa, a.nkv, a.b, a.K.st, a.K.sh, a.K.sb, 128) ||
+        !encode_bf16_4d(&maps.vs, a.V.data, HD, a.bsa, a.nkv, a.b, a.V.st, a.V.sh, a.V.sb, 128))
       return cudaErrorNotSupported;
   } else {
     maps.ks = maps.kc;  // never read: there are no selected tiles
     maps.vs = maps.vc;
   }
   const size_t smem = sizeof(Smem) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(attn_tma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(attn_tma_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int G = a.nq / a.nkv;
   cudaLaunchConfig_t cfg = {};
@@ -487,18 +492,27 @@ cudaError_t launch_attn_tc(const AttnArgs& args, bool pdl, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, attn_tma_kernel, maps, a);
+  e = cudaLaunchKernelEx(&cfg, attn_tma_kernel<HD>, maps, a);
   if (e != cudaSuccess || a.nsplit == 1) return e;
   const int64_t rows = (int64_t)a.b * a.nq * a.BCP;
   cudaLaunchConfig_t mc = {};
-  mc.gridDim = dim3((unsigned)((rows * (D / 8) + kMergeThreads - 1) / kMergeThreads));
+  mc.gridDim = dim3((unsigned)((rows * (HD / 8) + kMergeThreads - 1) / kMergeThreads));
   mc.blockDim = dim3(kMergeThreads);
   mc.stream = stream;
   mc.attrs = attr;
   mc.numAttrs = 1;  // waits for the attention inside
-  return cudaLaunchKernelEx(&mc, attn_split_merge_kernel, static_cast<const bf16*>(a.O_parts),
+  return cudaLaunchKernelEx(&mc, attn_split_merge_kernel<HD>, static_cast<const bf16*>(a.O_parts),
                             static_cast<const float*>(a.lse_parts), a.nsplit, rows, static_cast<bf16*>(a.O),
                             a.lse);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs& a, bool pdl, cudaStream_t stream) {
+  if (a.d != D && !(a.d == 64 && a.tc_d64)) return cudaErrorNotSupported;
+  // rows gathered by index while loading: the other kernel
+  if (a.kv_idx != nullptr && a.bsa > 0) return a.d == D ? launch_attn_tc_gather(a, stream) : cudaErrorNotSupported;
+  return a.d == D ? launch_tma<D>(a, pdl, stream) : launch_tma<64>(a, pdl, stream);
 }
 
 }  // namespace quoka

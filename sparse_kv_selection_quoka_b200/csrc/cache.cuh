@@ -96,7 +96,7 @@ struct Range {
 // them: sum over rows of max(1, ceil(n / most)) <= target + rows with
 // most >= total / target, and <= rows * ceil(N / least).
 __host__ __device__ __forceinline__ int64_t range_target(int64_t rows, int ctas) {
-  return ctas - rows / 2 > ctas / 2 ? ctas - rows / 2 : ctas / 2;
+  return ctas - rows / 2 > ctas / 2 ? ctas - rows / 2 : ctas / 2;  // (ctas >= 2)
 }
 __host__ __forceinline__ int64_t range_grid(int64_t rows, int N, int ctas, int least) {
   const int64_t a = range_target(rows, ctas) + rows, b = rows * (N > least ? (N + least - 1) / least : 1);

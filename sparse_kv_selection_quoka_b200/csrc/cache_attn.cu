@@ -1,5 +1,5 @@
-// GQA attention of a few query rows over the paged 8-bit cache: decode steps
-// and short blocks (G * BCP <= 64 query rows per KV head).
+// GQA attention over the paged 8-bit cache straight from its codes: decode steps
+// and short blocks (G * BCP <= 64 query rows per KV head), and all fp32 queries.
 //
 // [QUOKA §4.2, problem 3] the attention of the other paths,
 //   O[b,h,t] = sum_k softmax_k(scale * q . k) v,  j = floor(h / G),
@@ -63,8 +63,10 @@ constexpr int kStages = 2;
 // stay below 2^15 (fp16 holds 65504), and one that fp16 holds as a subnormal
 // is off by at most 2^-25, 2^-32 of the row's largest.
 constexpr float kHead = 7.f, kLazy = 15.f;
-// One round of CTAs at three an SM, a range being at least kSplitKeys keys.
-constexpr int kSplitCTAs = 444, kSplitKeys = 128;
+constexpr int kSplitKeys = 128;    // a range has at least this many keys
+constexpr int kBlockRows = 64;     // query rows of a CTA
+constexpr int kMaxCTAs = 444;      // resident at once, at most
+constexpr int kMaxParts = 448;     // ranges of a row: at most the ranges asked for, <= kMaxCTAs
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -254,7 +256,7 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
   if (__any_sync(0xffffffffu, bad) && lane == 0 && sh.fault == 0) sh.fault = 6;  // QUOKA_ERR_BOUNDS
 }
 
-// One CTA per range. RT: 8-row query tiles of a warp.
+// One CTA per range and block of 64 query rows. RT: 8-row query tiles of a warp.
 template <typename T, int D, bool IDX, int RT>
 __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
   constexpr int SPLIT = sizeof(T) == 2 ? 1 : 2;
@@ -264,6 +266,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int G = a.nq / a.c.nkv, R = G * a.BCP;
+  const int blocks = (R + kBlockRows - 1) / kBlockRows, range = blockIdx.x / blocks;
+  const int rb = (int)blockIdx.x % blocks * kBlockRows, Rb = min(R - rb, kBlockRows);  // this block's rows
   const int tiles = RT == 1 || R <= 16 ? 1 : R <= 32 ? 2 : 4;  // (a third tile alone would leave a warp idle as well)
   uint8_t* ring = sm100::align_smem_1024(smem);
   uint32_t* qs = reinterpret_cast<uint32_t*>(ring + Rg::kTotal);
@@ -279,12 +283,13 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 4)
-    find_range(a.b * a.c.nkv, a.target, kSplitKeys, 64, blockIdx.x, lane, [&](int row) { return row_keys<IDX>(a, row); },
+    find_range(a.b * a.c.nkv, a.target, kSplitKeys, 64, range, lane, [&](int row) { return row_keys<IDX>(a, row); },
                &sh.range);
   __syncthreads();
   const int row = sh.range.row, k0 = sh.range.k0, k1 = sh.range.k1;
   if (row < 0) return;
-  if (tid == 0 && (int)blockIdx.x == sh.range.first) a.row_parts[row] = make_int2(sh.range.first, sh.range.parts);
+  if (tid == 0 && rb == 0 && range == sh.range.first)
+    a.row_parts[row] = make_int2(sh.range.first, sh.range.parts);
   const int bi = row / a.c.nkv, j = row % a.c.nkv;
 
   float o[RT][KS][4];
@@ -305,18 +310,18 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
     if (want != len && lane == 0) sh.fault = 6;  // QUOKA_ERR_BOUNDS
     load_rows<D, IDX>(a, maps, sh, ring, lane, bi, j, len, k0, k1);
   } else {
-    // ---- query rows: row r is head j G + r / BCP, chunk position r % BCP; a
+    // ---- query rows: row r is head j G + (rb + r) / BCP, chunk position (rb + r) % BCP; a
     // warp takes four rows at a time, their loads together
     for (int r4 = warp; r4 < tiles * RT * 8; r4 += 16) {
       float x[4][D / 32];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int r = r4 + 4 * y;
-        const T* q = static_cast<const T*>(a.Q.data) + bi * a.Q.sb + (int64_t)(j * G + r / a.BCP) * a.Q.sh +
-                     (int64_t)(r % a.BCP) * a.Q.st;
+        const T* q = static_cast<const T*>(a.Q.data) + bi * a.Q.sb + (int64_t)(j * G + (rb + r) / a.BCP) * a.Q.sh +
+                     (int64_t)((rb + r) % a.BCP) * a.Q.st;
         // lane: columns [D / 32 * lane, + D / 32)
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) x[y][i] = r < R ? to_f32(q[D / 32 * lane + i]) : 0.f;
+        for (int i = 0; i < D / 32; ++i) x[y][i] = r < Rb ? to_f32(q[D / 32 * lane + i]) : 0.f;
       }
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
@@ -540,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
           ml[(warp * TR + r) * 2] = m[rt][i];
           ml[(warp * TR + r) * 2 + 1] = l[rt][i];
         }
-        if (tile * TR + r < R) {  // columns [D / 8 * g, + D / 8)
+        if (tile * TR + r < Rb) {  // columns [D / 8 * g, + D / 8)
           float4* dst = reinterpret_cast<float4*>(os + (warp * TR + r) * D + D / 8 * g);
 #pragma unroll
           for (int k = 0; k < KS; k += 2)
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
       }
   }
   __syncthreads();
-  for (int e = tid; e < R * (D / 4); e += kThreads) {
+  for (int e = tid; e < Rb * (D / 4); e += kThreads) {
     const int r = e / (D / 4), c4 = e % (D / 4);
     const int tl = r / TR, rr = r % TR;
     float M = -INFINITY;
@@ -569,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
       x.w = fmaf(fw, y.w, x.w);
     }
     const float inv = L != 0.f ? 1.f / L : 0.f;
-    const int64_t at = (int64_t)blockIdx.x * R + r;
+    const int64_t at = (int64_t)range * R + rb + r;
     *reinterpret_cast<float4*>(a.O_parts + at * D + 4 * c4) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     // log2 of the range's partition function (-inf: no key)
     if (c4 == 0) a.lse_parts[at] = L != 0.f ? M + log2f(L) : -INFINITY;
@@ -580,9 +585,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
 // Joins the ranges of one query row, adds the chunk's own keys s <= t, and
 // writes the row: O = sum_i 2^(x_i - X) O_i, X = log2 sum_i 2^(x_i). One CTA
 // per row: a thread owns four columns of every kGroups-th range and chunk
-// key, so that a row's partials are fetched in one or two rounds of loads.
-constexpr int kMergeThreads = 128;
-
+// key. The first ranges' outputs are fetched together with all sums, so that
+// a row usually costs one round of loads.
 __device__ __forceinline__ float4 ld4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float4 ld4(const bf16* p) {
   const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
@@ -598,18 +602,24 @@ __device__ __forceinline__ void st4(bf16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = o;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheAttnArgs a) {
-  constexpr int C4 = D / 4, kGroups = kMergeThreads / C4;
+// MT threads.
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(MT) cache_merge_kernel(const CacheAttnArgs a) {
+  constexpr int C4 = D / 4, kGroups = MT / C4, kWarps = MT / 32;
+  constexpr int kOwn = 8;  // ranges a group fetches ahead
   __shared__ float4 acc[kGroups][C4];
-  __shared__ float sc[kCacheMaxRows];
+  __shared__ float sw[kMaxParts];
+  __shared__ float red[2][kWarps];
+  extern __shared__ float sc[];  // the chunk's keys: scores, then weights
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c4 = tid % C4, grp = tid / C4;
   const int t = (int)(row % a.BCP), h = (int)(row / a.BCP % a.nq), bi = (int)(row / a.BCP / a.nq);
   const int G = a.nq / a.c.nkv, j = h / G, R = G * a.BCP;
   const int nc = a.chunk ? t + 1 : 0;
-  const T* vc = static_cast<const T*>(a.Vc.data) + bi * a.Vc.sb + j * a.Vc.sh;
+  const T* vc = static_cast<const T*>(a.Vc.data) + bi * a.Vc.sb + j * a.Vc.sh + 4 * c4;
+  float4 v0 = make_float4(0.f, 0.f, 0.f, 0.f);
   if (nc > 0) {  // (inputs of the call: read before the partials are waited for)
+    if (grp < nc) v0 = ld4(vc + grp * a.Vc.st);
     // scores of the chunk's keys in log2 units: eight lanes a key
     constexpr int W = D / 8;
     const int part = lane & 7;
@@ -618,7 +628,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     float4 qv[W / 4];
 #pragma unroll
     for (int i = 0; i < W / 4; ++i) qv[i] = ld4(q + 4 * i);
-    for (int k = warp * 4 + (lane >> 3); k < (nc + 3) / 4 * 4; k += kMergeThreads / 8) {
+    for (int k = warp * 4 + (lane >> 3); k < (nc + 3) / 4 * 4; k += MT / 8) {
       float x = 0.f;
       if (k < nc) {
 #pragma unroll
@@ -637,27 +647,39 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     __syncthreads();
   }
   pdl_wait();
-  const int2 parts = __ldcg(a.row_parts + bi * a.c.nkv + j);  // first range and their number
+  int2 parts = __ldcg(a.row_parts + bi * a.c.nkv + j);  // first range and their number
+  parts.y = min(parts.y, kMaxParts);
   const int64_t at = (int64_t)parts.x * R + (h - j * G) * a.BCP + t;
   const float* lp = a.lse_parts + at;
-  const float* op = a.O_parts + at * D;
-  // the first 32 ranges' outputs and sums are fetched together
-  constexpr int kOwn = 32 / kGroups;
+  const float4* op = reinterpret_cast<const float4*>(a.O_parts + at * D) + c4;
+  const int64_t pitch = (int64_t)R * C4;  // from range to range
   float4 own[kOwn];
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
     const int s = i * kGroups + grp;
     own[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (s < parts.y) own[i] = __ldcg(reinterpret_cast<const float4*>(op + (int64_t)s * R * D) + c4);
+    if (s < parts.y) own[i] = __ldcg(op + s * pitch);
   }
-  const float x0 = lane < parts.y ? __ldcg(lp + (int64_t)lane * R) : -INFINITY;
-  float M = x0;
-  for (int s = 32 + lane; s < parts.y; s += 32) M = fmaxf(M, __ldcg(lp + (int64_t)s * R));
-  for (int k = lane; k < nc; k += 32) M = fmaxf(M, sc[k]);
+  float M = -INFINITY;
+  for (int s = tid; s < parts.y; s += MT) M = fmaxf(M, sw[s] = __ldcg(lp + (int64_t)s * R));
+  for (int k = tid; k < nc; k += MT) M = fmaxf(M, sc[k]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[0][w]);
   const float ref = M == -INFINITY ? 0.f : M;  // (no key, or scores that are NaN)
   float L = 0.f;
+  // (a range without keys has a weight of 0 and a zero output)
+  for (int s = tid; s < parts.y; s += MT) L += sw[s] = exp2f(sw[s] - ref);
+  for (int k = tid; k < nc; k += MT) L += sc[k] = exp2f(sc[k] - ref);
+  L = warp_sum(L);
+  if (lane == 0) red[1][warp] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) L += red[1][w];
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float w, float4 x) {
     o.x = fmaf(w, x.x, o.x);
@@ -665,23 +687,14 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     o.z = fmaf(w, x.z, o.z);
     o.w = fmaf(w, x.w, o.w);
   };
-  // (a range without keys has a weight of 0 and a zero output)
-  for (int s0 = 0; s0 < parts.y; s0 += 32) {
-    const float x = s0 == 0 ? x0 : s0 + lane < parts.y ? __ldcg(lp + (int64_t)(s0 + lane) * R) : -INFINITY;
-    const float w = exp2f(x - ref);
-    L += w;
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-      const int s = i * kGroups + grp;
-      const float ws = __shfl_sync(0xffffffffu, w, s);
-      if (s0 > 0 && s0 + s < parts.y)
-        own[i] = __ldcg(reinterpret_cast<const float4*>(op + (int64_t)(s0 + s) * R * D) + c4);
-      if (s0 + s < parts.y) add(ws, own[i]);
-    }
-  }
-  for (int k = lane; k < nc; k += 32) L += exp2f(sc[k] - ref);
-  L = warp_sum(L);
-  for (int k = grp; k < nc; k += kGroups) add(exp2f(sc[k] - ref), ld4(vc + k * a.Vc.st + 4 * c4));
+  for (int i = 0; i < kOwn; ++i)
+    if (i * kGroups + grp < parts.y) add(sw[i * kGroups + grp], own[i]);
+#pragma unroll 4
+  for (int s = kOwn * kGroups + grp; s < parts.y; s += kGroups) add(sw[s], __ldcg(op + s * pitch));
+  if (grp < nc) add(sc[grp], v0);
+#pragma unroll 4
+  for (int k = grp + kGroups; k < nc; k += kGroups) add(sc[k], ld4(vc + k * a.Vc.st));
   acc[grp][c4] = o;
   __syncthreads();
   if (grp == 0) {
@@ -692,14 +705,40 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     if (a.lse != nullptr && tid == 0) a.lse[row] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
   }
   if (warp == 1) {
+    const int blocks = (R + kBlockRows - 1) / kBlockRows;
     for (int s = lane; s < parts.y; s += 32) {
-      const int x = __ldcg(a.faults + parts.x + s);
+      const int x = __ldcg(a.faults + (int64_t)(parts.x + s) * blocks + ((h - j * G) * a.BCP + t) / kBlockRows);
       if (x != 0) {
         latch_status(a.status, x & 255);
         if (x >> 8) latch_where(a.status, x >> 8);
       }
     }
   }
+}
+
+// A row takes 512 threads while every row has an SM for itself (its keys are then
+// cut into many ranges), else 128.
+constexpr int kManyRows = 149;
+
+template <typename T, int D, int MT>
+cudaError_t launch_merge(const CacheAttnArgs& a, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t mc = {};
+  mc.gridDim = dim3((unsigned)((int64_t)a.b * a.nq * a.BCP));
+  mc.blockDim = dim3(MT);
+  mc.dynamicSmemBytes = a.chunk ? a.BCP * sizeof(float) : 0;
+  mc.stream = stream;
+  mc.attrs = attr;
+  mc.numAttrs = 1;  // waits for the ranges inside
+  auto* kern = cache_merge_kernel<T, D, MT>;
+  if (mc.dynamicSmemBytes > 16 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mc.dynamicSmemBytes);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaLaunchKernelEx(&mc, kern, a);
 }
 
 template <typename T, int D, int RT>
@@ -716,35 +755,33 @@ cudaError_t launch_typed(const CacheAttnArgs& a, cudaStream_t stream) {
                               !encode_codes_4d(&maps.v, a.c.v, D, page, a.c.nkv, a.c.npages, a.c.sr, a.c.sh, a.c.sp, box)))
     return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};  // (clears the status words: behind everything before)
-  cfg.gridDim = dim3(a.ranges);
+  cfg.gridDim = dim3((unsigned)((int64_t)a.ranges * ((R + kBlockRows - 1) / kBlockRows)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   e = cudaLaunchKernelEx(&cfg, kern, maps, a);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t mc = {};
-  mc.gridDim = dim3((unsigned)((int64_t)a.b * a.nq * a.BCP));
-  mc.blockDim = dim3(kMergeThreads);
-  mc.stream = stream;
-  mc.attrs = attr;
-  mc.numAttrs = 1;  // waits for the ranges inside
-  return cudaLaunchKernelEx(&mc, cache_merge_kernel<T, D>, a);
+  return (int64_t)a.b * a.nq * a.BCP >= kManyRows ? launch_merge<T, D, 128>(a, stream) : launch_merge<T, D, 512>(a, stream);
+}
+
+// CTAs of a launch: one round of those resident at once (R <= 8 query rows:
+// three an SM, else two), over the blocks of query rows.
+int split_ctas(int64_t R) {
+  const int64_t blocks = (R + kBlockRows - 1) / kBlockRows;
+  return (int)std::max<int64_t>(2, 148 * (R <= 8 ? 3 : 2) / blocks);
 }
 
 }  // namespace
 
-int64_t cache_attn_ranges(int64_t rows, int N) { return range_grid(rows, N, kSplitCTAs, kSplitKeys); }
+int64_t cache_attn_ranges(int64_t rows, int64_t R, int N) { return range_grid(rows, N, split_ctas(R), kSplitKeys); }
 
 cudaError_t launch_cache_attn(bool is_bf16, int d, const CacheAttnArgs& args, cudaStream_t stream) {
   CacheAttnArgs a = args;
   const int R = (a.nq / a.c.nkv) * a.BCP;
-  const int64_t rows = (int64_t)a.b * a.c.nkv, ranges = cache_attn_ranges(rows, a.N);
-  if (R < 1 || R > kCacheMaxRows) return cudaErrorInvalidValue;
-  if (ranges > 0x7FFFFFFF || (int64_t)a.b * a.nq * a.BCP > 0x7FFFFFFF) return cudaErrorNotSupported;
-  a.target = (int)range_target(rows, kSplitCTAs);
+  const int64_t rows = (int64_t)a.b * a.c.nkv, ranges = cache_attn_ranges(rows, R, a.N);
+  if (R < 1) return cudaErrorInvalidValue;
+  if (ranges * ((R + kBlockRows - 1) / kBlockRows) > 0x7FFFFFFF || (int64_t)a.b * a.nq * a.BCP > 0x7FFFFFFF) return cudaErrorNotSupported;
+  a.target = (int)range_target(rows, split_ctas(R));
   a.ranges = (int)ranges;
   if (d != 64 && d != 128) return cudaErrorNotSupported;
   if (R <= 8) {

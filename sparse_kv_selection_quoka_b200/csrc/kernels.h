@@ -106,6 +106,7 @@ struct AttnArgs {
   int* status;
   int no_chunk = 0;         // 1: the chunk's own keys are left out (a shard's partial attention);
                             // rows with no visible key then give O = 0 and lse = -inf
+  int tc_d64 = 0;           // 1: launch_attn_tc also takes d = 64 (rows already gathered)
   uint64_t wait_ns = 0;     // bound of every wait (set by the launcher from wait_hooks())
   int inject = 0;           // test hook (set by the launcher from wait_hooks())
   // Split key ranges (tensor-core attention over gathered rows only): with
@@ -127,7 +128,8 @@ int attn_splits(int64_t tiles, int nt);
 // Steps (f)+(g) in fp32 on the CUDA cores (any input dtype).
 cudaError_t launch_attn_simt(bool bf16, const AttnArgs& a, cudaStream_t stream);
 
-// Steps (f)+(g) on the tcgen05 tensor cores (bf16, d = 128; O contiguous).
+// Steps (f)+(g) on the tcgen05 tensor cores (bf16, d = 128, or 64 with
+// a.tc_d64; O contiguous).
 // With a.kv_idx null (or bsa = 0), a.K / a.V are the gathered selected rows
 // (b, nkv, >= bsa, d) and every K/V tile is a TMA box (attn_tma.cu);
 // otherwise launch_attn_tc_gather runs, which gathers the rows by index
@@ -208,9 +210,9 @@ struct CacheGatherArgs {
 };
 cudaError_t launch_cache_gather(bool bf16, int d, const CacheGatherArgs& a, bool pdl, cudaStream_t stream);
 
-// Attention of at most kCacheMaxRows query rows per KV head over the cache
-// and the chunk's own keys, by key ranges joined by a second kernel
-// (cache_attn.cu).
+// Attention over the cache's codes and the chunk's own keys, by key ranges
+// joined by a second kernel (cache_attn.cu). bf16 queries with more than
+// kCacheMaxRows rows per KV head are better off with dequantised rows.
 constexpr int kCacheMaxRows = 64;  // G * BCP
 struct CacheAttnArgs {
   CacheView c;
@@ -224,14 +226,15 @@ struct CacheAttnArgs {
   float* O_parts;           // (ranges, G * BCP, d) fp32
   float* lse_parts;         // (ranges, G * BCP) fp32, in log2 units
   int2* row_parts;          // (b, nkv): a row's first range and their number
-  int* faults;              // (ranges): what a range's CTA has to latch
+  int* faults;              // (ranges, ceil(G * BCP / 64)): what a CTA has to latch
   int ranges, target;       // set by the launcher
   void* O;
   float* lse;
   int* status;
 };
-// Ranges that launch_cache_attn cuts `rows` = b * nkv rows of at most N keys into, at most.
-int64_t cache_attn_ranges(int64_t rows, int N);
+// Ranges that launch_cache_attn cuts `rows` = b * nkv rows of at most N keys into, at most, for
+// R = G * BCP query rows each.
+int64_t cache_attn_ranges(int64_t rows, int64_t R, int N);
 cudaError_t launch_cache_attn(bool bf16, int d, const CacheAttnArgs& a, cudaStream_t stream);
 
 // Step (d) over the cache's keys: S_agg (b, nkv, max_len); entries at and

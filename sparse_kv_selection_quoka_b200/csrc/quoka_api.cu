@@ -82,8 +82,9 @@ struct WsLayout {
 // Key-range splits of the tensor-core attention over the gathered rows
 // (bf16, d = 128) for a chunk of b * nq * ceil(BCP / 128) query tiles and
 // BSA_eff selected keys (with the chunk's own keys unless no_chunk).
-int attn_nsplit(int64_t b, int64_t nq, int64_t BCP, int64_t d, int64_t bsa_eff, bool bf16, bool no_chunk) {
-  if (!bf16 || d != 128) return 1;
+int attn_nsplit(int64_t b, int64_t nq, int64_t BCP, int64_t d, int64_t bsa_eff, bool bf16, bool no_chunk,
+                bool tc_d64 = false) {
+  if (!bf16 || (d != 128 && !tc_d64)) return 1;
   const int64_t tiles = b * nq * ((BCP + 127) / 128);
   const int64_t nt = (bsa_eff + 127) / 128 + (no_chunk ? 0 : 1);
   return quoka::attn_splits(tiles, (int)std::min<int64_t>(nt, 1 << 20));
@@ -333,9 +334,10 @@ quoka_status run_attn(const quoka_tensor* Q, Strided K, Strided V, const quoka_t
                       const quoka_tensor* Vc, const AttnShapes& s, int64_t T, const int32_t* kv_idx,
                       const int32_t* kv_count, int bsa_eff, float scale, void* O, float* lse,
                       int* status, cudaStream_t stream, bool pdl = false, bool no_chunk = false,
-                      void* parts = nullptr, size_t parts_bytes = 0) {
+                      void* parts = nullptr, size_t parts_bytes = 0, bool tc_d64 = false) {
   quoka::AttnArgs a;
   a.no_chunk = no_chunk ? 1 : 0;
+  a.tc_d64 = tc_d64 ? 1 : 0;
   a.Q = strided(Q);
   a.K = K;
   a.V = V;
@@ -357,7 +359,7 @@ quoka_status run_attn(const quoka_tensor* Q, Strided K, Strided V, const quoka_t
   if (kv_idx == nullptr && parts != nullptr) {
     // split key ranges when the query tiles leave most SMs idle and the
     // workspace holds the partials
-    const int ns = attn_nsplit(s.b, s.nq, s.BCP, s.d, bsa_eff, Q->dtype == QUOKA_BF16, no_chunk);
+    const int ns = attn_nsplit(s.b, s.nq, s.BCP, s.d, bsa_eff, Q->dtype == QUOKA_BF16, no_chunk, tc_d64);
     if (ns > 1 && parts_bytes >= attn_parts_bytes(s.b, s.nq, s.BCP, s.d, ns)) {
       const int64_t rows = (int64_t)ns * s.b * s.nq * s.BCP;
       a.nsplit = ns;
@@ -487,8 +489,8 @@ bool overlaps(const void* a, size_t na, const quoka_tensor* t) {
 }
 
 // Workspace of quoka_cache_attn: the status words, then either the partials
-// of the key ranges (few query rows) or the dequantised keys and values with
-// their counts and the partials of the tensor-core attention.
+// of the key ranges (few query rows, or fp32) or the dequantised keys and values
+// with their counts and the partials of the tensor-core attention.
 struct CacheAttnWs {
   bool few;
   size_t o_parts, lse_parts, row_parts, faults, ksel, vsel, count, aparts, aparts_bytes, total;
@@ -503,18 +505,19 @@ CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t
     off += align_up(bytes);
     return p;
   };
-  w.few = (nq / nkv) * BCP <= quoka::kCacheMaxRows;
+  const int64_t R = (nq / nkv) * BCP;
+  w.few = dtype == QUOKA_F32 || R <= quoka::kCacheMaxRows;
   if (w.few) {
-    const int64_t ranges = quoka::cache_attn_ranges(b * nkv, (int)N), rows = ranges * (nq / nkv) * BCP;
+    const int64_t ranges = quoka::cache_attn_ranges(b * nkv, R, (int)N), rows = ranges * R;
     w.o_parts = take((size_t)(rows * d) * 4);
     w.lse_parts = take((size_t)rows * 4);
     w.row_parts = take((size_t)(b * nkv) * 8);
-    w.faults = take((size_t)ranges * 4);
+    w.faults = take((size_t)(ranges * ((R + 63) / 64)) * 4);
   } else {
     w.ksel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
     w.vsel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
     w.count = take((size_t)(b * nkv) * 4);
-    w.aparts_bytes = attn_parts_bytes(b, nq, BCP, d, attn_nsplit(b, nq, BCP, d, N, dtype == QUOKA_BF16, no_chunk));
+    w.aparts_bytes = attn_parts_bytes(b, nq, BCP, d, attn_nsplit(b, nq, BCP, d, N, dtype == QUOKA_BF16, no_chunk, true));
     w.aparts = take(w.aparts_bytes);
   }
   w.total = off;
@@ -950,7 +953,7 @@ quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, i
   return run_attn(Q, Strided{at<void>(ws, w.ksel), sb, sh, d}, Strided{at<void>(ws, w.vsel), sb, sh, d},
                   no_chunk ? &own : Kc, no_chunk ? &own : Vc, s, N, nullptr, at<int32_t>(ws, w.count), N, scale, O,
                   lse, status, cs, true, no_chunk, w.aparts_bytes > 0 ? at<void>(ws, w.aparts) : nullptr,
-                  w.aparts_bytes);
+                  w.aparts_bytes, true);
 }
 
 quoka_status quoka_get_device_status(const void* ws, void* stream, int32_t* device_status) {

@@ -177,16 +177,17 @@ def check_attention(O, lse, want, dt, d, n, few):
       2^-22 of the sum of magnitudes (`size`), and the fp32 query as two halves
       (2^-22): ds = (d + 8) 2^-22 size;
     weight: 2^x of an fp32 x, |x| <= 64 where it matters (2^-17), the rounding
-      to the operand type (few rows: fp16 2^-11, two halves 2^-21 for fp32
-      inputs; many rows: bf16 2^-8, and once more for a range's bf16 partial;
-      fp32: none), twice the score's error in numerator and denominator; with
+      to the operand type (few rows, and fp32: fp16 2^-11, two halves 2^-21 for
+      fp32 inputs; many bf16 rows: bf16 2^-8, and once more for a range's bf16
+      partial), twice the score's error in numerator and denominator; with
       few rows 2^-32 of the largest w_k = p_k 2^ev_k at least (fp16 subnormals),
       which is at most 2^E L, L the denominator: 2^-32 B;
     sums: n keys, each addition off by 2^-22 of the sum of magnitudes;
     output: half a step of its type."""
     wO, wl, A, size, B = want
     ds = (d + 8) * 2.0**-22 * size
-    weight = {True: {"bf16": 2.0**-11, "f32": 2.0**-21}, False: {"bf16": 2 * 2.0**-8, "f32": 0.0}}[few][dt]
+    few = few or dt == "f32"
+    weight = {"bf16": 2.0**-11 if few else 2 * 2.0**-8, "f32": 2.0**-21}[dt]
     rel = weight + 2.0**-17 + 2 * ds + (n + 64) * 2.0**-22
     half = torch.finfo(TYPES[dt]).eps / 2
     O, lse = O.double().cpu(), lse.double().cpu()
