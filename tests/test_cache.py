@@ -369,6 +369,8 @@ SELECTS = [
     ([2500, 1], 5001, 2, 16, 128, 32, 64, 17, 600, "f32", "hnd"),
     ([6000, 5999], 6000, 2, 8, 128, 128, 1, 1, 512, "bf16", "hnd"),
     ([20000], 20000, 1, 4, 64, 64, 33, 8, 4000, "bf16", "hnd"),
+    ([(71 * i) % 311 for i in range(50)], 310, 3, 3, 128, 16, 1, 1, 40, "bf16", "hnd"),  # 150 rows, ragged
+    ([513, 512], 1025, 1, 5, 64, 16, 9, 5, 100, "bf16", "nhd"),
 ]
 
 
@@ -457,6 +459,13 @@ ATTNS = [
     ([90, 200], 200, 1, 8, 64, 32, 16, 77, False, "f32", "hnd"),
     ([0], 0, 1, 2, 128, 16, 40, 0, True, "bf16", "hnd"),             # no cached key at all
     ([0], 0, 1, 2, 64, 16, 2, 0, True, "f32", "hnd"),
+    ([20000], 20000, 1, 2, 128, 128, 1, 0, False, "bf16", "hnd"),    # one row in more ranges than are fetched ahead
+    ([5000, 4900, 0], 5000, 1, 10, 64, 64, 5, 0, True, "f32", "nhd"),  # the same, with the rows of a full GPU
+    ([(37 * i) % 131 for i in range(40)], 128, 2, 4, 64, 32, 1, 0, False, "bf16", "hnd"),  # 80 rows, ragged
+    ([(29 * i) % 23 for i in range(150)], 22, 4, 4, 64, 16, 1, 7, True, "f32", "nhd"),     # 600 rows, tiny
+    ([200], 200, 1, 2, 64, 16, 170, 50, True, "f32", "hnd"),         # fp32 in six blocks of rows
+    ([900, 31], 1000, 2, 4, 64, 128, 150, 0, False, "bf16", "nhd"),   # d = 64 on the dense path, split key ranges
+    ([700], 700, 1, 1, 64, 32, 257, 129, True, "bf16", "hnd"),
 ]
 
 
