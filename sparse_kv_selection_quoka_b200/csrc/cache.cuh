@@ -103,7 +103,8 @@ __host__ __forceinline__ int64_t range_grid(int64_t rows, int N, int ctas, int l
   return a < b ? a : b;
 }
 
-// Range `cta` (called by one warp; written to *out). keys(row): a row's keys, at
+// Range `cta`, or, for -1 - row, the first range of that row (called by one warp;
+// written to *out). keys(row): a row's keys, at
 // most 2^30. Rows are cut into equal runs of at most max(least, total / target)
 // keys, rounded up to `step`.
 template <typename Keys>
@@ -128,13 +129,14 @@ __device__ __forceinline__ void find_range(int rows, int target, int least, int 
       if (lane >= o) incl += x;
     }
     const int first = before + incl - parts;
-    if (cta >= first && cta < first + parts) {
+    if (cta < 0 ? i == -1 - cta : cta >= first && cta < first + parts) {
+      if (cta < 0) cta = first;
       const int per = ((n + parts - 1) / parts + step - 1) & ~(step - 1);
       const int k0 = (int)min((int64_t)n, (int64_t)(cta - first) * per);
       *out = Range{i, k0, min(n, k0 + per), first, parts};
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
-    if (before > cta) break;
+    if (cta >= 0 && before > cta) break;
   }
 }
 

@@ -209,39 +209,44 @@ __global__ void __launch_bounds__(NT) cache_append_kernel(const CacheAppendArgs 
 
   float x[NP][8], y[NP][8];
   uint32_t top = 0u;  // bits of the largest finite magnitude
-  {
-    Raw8<T> rx[NP], ry[NP];
+  Raw8<T> rx[NP], ry[NP];
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int t = t0 + k * RPP + rr;
-      if (t < t1) {
-        load_raw(x0 + (int64_t)(t - start) * X.st + 8 * c0, rx[k]);
-        load_raw(x0 + (int64_t)(t - start) * X.st + 8 * c1, ry[k]);
-      }
+  for (int k = 0; k < NP; ++k) {
+    const int t = t0 + k * RPP + rr;
+    if (t < t1) {
+      load_raw(x0 + (int64_t)(t - start) * X.st + 8 * c0, rx[k]);
+      load_raw(x0 + (int64_t)(t - start) * X.st + 8 * c1, ry[k]);
+    }
+  }
+  float cs[8], sn[8];  // angles: the first pass's are fetched with the rows
+  auto angles = [&](int t) {
+    load8(a.cos + (int64_t)t * half + 8 * i, cs);
+    load8(a.sin + (int64_t)t * half + 8 * i, sn);
+  };
+  if (turn && t0 + rr < t1) angles(t0 + rr);
+  float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + (int64_t)pid * nkv + j;
+  float old = 0.f;  // (fetched while the rows arrive)
+  if (t0 > p0 && pid >= 0 && pid < a.c.npages) old = __ldcg(scale);
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int t = t0 + k * RPP + rr;
+    if (t >= t1) continue;
+    to_floats(rx[k], x[k]);
+    to_floats(ry[k], y[k]);
+    if (turn) {
+      if (k > 0) angles(t);
+      rotate(rot, cs, sn, x[k], y[k]);
+    }
+    if (!is_v && a.Kr != nullptr) {
+      T* o = static_cast<T*>(a.Kr) + (((int64_t)bi * nkv + j) * a.BCP + (t - start)) * D;
+      store8(o + 8 * c0, x[k]);
+      store8(o + 8 * c1, y[k]);
     }
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int t = t0 + k * RPP + rr;
-      if (t >= t1) continue;
-      to_floats(rx[k], x[k]);
-      to_floats(ry[k], y[k]);
-      if (turn) {
-        float cs[8], sn[8];
-        load8(a.cos + (int64_t)t * half + 8 * i, cs);
-        load8(a.sin + (int64_t)t * half + 8 * i, sn);
-        rotate(rot, cs, sn, x[k], y[k]);
-      }
-      if (!is_v && a.Kr != nullptr) {
-        T* o = static_cast<T*>(a.Kr) + (((int64_t)bi * nkv + j) * a.BCP + (t - start)) * D;
-        store8(o + 8 * c0, x[k]);
-        store8(o + 8 * c1, y[k]);
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t mx = __float_as_uint(x[k][u]) & 0x7FFFFFFFu, my = __float_as_uint(y[k][u]) & 0x7FFFFFFFu;
-        if (mx < 0x7F800000u) top = max(top, mx);
-        if (my < 0x7F800000u) top = max(top, my);
-      }
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t mx = __float_as_uint(x[k][u]) & 0x7FFFFFFFu, my = __float_as_uint(y[k][u]) & 0x7FFFFFFFu;
+      if (mx < 0x7F800000u) top = max(top, mx);
+      if (my < 0x7F800000u) top = max(top, my);
     }
   }
   const bool held = pid >= 0 && pid < a.c.npages;
@@ -251,8 +256,6 @@ __global__ void __launch_bounds__(NT) cache_append_kernel(const CacheAppendArgs 
   }
   top = __reduce_max_sync(0xffffffffu, top);
   if ((tid & 31) == 0) wmax[tid >> 5] = top;
-  float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + (int64_t)pid * nkv + j;
-  const float old = t0 > p0 ? __ldcg(scale) : 0.f;
   __syncthreads();  // (the old scale is read by all before it is replaced below)
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) top = max(top, wmax[w]);

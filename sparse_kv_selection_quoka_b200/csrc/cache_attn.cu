@@ -610,6 +610,7 @@ __global__ void __launch_bounds__(MT) cache_merge_kernel(const CacheAttnArgs a) 
   __shared__ float4 acc[kGroups][C4];
   __shared__ float sw[kMaxParts];
   __shared__ float red[2][kWarps];
+  __shared__ Range found;
   extern __shared__ float sc[];  // the chunk's keys: scores, then weights
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c4 = tid % C4, grp = tid / C4;
@@ -646,8 +647,21 @@ __global__ void __launch_bounds__(MT) cache_merge_kernel(const CacheAttnArgs a) 
     }
     __syncthreads();
   }
-  pdl_wait();
-  int2 parts = __ldcg(a.row_parts + bi * a.c.nkv + j);  // first range and their number
+  // the row's first range and their number: found again while the ranges are
+  // still at work when that is cheap, else read behind them
+  int2 parts;
+  const int nrows = a.b * a.c.nkv, row_of = bi * a.c.nkv + j;
+  if (nrows <= 32) {
+    if (tid < 32)
+      find_range(nrows, a.target, kSplitKeys, 64, -1 - row_of, lane,
+                 [&](int i) { return a.kv_idx != nullptr ? row_keys<true>(a, i) : row_keys<false>(a, i); }, &found);
+    __syncthreads();
+    parts = make_int2(found.first, found.parts);
+    pdl_wait();
+  } else {
+    pdl_wait();
+    parts = __ldcg(a.row_parts + row_of);
+  }
   parts.y = min(parts.y, kMaxParts);
   const int64_t at = (int64_t)parts.x * R + (h - j * G) * a.BCP + t;
   const float* lp = a.lse_parts + at;
