@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const __grid_c
           break;
         }
         const uint8_t* stage = ring + st * kStage * D;
-        const int r0 = warp * 32, key = k0 + s * kStage + r0 + gk;
+        const int r0 = warp * 32;
         float x[2][2];   // the best of keys gk, gk + 8 of both 16-key tiles over the lane's columns
         float k2[2][2];  // |k|^2 of the keys whose diagonal element this lane holds
         if (PACKED) {
@@ -288,21 +288,30 @@ __global__ void __launch_bounds__(kThreads, 3) cache_score_kernel(const __grid_c
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int v = 0; v < 2; ++v) x[m][v] = fmaxf(x[m][v], __shfl_xor_sync(0xffffffffu, x[m][v], 1));
-        if (t4 == (g >> 1)) {  // the lane that holds the diagonal's g-th element
-          float* S = a.S_agg + row * a.max_len + key;
+        // lane l takes key l of the 32: from the lane of its quad that holds the
+        // diagonal's element
+        {
+          const int lg = (lane & 7) ^ ((lane & 1) << 2), src = 4 * lg + (lg >> 1);
+          float best = 0.f, n = 0.f;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
-              const int at = 16 * m + 8 * v;
-              if (key + at >= k1) continue;
-              // (rsqrt is within 2^-22; a key of zeros scores 0, one with a NaN -inf)
-              const float n = k2[m][v];
-              float y = n > 0.f ? x[m][v] * (1.f / kQScale) * rsqrtf(n) : n == 0.f ? 0.f : -INFINITY;
-              if (!PACKED && pass > 0) y = fmaxf(y, S[at]);  // (this thread's own score of the passes before)
-              S[at] = y;
-              if (pass == passes - 1) atomicAdd(&sh.hist[score_bin(y)], 1u);
+              const float x_ = __shfl_sync(0xffffffffu, x[m][v], src), n_ = __shfl_sync(0xffffffffu, k2[m][v], src);
+              if ((lane >> 3) == 2 * m + v) {
+                best = x_;
+                n = n_;
+              }
             }
+          const int key = k0 + s * kStage + r0 + lane;
+          if (key < k1) {
+            // (rsqrt is within 2^-22; a key of zeros scores 0, one with a NaN -inf)
+            float y = n > 0.f ? best * (1.f / kQScale) * rsqrtf(n) : n == 0.f ? 0.f : -INFINITY;
+            float* S = a.S_agg + row * a.max_len + key;
+            if (!PACKED && pass > 0) y = fmaxf(y, *S);  // (this thread's own score of the passes before)
+            *S = y;
+            if (pass == passes - 1) atomicAdd(&sh.hist[score_bin(y)], 1u);
+          }
         }
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&sh.empty[st]);
