@@ -92,51 +92,62 @@ struct Range {
   int first, parts;  // the row's first range and their number
 };
 
-// Ranges asked for (before rounding up row by row), and the grid that holds
-// them: sum over rows of max(1, ceil(n / most)) <= target + rows with
+// Beyond this many rows each takes one CTA: they fill the GPU several times over,
+// and a look at all lengths would cost each CTA more than it evens out.
+constexpr int kRangeRows = 1024;
+
+// Ranges asked for (before rounding up row by row; ctas >= 2), and the grid that
+// holds them: sum over rows of max(1, ceil(n / most)) <= target + rows with
 // most >= total / target, and <= rows * ceil(N / least).
 __host__ __device__ __forceinline__ int64_t range_target(int64_t rows, int ctas) {
-  return ctas - rows / 2 > ctas / 2 ? ctas - rows / 2 : ctas / 2;  // (ctas >= 2)
+  return ctas - rows / 2 > ctas / 2 ? ctas - rows / 2 : ctas / 2;
 }
 __host__ __forceinline__ int64_t range_grid(int64_t rows, int N, int ctas, int least) {
+  if (rows > kRangeRows) return rows;
   const int64_t a = range_target(rows, ctas) + rows, b = rows * (N > least ? (N + least - 1) / least : 1);
   return a < b ? a : b;
 }
 
 // Range `cta`, or, for -1 - row, the first range of that row (called by one warp;
-// written to *out). keys(row): a row's keys, at
-// most 2^30. Rows are cut into equal runs of at most max(least, total / target)
-// keys, rounded up to `step`.
+// written to *out). keys(row): a row's keys, at most 2^30. Rows are cut into equal
+// runs of at most max(least, total / target) keys, rounded up to `step`.
 template <typename Keys>
 __device__ __forceinline__ void find_range(int rows, int target, int least, int step, int cta, int lane, Keys&& keys,
                                            Range* out) {
+  if (rows > kRangeRows) {
+    const int row = cta < 0 ? -1 - cta : cta;
+    if (lane == 0) *out = Range{row, 0, keys(row), row, 1};
+    return;
+  }
   int64_t total = 0;
   for (int i = lane; i < rows; i += 32) total += keys(i);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int most = (int)min(max((int64_t)least, (total + target - 1) / target), (int64_t)1 << 30);
-  int before = 0;  // ranges of the rows before
   if (lane == 0) out->row = -1;
   __syncwarp();
+  int before = 0;  // ranges of the rows before
+#pragma unroll 1
   for (int i0 = 0; i0 < rows; i0 += 32) {
-    const int i = i0 + lane;
-    const int n = i < rows ? keys(i) : 0;
+    const int i = i0 + lane, n = i < rows ? keys(i) : 0;
     const int parts = i < rows ? max(1, (n + most - 1) / most) : 0;
-    int incl = parts;
+    const int all = __reduce_add_sync(0xffffffffu, parts);
+    if (cta < 0 ? -1 - cta < i0 + 32 : cta < before + all) {  // among these 32 rows
+      int incl = parts;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      const int first = before + incl - parts, at = cta < 0 ? first : cta;
+      if (cta < 0 ? i == -1 - cta : cta >= first && cta < first + parts) {
+        const int per = ((n + parts - 1) / parts + step - 1) & ~(step - 1);
+        const int k0 = (int)min((int64_t)n, (int64_t)(at - first) * per);
+        *out = Range{i, k0, min(n, k0 + per), first, parts};
+      }
+      return;
     }
-    const int first = before + incl - parts;
-    if (cta < 0 ? i == -1 - cta : cta >= first && cta < first + parts) {
-      if (cta < 0) cta = first;
-      const int per = ((n + parts - 1) / parts + step - 1) & ~(step - 1);
-      const int k0 = (int)min((int64_t)n, (int64_t)(cta - first) * per);
-      *out = Range{i, k0, min(n, k0 + per), first, parts};
-    }
-    before += __shfl_sync(0xffffffffu, incl, 31);
-    if (cta >= 0 && before > cta) break;
+    before += all;
   }
 }
 

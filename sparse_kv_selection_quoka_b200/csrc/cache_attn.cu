@@ -41,7 +41,7 @@
 // movmatrix. Chunk c of row r lies at c ^ (r & 7), and operand row n of a step
 // stands for key n ^ 4 (n & 1), so that neither read has a bank conflict
 // (d = 128; d = 64 keeps a two-way one on V). A second kernel joins the ranges
-// of every query row and adds the chunk's own keys (at most 64) in fp32.
+// of every query row and adds the chunk's own keys in fp32.
 // Bound by the cache's bytes, each read once per 64 query rows.
 #include <algorithm>
 
@@ -65,8 +65,7 @@ constexpr int kStages = 2;
 constexpr float kHead = 7.f, kLazy = 15.f;
 constexpr int kSplitKeys = 128;    // a range has at least this many keys
 constexpr int kBlockRows = 64;     // query rows of a CTA
-constexpr int kMaxCTAs = 444;      // resident at once, at most
-constexpr int kMaxParts = 448;     // ranges of a row: at most the ranges asked for, <= kMaxCTAs
+constexpr int kMaxParts = 444;     // ranges of a row: at most the ranges asked for
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -250,7 +249,7 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
   if constexpr (IDX) {
     sm100::cp_async_commit();
     sm100::cp_async_wait<0>();
-  } else if (s < nst) {  // gave up: no copy may be in flight when the CTA goes on
+  } else {  // no copy may be in flight when the CTA goes on, even if a wait gave up
     for (int i = max(0, s - kStages); i < s; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && sh.fault == 0) sh.fault = 6;  // QUOKA_ERR_BOUNDS
@@ -258,7 +257,8 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
 
 // One CTA per range and block of 64 query rows. RT: 8-row query tiles of a warp.
 template <typename T, int D, bool IDX, int RT>
-__global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
+__global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2)
+cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
   constexpr int SPLIT = sizeof(T) == 2 ? 1 : 2;
   constexpr int KS = D / 16;  // k-steps of K Q^T, and row tiles of O^T
   using Rg = Ring<D>;
@@ -326,25 +326,26 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int r = r4 + 4 * y;
-        if (r >= tiles * RT * 8) break;
-        float top = 0.f;
+        if (r < tiles * RT * 8) {
+          float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) top = fmaxf(top, fabsf(x[y][i]));
+          for (int i = 0; i < D / 32; ++i) top = fmaxf(top, fabsf(x[y][i]));
 #pragma unroll
-        for (int o_ = 16; o_ > 0; o_ >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o_));
-        int e = (int)(__float_as_uint(top) >> 23) - 127 - 13;  // top * 2^-e lies in [2^13, 2^14)
-        e = min(max(e, -100), 100);                            // (zero, tiny, infinite rows)
-        const float f = exp2i(-e);
-        if (lane == 0) rowf[r] = exp2i(e) * a.scale * kLog2e;
+          for (int o_ = 16; o_ > 0; o_ >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o_));
+          int e = (int)(__float_as_uint(top) >> 23) - 127 - 13;  // top * 2^-e lies in [2^13, 2^14)
+          e = min(max(e, -100), 114);                            // (zero and tiny rows, infinities)
+          const float f = exp2i(-e);
+          if (lane == 0) rowf[r] = exp2i(e) * a.scale * kLog2e;
 #pragma unroll
-        for (int i = 0; i < D / 32; i += 2) {
-          const int d = D / 32 * lane + i;
-          // column d belongs to chunk d / 16 = t + 4 * (ks / 4), word (d % 16) / 4 = ks % 4 of it
-          const int ch = d >> 4, ks = 4 * (ch >> 2) + ((d & 15) >> 2), reg = (d >> 1) & 1;
-          uint32_t* dst = qs + (((r >> 3) * KS + ks) * 32 + (r & 7) * 4 + (ch & 3)) * (2 * SPLIT) + reg;
-          const uint32_t hi = pack_h2(x[y][i] * f, x[y][i + 1] * f);
-          *dst = hi;
-          if constexpr (SPLIT == 2) dst[2] = rest_h2(x[y][i] * f, x[y][i + 1] * f, hi);
+          for (int i = 0; i < D / 32; i += 2) {
+            const int d = D / 32 * lane + i;
+            // column d belongs to chunk d / 16 = t + 4 * (ks / 4), word (d % 16) / 4 = ks % 4 of it
+            const int ch = d >> 4, ks = 4 * (ch >> 2) + ((d & 15) >> 2), reg = (d >> 1) & 1;
+            uint32_t* dst = qs + (((r >> 3) * KS + ks) * 32 + (r & 7) * 4 + (ch & 3)) * (2 * SPLIT) + reg;
+            const uint32_t hi = pack_h2(x[y][i] * f, x[y][i + 1] * f);
+            *dst = hi;
+            if constexpr (SPLIT == 2) dst[2] = rest_h2(x[y][i] * f, x[y][i + 1] * f, hi);
+          }
         }
       }
     }
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) cache_slice_kernel(
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float& s_ = c[y][rt][2 * u + i];
-              s_ = there ? fmaf(s_, f[rt][i] * ks, (float)ev) : -INFINITY;
+              s_ = there ? fmaf(s_ * f[rt][i], ks, (float)ev) : -INFINITY;
               x[rt][i] = fmaxf(x[rt][i], s_);
             }
         }
@@ -606,7 +607,7 @@ __device__ __forceinline__ void st4(bf16* p, float4 v) {
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(MT) cache_merge_kernel(const CacheAttnArgs a) {
   constexpr int C4 = D / 4, kGroups = MT / C4, kWarps = MT / 32;
-  constexpr int kOwn = 8;  // ranges a group fetches ahead
+  constexpr int kOwn = MT == 512 ? 4 : 8;  // ranges a group fetches ahead
   __shared__ float4 acc[kGroups][C4];
   __shared__ float sw[kMaxParts];
   __shared__ float red[2][kWarps];
@@ -782,6 +783,7 @@ cudaError_t launch_typed(const CacheAttnArgs& a, cudaStream_t stream) {
 // three an SM, else two), over the blocks of query rows.
 int split_ctas(int64_t R) {
   const int64_t blocks = (R + kBlockRows - 1) / kBlockRows;
+  static_assert(148 * 3 <= kMaxParts, "a row's ranges fit the join's table");
   return (int)std::max<int64_t>(2, 148 * (R <= 8 ? 3 : 2) / blocks);
 }
 

@@ -93,8 +93,8 @@ __device__ __forceinline__ void load_rows(const CacheScoreArgs& a, const CUtenso
     p0 = p1;
     p1 = p2;
   }
-  if (it < total)  // gave up: no copy may be in flight when the CTA ends
-    for (int i = max(0, it - kStages); i < it; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
+  // no copy may be in flight when the CTA ends, even if a wait gave up
+  for (int i = max(0, it - kStages); i < it; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
   if (bad) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
 }
 
