@@ -26,6 +26,10 @@
 // on the first 64-column atom of every tile: 4 k-steps of Q K^T, 64 columns of
 // O, half the bytes.
 //
+// Packed rows (a.pack, only for callers that ask for it): with few rows per
+// head a tile takes rows of several heads of a KV head, row r at chunk position
+// r % BCP.
+//
 // Split key ranges: when the query tiles alone leave most SMs idle (short
 // chunks, few heads), each query tile's key tiles are cut into nsplit
 // contiguous ranges and the grid runs one CTA per (tile, range). Such a CTA
@@ -155,9 +159,12 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int j = blockIdx.y, bi = blockIdx.z;
   const int G = a.nq / a.nkv;
-  const int ntt = (a.BCP + 127) / 128;  // row tiles per query head
-  const int qt = (int)blockIdx.x % (G * ntt), split = (int)blockIdx.x / (G * ntt);
-  const int h = j * G + qt / ntt;
+  // the row axis that is cut into tiles: a query head's BCP rows, or (a.pack) the
+  // G * BCP rows of a KV head; heads of that axis per KV head, and in all
+  const int nrow = a.pack ? G * a.BCP : a.BCP, hpk = a.pack ? 1 : G, heads = a.nkv * hpk;
+  const int ntt = (nrow + 127) / 128;  // row tiles per head
+  const int qt = (int)blockIdx.x % (hpk * ntt), split = (int)blockIdx.x / (hpk * ntt);
+  const int h = j * hpk + qt / ntt;
   const int t0 = (qt % ntt) * 128;
 
   // Setup and the Q load touch nothing the previous kernel writes: they run
@@ -205,7 +212,7 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
   pdl_wait();  // the gathered rows and their counts come from the previous kernel
   const int64_t kvrow = (int64_t)bi * a.nkv + j;
   const int nsel = a.bsa > 0 ? max(0, min(__ldcg(a.kv_count + kvrow), a.bsa)) : 0;
-  const int nchunk = a.no_chunk ? 0 : min(a.BCP, t0 + 128);
+  const int nchunk = a.no_chunk ? 0 : a.pack ? a.BCP : min(a.BCP, t0 + 128);
   const int ntile_sel = (nsel + N - 1) / N;
   const int nT_all = ntile_sel + (nchunk + N - 1) / N;  // key tiles (0 only without the chunk's keys)
   // this CTA's key tiles: range `split` of nsplit (all of them when 1)
@@ -285,6 +292,7 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     const int w = warp >> 2;  // key tiles w, w + 2, ... of this warpgroup
     const int r = tid & 127;  // row == TMEM lane
     const int t = t0 + r;
+    const int pos = a.pack ? t % a.BCP : t;  // the row's chunk position
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t S = tmem + lane_off + 128u * w;
     const float qscale = a.scale * 1.4426950408889634f;
@@ -304,9 +312,9 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
       // key c of the tile is key number base_n + c of its list (selected
       // keys counted from the range's first one); it is visible to row t
       // when it is a selected key below nsel, or a chunk key at a position
-      // p < nchunk with p <= t
+      // p < nchunk not after the row's
       const int base_n = (sel_tile ? kt : kt - sel_rel) * N;
-      const int lim = sel_tile ? nsel_rel : min(nchunk, t + 1);
+      const int lim = sel_tile ? nsel_rel : min(nchunk, pos + 1);
       softmax_tile_split<PV_PARTS, HD>(S, tmem + lane_off + 256u + 128u * w, i > 0, base_n, lim,
                                                      qscale, m, l, sm.p_part[w]);
     }
@@ -361,8 +369,8 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
         *reinterpret_cast<uint4*>(sm.q + sw128_offset(r, (HD / 2 * w + 32 * c2 + u) >> 3, 128)) = pk;
       }
     }
-    if (w == 0 && t < a.BCP) {
-      const int64_t orow = ((int64_t)bi * a.nq + h) * a.BCP + t;
+    if (w == 0 && t < nrow) {
+      const int64_t orow = ((int64_t)bi * heads + h) * nrow + t;
       if (part)
         a.lse_parts[(int64_t)split * a.b * a.nq * a.BCP + orow] =
             L > 0.f ? (M + __log2f(L)) * 0.6931471805599453f : -INFINITY;
@@ -396,7 +404,8 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
 // row with none gives O = 0, lse = -inf.
 constexpr int kMergeThreads = 256;
 
-template <int HD>
+// MS: ranges at most.
+template <int HD, int MS>
 __global__ void __launch_bounds__(kMergeThreads)
 attn_split_merge_kernel(const bf16* __restrict__ O_parts, const float* __restrict__ lse_parts, int nsplit,
                         int64_t rows, bf16* __restrict__ O, float* __restrict__ lse) {
@@ -405,17 +414,17 @@ attn_split_merge_kernel(const bf16* __restrict__ O_parts, const float* __restric
   if (g >= rows * (HD / 8)) return;
   const int64_t row = g / (HD / 8);
   const int c0 = (int)(g % (HD / 8)) * 8;
-  float ls[4];
+  float ls[MS];
   float M = -INFINITY;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
+  for (int s = 0; s < MS; ++s) {
     ls[s] = s < nsplit ? __ldcg(lse_parts + (int64_t)s * rows + row) : -INFINITY;
     M = fmaxf(M, ls[s]);
   }
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   float L = 0.f;
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
+  for (int s = 0; s < MS; ++s) {
     if (ls[s] == -INFINITY) continue;
     const float wgt = __expf(ls[s] - M);
     L += wgt;
@@ -439,9 +448,9 @@ attn_split_merge_kernel(const bf16* __restrict__ O_parts, const float* __restric
 
 }  // namespace
 
-int attn_splits(int64_t tiles, int nt) {
+int attn_splits(int64_t tiles, int nt, int most) {
   if (tiles < 1 || 2 * tiles > kAttnWaveCTAs) return 1;
-  int s = (int)std::min<int64_t>(4, kAttnWaveCTAs / tiles);
+  int s = (int)std::min<int64_t>(most, kAttnWaveCTAs / tiles);
   s = std::min(s, nt / 2);
   return s < 2 ? 1 : s;
 }
@@ -451,20 +460,22 @@ namespace {
 template <int HD>
 cudaError_t launch_tma(const AttnArgs& args, bool pdl, cudaStream_t stream) {
   AttnArgs a = args;
-  if (a.nsplit < 1 || a.nsplit > 4 || (a.nsplit > 1 && (a.O_parts == nullptr || a.lse_parts == nullptr)))
+  if (a.nsplit < 1 || a.nsplit > kAttnMaxSplits || (a.nsplit > 1 && (a.O_parts == nullptr || a.lse_parts == nullptr)))
     return cudaErrorInvalidValue;
   const WaitHooks hooks = wait_hooks();
   a.wait_ns = hooks.wait_ns;
   a.inject = hooks.inject == INJECT_ATTN_TMA ? 1 : 0;
   Maps maps;
-  const int64_t oh = (int64_t)a.BCP * HD, ob = (int64_t)a.nq * oh;  // O is contiguous
-  if (!encode_bf16_4d(&maps.q, a.Q.data, HD, a.BCP, a.nq, a.b, a.Q.st, a.Q.sh, a.Q.sb, 128) ||
+  const int G = a.nq / a.nkv;
+  const int nrow = a.pack ? G * a.BCP : a.BCP, heads = a.pack ? a.nkv : a.nq;
+  const int64_t oh = (int64_t)nrow * HD, ob = (int64_t)heads * oh;  // O is contiguous
+  if (!encode_bf16_4d(&maps.q, a.Q.data, HD, nrow, heads, a.b, a.Q.st, a.pack ? G * a.Q.sh : a.Q.sh, a.Q.sb, 128) ||
       !encode_bf16_4d(&maps.kc, a.Kc.data, HD, a.BCP, a.nkv, a.b, a.Kc.st, a.Kc.sh, a.Kc.sb, 128) ||
       !encode_bf16_4d(&maps.vc, a.Vc.data, HD, a.BCP, a.nkv, a.b, a.Vc.st, a.Vc.sh, a.Vc.sb, 128) ||
-      !encode_bf16_4d(&maps.o, a.O, HD, a.BCP, a.nq, a.b, HD, oh, ob, 128))
+      !encode_bf16_4d(&maps.o, a.O, HD, nrow, heads, a.b, HD, oh, ob, 128))
     return cudaErrorNotSupported;
   if (a.nsplit > 1) {
-    if (!encode_bf16_4d(&maps.op, a.O_parts, HD, a.BCP, a.nq, (uint64_t)a.nsplit * a.b, HD, oh, ob, 128))
+    if (!encode_bf16_4d(&maps.op, a.O_parts, HD, nrow, heads, (uint64_t)a.nsplit * a.b, HD, oh, ob, 128))
       return cudaErrorNotSupported;
   } else {
     maps.op = maps.o;  // never written
@@ -481,9 +492,8 @@ cudaError_t launch_tma(const AttnArgs& args, bool pdl, cudaStream_t stream) {
   const size_t smem = sizeof(Smem) + 1024;
   cudaError_t e = cudaFuncSetAttribute(attn_tma_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int G = a.nq / a.nkv;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(G * ((a.BCP + 127) / 128) * a.nsplit, a.nkv, a.b);  // one query tile (range) per CTA
+  cfg.gridDim = dim3(heads / a.nkv * ((nrow + 127) / 128) * a.nsplit, a.nkv, a.b);  // one query tile (range) per CTA
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -501,7 +511,8 @@ cudaError_t launch_tma(const AttnArgs& args, bool pdl, cudaStream_t stream) {
   mc.stream = stream;
   mc.attrs = attr;
   mc.numAttrs = 1;  // waits for the attention inside
-  return cudaLaunchKernelEx(&mc, attn_split_merge_kernel<HD>, static_cast<const bf16*>(a.O_parts),
+  auto* merge = a.nsplit <= 4 ? attn_split_merge_kernel<HD, 4> : attn_split_merge_kernel<HD, kAttnMaxSplits>;
+  return cudaLaunchKernelEx(&mc, merge, static_cast<const bf16*>(a.O_parts),
                             static_cast<const float*>(a.lse_parts), a.nsplit, rows, static_cast<bf16*>(a.O),
                             a.lse);
 }

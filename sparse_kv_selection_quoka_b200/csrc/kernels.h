@@ -106,6 +106,10 @@ struct AttnArgs {
   int* status;
   int no_chunk = 0;         // 1: the chunk's own keys are left out (a shard's partial attention);
                             // rows with no visible key then give O = 0 and lse = -inf
+  // 1: the G * BCP query rows of a KV head are one run of rows (Q's heads follow
+  // one another without a gap: Q.sh = BCP * Q.st), cut into 128-row tiles across
+  // heads (tensor-core attention over gathered rows only)
+  int pack = 0;
   int tc_d64 = 0;           // 1: launch_attn_tc also takes d = 64 (rows already gathered)
   uint64_t wait_ns = 0;     // bound of every wait (set by the launcher from wait_hooks())
   int inject = 0;           // test hook (set by the launcher from wait_hooks())
@@ -120,10 +124,11 @@ struct AttnArgs {
 
 // Key-range splits of the tensor-core attention for a launch of `tiles`
 // 128-row query tiles with at most `nt` key tiles each: 1 when the tiles
-// already fill the GPU, else as many ranges (<= 4, each of >= 2 key tiles)
+// already fill the GPU, else as many ranges (<= most, each of >= 2 key tiles)
 // as keep the CTAs within one wave of kAttnWaveCTAs.
 constexpr int kAttnWaveCTAs = 148;  // SMs of a B200: one attention CTA per SM
-int attn_splits(int64_t tiles, int nt);
+constexpr int kAttnMaxSplits = 16;
+int attn_splits(int64_t tiles, int nt, int most = 4);  // most <= kAttnMaxSplits
 
 // Steps (f)+(g) in fp32 on the CUDA cores (any input dtype).
 cudaError_t launch_attn_simt(bool bf16, const AttnArgs& a, cudaStream_t stream);

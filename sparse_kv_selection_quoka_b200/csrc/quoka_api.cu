@@ -82,9 +82,8 @@ struct WsLayout {
 // Key-range splits of the tensor-core attention over the gathered rows
 // (bf16, d = 128) for a chunk of b * nq * ceil(BCP / 128) query tiles and
 // BSA_eff selected keys (with the chunk's own keys unless no_chunk).
-int attn_nsplit(int64_t b, int64_t nq, int64_t BCP, int64_t d, int64_t bsa_eff, bool bf16, bool no_chunk,
-                bool tc_d64 = false) {
-  if (!bf16 || (d != 128 && !tc_d64)) return 1;
+int attn_nsplit(int64_t b, int64_t nq, int64_t BCP, int64_t d, int64_t bsa_eff, bool bf16, bool no_chunk) {
+  if (!bf16 || d != 128) return 1;
   const int64_t tiles = b * nq * ((BCP + 127) / 128);
   const int64_t nt = (bsa_eff + 127) / 128 + (no_chunk ? 0 : 1);
   return quoka::attn_splits(tiles, (int)std::min<int64_t>(nt, 1 << 20));
@@ -334,10 +333,9 @@ quoka_status run_attn(const quoka_tensor* Q, Strided K, Strided V, const quoka_t
                       const quoka_tensor* Vc, const AttnShapes& s, int64_t T, const int32_t* kv_idx,
                       const int32_t* kv_count, int bsa_eff, float scale, void* O, float* lse,
                       int* status, cudaStream_t stream, bool pdl = false, bool no_chunk = false,
-                      void* parts = nullptr, size_t parts_bytes = 0, bool tc_d64 = false) {
+                      void* parts = nullptr, size_t parts_bytes = 0) {
   quoka::AttnArgs a;
   a.no_chunk = no_chunk ? 1 : 0;
-  a.tc_d64 = tc_d64 ? 1 : 0;
   a.Q = strided(Q);
   a.K = K;
   a.V = V;
@@ -359,7 +357,7 @@ quoka_status run_attn(const quoka_tensor* Q, Strided K, Strided V, const quoka_t
   if (kv_idx == nullptr && parts != nullptr) {
     // split key ranges when the query tiles leave most SMs idle and the
     // workspace holds the partials
-    const int ns = attn_nsplit(s.b, s.nq, s.BCP, s.d, bsa_eff, Q->dtype == QUOKA_BF16, no_chunk, tc_d64);
+    const int ns = attn_nsplit(s.b, s.nq, s.BCP, s.d, bsa_eff, Q->dtype == QUOKA_BF16, no_chunk);
     if (ns > 1 && parts_bytes >= attn_parts_bytes(s.b, s.nq, s.BCP, s.d, ns)) {
       const int64_t rows = (int64_t)ns * s.b * s.nq * s.BCP;
       a.nsplit = ns;
@@ -488,6 +486,18 @@ bool overlaps(const void* a, size_t na, const quoka_tensor* t) {
   return a0 < t1 && t0 < a0 + na;
 }
 
+// The attention of many bf16 query rows over dequantised rows: whether a tile
+// takes rows of several heads (fewer tiles then), and into how many ranges the
+// keys are cut.
+bool cache_attn_packs(int64_t nq, int64_t nkv, int64_t BCP) {
+  return nkv * ((nq / nkv * BCP + 127) / 128) < nq * ((BCP + 127) / 128);
+}
+int cache_attn_nsplit(int64_t b, int64_t nq, int64_t nkv, int64_t BCP, int64_t N, bool no_chunk, bool pack) {
+  const int64_t tiles = pack ? b * nkv * ((nq / nkv * BCP + 127) / 128) : b * nq * ((BCP + 127) / 128);
+  const int64_t nt = (N + 127) / 128 + (no_chunk ? 0 : (BCP + 127) / 128);
+  return quoka::attn_splits(tiles, (int)std::min<int64_t>(nt, 1 << 20), quoka::kAttnMaxSplits);
+}
+
 // Workspace of quoka_cache_attn: the status words, then either the partials
 // of the key ranges (few query rows, or fp32) or the dequantised keys and values
 // with their counts and the partials of the tensor-core attention.
@@ -517,7 +527,10 @@ CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t
     w.ksel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
     w.vsel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
     w.count = take((size_t)(b * nkv) * 4);
-    w.aparts_bytes = attn_parts_bytes(b, nq, BCP, d, attn_nsplit(b, nq, BCP, d, N, dtype == QUOKA_BF16, no_chunk, true));
+    // (whether rows can be packed depends on Q's strides: room for either)
+    const int n = std::max(cache_attn_nsplit(b, nq, nkv, BCP, N, no_chunk, false),
+                           cache_attn_packs(nq, nkv, BCP) ? cache_attn_nsplit(b, nq, nkv, BCP, N, no_chunk, true) : 1);
+    w.aparts_bytes = attn_parts_bytes(b, nq, BCP, d, n);
     w.aparts = take(w.aparts_bytes);
   }
   w.total = off;
@@ -947,13 +960,35 @@ quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, i
     if (e != cudaSuccess) return cuda_status(e);
   }
   const int64_t sh = (int64_t)N * d, sb = nkv * sh;
-  const AttnShapes s{b, nq, nkv, d, N, BCP};
-  quoka_tensor own = *Q;  // without chunk keys: any valid tensor of their shape, not read
-  own.shape[1] = nkv;
-  return run_attn(Q, Strided{at<void>(ws, w.ksel), sb, sh, d}, Strided{at<void>(ws, w.vsel), sb, sh, d},
-                  no_chunk ? &own : Kc, no_chunk ? &own : Vc, s, N, nullptr, at<int32_t>(ws, w.count), N, scale, O,
-                  lse, status, cs, true, no_chunk, w.aparts_bytes > 0 ? at<void>(ws, w.aparts) : nullptr,
-                  w.aparts_bytes, true);
+  quoka::AttnArgs t;
+  t.Q = strided(Q);
+  t.K = Strided{at<void>(ws, w.ksel), sb, sh, d};
+  t.V = Strided{at<void>(ws, w.vsel), sb, sh, d};
+  t.Kc = no_chunk ? t.Q : strided(Kc);  // (without chunk keys: any valid rows, not read)
+  t.Vc = no_chunk ? t.Q : strided(Vc);
+  t.b = (int)b;
+  t.nq = (int)nq;
+  t.nkv = (int)nkv;
+  t.d = (int)d;
+  t.BCP = (int)BCP;
+  t.T = N;
+  t.kv_idx = nullptr;
+  t.kv_count = at<int32_t>(ws, w.count);
+  t.bsa = N;
+  t.scale = scale;
+  t.O = O;
+  t.lse = lse;
+  t.status = status;
+  t.no_chunk = no_chunk ? 1 : 0;
+  t.tc_d64 = 1;
+  t.pack = cache_attn_packs(nq, nkv, BCP) && t.Q.sh == BCP * t.Q.st ? 1 : 0;
+  t.nsplit = cache_attn_nsplit(b, nq, nkv, BCP, N, no_chunk, t.pack != 0);
+  if (t.nsplit > 1) {
+    t.O_parts = at<void>(ws, w.aparts);
+    t.lse_parts = reinterpret_cast<float*>(at<char>(ws, w.aparts) + align_up((size_t)(t.nsplit * b * nq * BCP * d) * 2));
+  }
+  // (an error here is an error: there is no other path)
+  return cuda_status(quoka::launch_attn_tc(t, true, cs));
 }
 
 quoka_status quoka_get_device_status(const void* ws, void* stream, int32_t* device_status) {
