@@ -1,5 +1,5 @@
 // GQA attention over the paged 8-bit cache straight from its codes: decode steps
-// and short blocks (G * BCP <= 64 query rows per KV head), and all fp32 queries.
+// and short blocks (G * BCP <= 32 query rows per KV head), and all fp32 queries.
 //
 // [QUOKA §4.2, problem 3] the attention of the other paths,
 //   O[b,h,t] = sum_k softmax_k(scale * q . k) v,  j = floor(h / G),

@@ -217,8 +217,11 @@ cudaError_t launch_cache_gather(bool bf16, int d, const CacheGatherArgs& a, bool
 
 // Attention over the cache's codes and the chunk's own keys, by key ranges
 // joined by a second kernel (cache_attn.cu). bf16 queries with more than
-// kCacheMaxRows rows per KV head are better off with dequantised rows.
-constexpr int kCacheMaxRows = 64;  // G * BCP
+// kCacheMaxRows rows per KV head are better off with dequantised rows and the
+// tcgen05 attention: 8 KV heads, 8192 keys, d = 128: 32 rows 23.9 us from the
+// codes and 28.8 that way, 48 rows 30.5 and 29.3; 16 sequences of 2000 keys: 32
+// rows 49.1 and 60.6, 48 rows 79.6 and 60.6.
+constexpr int kCacheMaxRows = 32;  // G * BCP
 struct CacheAttnArgs {
   CacheView c;
   Strided Q, Kc, Vc;

@@ -172,7 +172,8 @@ def attention(c, Q, Kc, Vc, idx=None, counts=None, scale=None):
 
 
 def check_attention(O, lse, want, dt, d, n, few):
-    """Bounds on the kernels' roundings:
+    """Bounds on the kernels' roundings; few: at most 32 query rows per KV head,
+    the codes' own kernel (fp32 always takes it).
     score: d fp32 additions of a tensor-core product, each off by at most
       2^-22 of the sum of magnitudes (`size`), and the fp32 query as two halves
       (2^-22): ds = (d + 8) 2^-22 size;
@@ -503,7 +504,7 @@ def test_attention(k):
     O, lse = q().quoka_cache_attn(strided(Q), c.cuda(), max_len, up(idx), up(counts), None if Kc is None else strided(Kc),
                                   None if Vc is None else strided(Vc), want_lse=True, ws=ws)
     assert q().quoka_get_device_status(ws) == 0
-    check_attention(O, lse, attention(c, Q, Kc, Vc, idx, counts), dt, d, (N or max_len) + BCP, nq // nkv * BCP <= 64)
+    check_attention(O, lse, attention(c, Q, Kc, Vc, idx, counts), dt, d, (N or max_len) + BCP, nq // nkv * BCP <= 32)
 
 
 @gpu
@@ -599,7 +600,7 @@ def test_serving_loop(dt, d):
         want = attention(c, Qr.cpu(), Kr.cpu(), V, idx.cpu(), cnt.cpu())
         for i, m in enumerate(new):  # rows of padded tokens are nobody's
             check_attention(O[i:i + 1, :, :m], lse[i:i + 1, :, :m], [w[i:i + 1, :, :m] for w in want], dt, d,
-                            idx.shape[2] + BCP, nq // nkv * BCP <= 64) if m else None
+                            idx.shape[2] + BCP, nq // nkv * BCP <= 32) if m else None
         append(c, K, V, cos, sin, False, new)
         assert same_codes(dev.k.cpu(), c.k) and same_codes(dev.v.cpu(), c.v)
         assert torch.equal(dev.k_scale.cpu(), c.k_scale) and torch.equal(dev.v_scale.cpu(), c.v_scale)
