@@ -24,7 +24,10 @@
 // the two halves of its pairs, and issues all its loads before it computes.
 // Bound by bytes: every row is read once and written once as codes (and once
 // rotated); a chunk of few tokens by the chain length, page, scale, and takes
-// small CTAs so that all of them are resident at once.
+// small CTAs so that all of them are resident at once. Measured (32 query and 8
+// KV heads, d = 128, bf16): 4 x 2048 tokens 37.7 us for 205.5 MB, 5.4 TB/s; one
+// token of 64 sequences 5.8 us with CTAs of 64 threads, 11.3 with 256 (which are
+// then not all resident) and each element's partner loaded a second time.
 #include "cache.cuh"
 
 namespace quoka {

@@ -42,7 +42,12 @@
 // stands for key n ^ 4 (n & 1), so that neither read has a bank conflict
 // (d = 128; d = 64 keeps a two-way one on V). A second kernel joins the ranges
 // of every query row and adds the chunk's own keys in fp32.
-// Bound by the cache's bytes, each read once per 64 query rows.
+// Bound by the cache's bytes, each read once per 64 query rows. Measured: a
+// decode step of 32 ragged sequences of up to 8192 keys, 32 query and 8 KV heads,
+// d = 128: 61.5 us for 337.9 MB, 5.5 TB/s, and 6 us for the join (187 us when every
+// warp loaded its own fragments from global memory, 76.6 with a cp.async ring);
+// the products left out of that kernel, it took 66 us. One sequence of 4096
+// listed keys: 9.2 us, a chain of count, list, table, rows; join 6.5.
 #include <algorithm>
 
 #include "cache.cuh"

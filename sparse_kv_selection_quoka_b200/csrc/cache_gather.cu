@@ -10,7 +10,10 @@
 // Bound by bytes: a row of d codes is read, one of d bf16 or fp32 written. A
 // warp takes 16 rows: each is looked up by one lane, then all their code loads
 // (K and V) are issued together and converted as they arrive, 16 bytes of
-// output a lane, consecutive lanes writing consecutive bytes.
+// output a lane, consecutive lanes writing consecutive bytes. Measured: 4096 of
+// 32768 rows of 8 heads, d = 128, bf16 7.6 us for 25.2 MB (10.9 with every lane
+// looking up its own 8 codes); 5 ragged sequences of up to 2999 rows, d = 64,
+// fp32 8.1 us for 35.5 MB (15.1).
 #include "cache.cuh"
 
 namespace quoka {
