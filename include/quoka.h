@@ -469,8 +469,9 @@ quoka_status quoka_cache_gather(const quoka_cache* cache, int max_len,
  * row), or over all keys below seq_len (kv_idx and kv_count NULL, N =
  * max_len), and over the chunk's own keys Kc[b, j, s], s <= t (Kc and Vc both
  * NULL: without them).
- *   Q (b, nq, BCP, d); Kc, Vc (b, nkv, BCP, d), dtype of Q; O out
- *   (b, nq, BCP, d), contiguous; lse out (b, nq, BCP) float or NULL. A row
+ *   Q (b, nq, BCP, d); Kc, Vc (b, nkv, BCP, d), dtype of Q (every row of Vc
+ *   finite, those of padding too: a chunk of many bf16 rows multiplies rows
+ *   that the mask leaves out by zero); O out (b, nq, BCP, d), contiguous; lse out (b, nq, BCP) float or NULL. A row
  *   that sees no key gives O = 0, lse = -inf.
  *   ws at least quoka_cache_attn_workspace_size() bytes, 256-byte aligned. */
 size_t quoka_cache_attn_workspace_size(int b, int nq, int nkv, int d, int BCP,

@@ -160,6 +160,11 @@ topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const ui
     sh.kmax = 0u;
     sh.gt0 = 0u;
     sh.ncand = 0u;
+    // (what the steps below leave when a histogram does not fit the scores, as
+    // when the caller changes a length while the call runs: the same in every CTA)
+    sh.bin = sh.above = sh.bincount = 0u;
+    sh.ustar = 0xFFFFFFFFu;
+    sh.need_eq = 0u;
   }
   if (tid < TOPK_MAX_CLUSTER) {
     sh.rc_gtc[tid] = 0u;

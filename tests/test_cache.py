@@ -676,6 +676,100 @@ def test_calls_on_a_given_stream_and_repeatable():
         assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+class Fenced:
+    """A buffer of n bytes between two runs of 4 KB that no call may touch."""
+
+    def __init__(self, n):
+        self.raw = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.ws = self.raw[4096:4096 + n]
+
+    def like(self, shape, dtype):
+        return self.ws.view(dtype).view(shape)
+
+    def whole(self):
+        return bool((self.raw[:4096] == 0xA5).all() and (self.raw[4096 + self.ws.numel():] == 0xA5).all())
+
+
+@gpu
+@pytest.mark.parametrize("dt,BCP", [("bf16", 1), ("bf16", 70), ("f32", 40)])
+def test_calls_write_only_inside_outputs_and_workspace(dt, BCP):
+    """Outputs and workspaces of exactly the sizes asked for, fenced; keys and
+    values are the two halves of one pool."""
+    m, t, es = q(), TYPES[dt], torch.finfo(TYPES[dt]).bits // 8
+    b, nkv, nq, d, page, held = 3, 2, 6, 64, 32, [50, 0, 131]
+    c = Pages(held, [n + BCP for n in held], nkv, d, page, 21, scales=(-9, -5))
+    pool = torch.stack((c.k, c.v), 1).cuda()  # (npages, 2, nkv, page, d)
+    before = pool.clone()
+    cache = m.QuokaCache(pool[:, 0], pool[:, 1], c.k_scale.cuda(), c.v_scale.cuda(), c.table.cuda(),
+                         torch.tensor(held, dtype=torch.int32).cuda())
+    K, V, Q = (randn(s, b, h, BCP, d).to(t).cuda() for s, h in ((1, nkv), (2, nkv), (3, nq)))
+    cos, sin = (x.cuda() for x in angles(200 + BCP, 32))
+    kr, qr, st = Fenced(K.numel() * es), Fenced(Q.numel() * es), Fenced(256)
+    Kr, Qr = kr.like(K.shape, t), qr.like(Q.shape, t)
+    m.quoka_cache_append(cache, K, V, Q, cos, sin, Kr=Kr, Qr=Qr, ws=st.ws)
+    touched = torch.zeros(pool.shape[0], page, dtype=torch.bool)
+    for i, n in enumerate(held):
+        for pos in range(n // page * page, n + BCP):  # a half-full page may be brought to a new scale
+            touched[int(c.table[i, pos // page]), pos % page] = True
+    same = (pool == before).all(-1).all(2).all(1).cpu()
+    assert same[~touched].all() and kr.whole() and qr.whole() and st.whole()
+    cache.seq_len += BCP
+    L, NQ, BSA = 131 + BCP, min(2, BCP), 40
+    pool0, scales0 = pool.clone(), cache.k_scale.clone()
+    n = m.quoka_select_workspace_size(b, nq, nkv, d, L, BCP, NQ, BSA, t)
+    ws, ix, ct, sc = Fenced(n), Fenced(b * nkv * BSA * 4), Fenced(b * nkv * 4), Fenced(b * nkv * L * 4)
+    idx, cnt = ix.like((b, nkv, BSA), torch.int32), ct.like((b, nkv), torch.int32)
+    m.quoka_cache_select(Qr, cache, L, NQ, BSA, kv_idx=idx, kv_count=cnt, s_agg=sc.like((b, nkv, L), torch.float32), ws=ws.ws)
+    assert ws.whole() and ix.whole() and ct.whole() and sc.whole() and m.quoka_get_device_status(ws.ws) == 0
+    for args, N in (((idx, cnt), BSA), ((), L)):
+        ks, vs = Fenced(b * nkv * N * d * es), Fenced(b * nkv * N * d * es)
+        m.quoka_cache_gather(cache, L, *args, dtype=t, Ksel=ks.like((b, nkv, N, d), t), Vsel=vs.like((b, nkv, N, d), t), ws=st.ws)
+        assert ks.whole() and vs.whole() and st.whole()
+        for own in ((K, V), (None, None)):
+            n = m.quoka_cache_attn_workspace_size(b, nq, nkv, d, BCP, N, t)
+            ws, o, ls = Fenced(n), Fenced(Q.numel() * es), Fenced(b * nq * BCP * 4)
+            O, lse = o.like(Q.shape, t), ls.like((b, nq, BCP), torch.float32)
+            m.quoka_cache_attn(Qr, cache, L, *(args or (None, None)), *own, O=O, lse=lse, ws=ws.ws)
+            assert ws.whole() and o.whole() and ls.whole() and m.quoka_get_device_status(ws.ws) == 0
+            assert O.isfinite().all() and lse.isfinite().all()
+    assert torch.equal(pool, pool0) and torch.equal(cache.k_scale, scales0)
+
+
+@gpu
+def test_two_streams_at_once():
+    """Two calls on two streams with workspaces of their own give what they
+    give one after the other."""
+    m = q()
+    jobs = []
+    for k, (BCP, dt) in enumerate(((1, "bf16"), (90, "bf16"), (5, "f32"))):
+        c = Pages([3000, 1000], [3000, 1000], 2, 128, 64, 30 + k, scales=(-9, -5)).cuda()
+        jobs.append((randn(40 + k, 2, 8, BCP, 128).to(TYPES[dt]).cuda(), c))
+
+    def work(Q, c, s=None):
+        idx, cnt, _, _ = m.quoka_cache_select(Q, c, 3000, 1, 200, stream=s)
+        return [m.quoka_cache_attn(Q, c, 3000, stream=s)[0], m.quoka_cache_attn(Q, c, 3000, idx, cnt, stream=s)[0], cnt]
+
+    want = [work(*j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        got = [work(*j, s) for j, s in zip(jobs, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
+@gpu
+@pytest.mark.parametrize("rows,T,BSA", [(20, 33000, 4000), (40, 20001, 100), (130, 9000, 8999), (600, 5000, 1), (74, 40000, 777)])
+def test_topk_of_many_rows(rows, T, BSA):
+    """Rows that alone fill the GPU take fewer, longer slices; values on a coarse
+    grid, so that many are equal: ties go to the lower index."""
+    s = (torch.randint(-200, 200, (rows, 1, T), generator=torch.Generator().manual_seed(rows)).float() / 200).cuda()
+    idx, cnt = q().quoka_topk(s, BSA)
+    want = s.sort(dim=-1, descending=True, stable=True).indices[..., :BSA].sort(-1).values
+    assert (cnt == BSA).all() and torch.equal(idx.long(), want)
+
+
 @gpu
 def test_long_table_offsets_pass_32_bits():
     """A pool of more than 2^32 bytes, with the pages of a sequence at both ends."""
