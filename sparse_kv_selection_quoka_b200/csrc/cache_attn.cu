@@ -192,26 +192,12 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
       break;
     }
     const uint32_t dst = sm100::smem_u32(ring + st * R::kPitch);
-    uint32_t* ex = sh.ex[st];
-    uint32_t e[NU];
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      int ek = 0, ev = 0;
-      if (held(pg[0][u])) {
-        ek = scale_exp(ks[u], &bad);
-        ev = scale_exp(vs[u], &bad);
-      } else {
-        bad |= here(s, u);  // reads as zeros
-      }
-      e[u] = (uint32_t)(ek + 64) | (uint32_t)(ev + 64) << 16;
-    }
+    // the copies first: the scales may still be on their way
     if constexpr (IDX) {
       int64_t off[NU];
 #pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        ex[lane + 32 * u] = e[u];
+      for (int u = 0; u < NU; ++u)
         off[u] = held(pg[0][u]) ? pg[0][u] * a.c.sp + (int64_t)(tau[0][u] & pmask) * a.c.sr : -1;
-      }
       const int c = lane % CPR, r0 = lane / CPR;
       const uint8_t* kb = a.c.k + j * a.c.sh + 16 * c;
       const uint8_t* vb = a.c.v + j * a.c.sh + 16 * c;
@@ -225,21 +211,32 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
         sm100::cp_async_16(dst + R::kBytes + at, vb + so, n);
       }
       sm100::cp_async_arrive_noinc(&sh.full[st]);
-      sm100::mbar_arrive(&sh.full[st]);  // (releases the exponents)
-    } else {
-#pragma unroll
-      for (int i = 0; i < kStage / 32; ++i) ex[lane + 32 * i] = __shfl_sync(0xffffffffu, e[0], (lane + 32 * i) >> blog);
-      if (here(s, 0)) {
-        const uint32_t at = dst + ((lane << blog) * D);
-        // (a page that is not there lies out of bounds: zeros)
-        const int p = held(pg[0][0]) ? pg[0][0] : a.c.npages, r = tau[0][0] & pmask;
-        sm100::mbar_arrive_expect_tx(&sh.full[st], 2u * D << blog);
-        sm100::tma_load_4d(at, &maps.k, &sh.full[st], 0, r, j, p);
-        sm100::tma_load_4d(at + R::kBytes, &maps.v, &sh.full[st], 0, r, j, p);
-      } else {
-        sm100::mbar_arrive(&sh.full[st]);
-      }
+    } else if (here(s, 0)) {
+      const uint32_t at = dst + ((lane << blog) * D);
+      // (a page that is not there lies out of bounds: zeros)
+      const int p = held(pg[0][0]) ? pg[0][0] : a.c.npages, r = tau[0][0] & pmask;
+      sm100::mbar_expect_tx(&sh.full[st], 2u * D << blog);
+      sm100::tma_load_4d(at, &maps.k, &sh.full[st], 0, r, j, p);
+      sm100::tma_load_4d(at + R::kBytes, &maps.v, &sh.full[st], 0, r, j, p);
     }
+    __syncwarp();
+    uint32_t* ex = sh.ex[st];
+    uint32_t e[NU];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      int ek = 0, ev = 0;
+      if (held(pg[0][u])) {
+        ek = scale_exp(ks[u], &bad);
+        ev = scale_exp(vs[u], &bad);
+      } else {
+        bad |= here(s, u);  // reads as zeros
+      }
+      e[u] = (uint32_t)(ek + 64) | (uint32_t)(ev + 64) << 16;
+    }
+#pragma unroll
+    for (int i = 0; i < kStage / 32; ++i)
+      ex[lane + 32 * i] = IDX ? e[i % NU] : __shfl_sync(0xffffffffu, e[0], (lane + 32 * i) >> blog);
+    sm100::mbar_arrive(&sh.full[st]);  // (releases the exponents)
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       tau[0][u] = tau[1][u];
