@@ -239,6 +239,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(QSEL_CL_THREADS)
 qsel_cluster_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int BCP, int NQ,
                     int slice, float* __restrict__ Qhat, int32_t* __restrict__ q_idx, int normalize) {
+  pdl_trigger();  // the group mean's launch overlaps this kernel
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks();
@@ -360,24 +361,26 @@ __global__ void __launch_bounds__(D)
 qgroup_kernel(const float* __restrict__ Qhat, int nq, int NQ, float* __restrict__ Qg,
               bf16* __restrict__ Qg_hilo, uint32_t* __restrict__ hist, int* __restrict__ status) {
   const int i = blockIdx.x, j = blockIdx.y, bi = blockIdx.z, nkv = gridDim.y;
+  pdl_trigger();  // (the scoring kernel waits for this one's outputs)
   clear_status(status);  // (the query select before it latches nothing)
   const int G = nq / nkv;
   const int k = threadIdx.x;
-  float acc = 0.f;
-  for (int g = 0; g < G; ++g) acc += Qhat[(((int64_t)bi * nq + j * G + g) * NQ + i) * D + k];
-  const float v = acc / (float)G;
   const int64_t row = (int64_t)bi * nkv + j;
+  if (hist != nullptr) {
+    // the NQ blocks of a row zero its histogram between them
+    uint32_t* h = hist + row * TOPK_HIST_BINS;
+    for (int e = i * D + k; e < TOPK_HIST_BINS; e += NQ * D) h[e] = 0u;
+  }
+  pdl_wait();  // the chosen queries come from the query select
+  float acc = 0.f;
+  for (int g = 0; g < G; ++g) acc += __ldcg(Qhat + (((int64_t)bi * nq + j * G + g) * NQ + i) * D + k);
+  const float v = acc / (float)G;
   Qg[(row * NQ + i) * D + k] = v;
   if (Qg_hilo != nullptr) {
     const bf16 hi = __float2bfloat16_rn(v);
     const bf16 lo = __float2bfloat16_rn(v - __bfloat162float(hi));
     Qg_hilo[(row * 2 * NQ + i) * D + k] = hi;
     Qg_hilo[(row * 2 * NQ + NQ + i) * D + k] = lo;
-  }
-  if (hist != nullptr) {
-    // the NQ blocks of a row zero its histogram between them
-    uint32_t* h = hist + row * TOPK_HIST_BINS;
-    for (int e = i * D + k; e < TOPK_HIST_BINS; e += NQ * D) h[e] = 0u;
   }
 }
 
@@ -445,12 +448,18 @@ cudaError_t launch_qsel(bool is_bf16, int d, Strided Q, int b, int nq, int BCP, 
 
 cudaError_t launch_qgroup(int d, const float* Qhat, int b, int nq, int nkv, int NQ, float* Qg,
                           uint16_t* Qg_hilo, uint32_t* hist, int* status, cudaStream_t stream) {
-  dim3 grid(NQ, nkv, b);
-  bf16* hl = reinterpret_cast<bf16*>(Qg_hilo);
-  if (d == 128) qgroup_kernel<128><<<grid, 128, 0, stream>>>(Qhat, nq, NQ, Qg, hl, hist, status);
-  else if (d == 64) qgroup_kernel<64><<<grid, 64, 0, stream>>>(Qhat, nq, NQ, Qg, hl, hist, status);
-  else return cudaErrorNotSupported;
-  return cudaGetLastError();
+  if (d != 64 && d != 128) return cudaErrorNotSupported;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(NQ, nkv, b);
+  cfg.blockDim = dim3(d);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;  // waits for the query select inside
+  return cudaLaunchKernelEx(&cfg, d == 128 ? qgroup_kernel<128> : qgroup_kernel<64>, Qhat, nq, NQ, Qg,
+                            reinterpret_cast<bf16*>(Qg_hilo), hist, status);
 }
 
 }  // namespace quoka

@@ -26,6 +26,10 @@
 //      keys == u* needed to reach BSA: each warp owns a contiguous segment of
 //      the slice, counts its picks, one block scan gives every warp its
 //      offset, and the warp writes its picks in order with ballots.
+// Rows of at most TOPK_SMALL keys take one small CTA with the keys in registers
+// instead: a search of the key's bits from the top, two at a time, by counting
+// the keys at or above three thresholds (one block barrier a step), then one
+// scan that places the picks. 18 rows of 64 keys 7.2 -> 5.3 us, 4 of 905 7.6 -> 6.2.
 // When a bucket holds more candidates than the gathered list can take, the
 // exact passes run over every slice instead, their histograms summed over
 // the cluster through distributed shared memory.
@@ -600,6 +604,94 @@ topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const ui
   }
 }
 
+constexpr int TOPK_SMALL = 2048;
+constexpr int TOPK_SMALL_THREADS = 256;
+
+// One CTA per row, KPT consecutive keys a thread.
+template <int KPT>
+__global__ void __launch_bounds__(TOPK_SMALL_THREADS)
+topk_small_kernel(const float* __restrict__ S, int64_t T, int bsa, const int32_t* __restrict__ row_len,
+                  int32_t* __restrict__ kv_idx, int32_t* __restrict__ kv_count, const int* __restrict__ status) {
+  constexpr int WARPS = TOPK_SMALL_THREADS / 32;
+  __shared__ uint2 counts[2][WARPS];
+  __shared__ uint32_t wsum[WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int j = blockIdx.x, bi = blockIdx.y, nkv = gridDim.x;
+  const int64_t row = (int64_t)bi * nkv + j;
+  const int n = row_len != nullptr ? (int)max((int64_t)0, min((int64_t)__ldg(row_len + bi), T)) : (int)T;
+  const int take = min(bsa, n);
+  pdl_trigger();
+  pdl_wait();  // the scores come from the previous kernel
+  const int fault = status != nullptr ? __ldcg(status) : 0;
+  uint32_t k[KPT];  // (keys past the row's end count as 0, the lowest: they never tie with a pick before a real key)
+  const float* Sr = S + row * T + KPT * tid;
+#pragma unroll
+  for (int u = 0; u < KPT; ++u) k[u] = KPT * tid + u < n ? score_key(__ldcg(Sr + u)) : 0u;
+  if (fault != 0 || take == 0) {
+    if (tid == 0) kv_count[row] = 0;
+    return;
+  }
+  // u*: the largest value that at least `take` keys reach
+  uint32_t ustar = 0u;
+  for (int shift = 30, p = 0; shift >= 0; shift -= 2, p ^= 1) {
+    const uint32_t t1 = ustar | 1u << shift, t2 = ustar | 2u << shift, t3 = ustar | 3u << shift;
+    uint32_t c12 = 0u, c3 = 0u;
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) {
+      c12 += (k[u] >= t1 ? 1u : 0u) + (k[u] >= t2 ? 0x10000u : 0u);
+      c3 += k[u] >= t3 ? 1u : 0u;
+    }
+    c12 = __reduce_add_sync(0xffffffffu, c12);
+    c3 = __reduce_add_sync(0xffffffffu, c3);
+    if (lane == 0) counts[p][warp] = make_uint2(c12, c3);
+    __syncthreads();  // (the other buffer was read before this barrier)
+    c12 = c3 = 0u;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const uint2 c = counts[p][w];
+      c12 += c.x;
+      c3 += c.y;
+    }
+    if (c3 >= (uint32_t)take) ustar = t3;
+    else if (c12 >> 16 >= (uint32_t)take) ustar = t2;
+    else if ((c12 & 0xFFFFu) >= (uint32_t)take) ustar = t1;
+  }
+  // the keys above u* and, in index order, the first of those equal to it
+  uint32_t gt = 0u, eq = 0u;
+#pragma unroll
+  for (int u = 0; u < KPT; ++u) {
+    const bool in = KPT * tid + u < n;
+    gt += in && k[u] > ustar;
+    eq += in && k[u] == ustar;
+  }
+  uint32_t incl = gt << 16 | eq;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  uint32_t before = incl - (gt << 16 | eq), all = 0u;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const uint32_t v = wsum[w];
+    if (w < warp) before += v;
+    all += v;
+  }
+  const uint32_t need_eq = (uint32_t)take - (all >> 16);  // picks among the equal keys
+  uint32_t eq_seen = before & 0xFFFFu, pos = (before >> 16) + min(eq_seen, need_eq);
+  int32_t* dst = kv_idx + row * bsa;
+#pragma unroll
+  for (int u = 0; u < KPT; ++u) {
+    if (KPT * tid + u >= n) continue;
+    bool pick = k[u] > ustar;
+    if (k[u] == ustar) pick = eq_seen++ < need_eq;
+    if (pick) dst[pos++] = KPT * tid + u;
+  }
+  if (tid == 0) kv_count[row] = take;
+}
+
 }  // namespace
 
 int64_t topk_max_T() { return (int64_t)TOPK_MAX_CLUSTER * TOPK_MAX_SLICE; }
@@ -610,6 +702,20 @@ cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, 
   // (every wait in the kernel is a hardware barrier phase that all threads
   // reach; `status` is only read, to skip the select after an earlier fault)
   if (bsa <= 0 || T <= 0 || bsa > T || T > topk_max_T()) return cudaErrorInvalidValue;
+  if (T <= TOPK_SMALL) {
+    auto* small = T <= 256 ? topk_small_kernel<1> : T <= 512 ? topk_small_kernel<2>
+                : T <= 1024 ? topk_small_kernel<4> : topk_small_kernel<8>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(nkv, b);
+    cfg.blockDim = dim3(TOPK_SMALL_THREADS);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, small, S_agg, T, bsa, row_len, kv_idx, kv_count, static_cast<const int*>(status));
+  }
   int C = (int)((T + TOPK_SLICE_TARGET - 1) / TOPK_SLICE_TARGET);
   // no more CTAs than SMs while the slices allow it: two on an SM only slow
   // each other's phases (issue- and barrier-bound)
