@@ -835,7 +835,13 @@ quoka_status quoka_cache_select(const quoka_tensor* Q, const quoka_cache* cache,
   a.hist = at<uint32_t>(ws, L.hist);
   // (the status words and the histogram are cleared by the kernel that makes the group means)
   cudaError_t e = cudaErrorNotSupported;
-  if (bf && d == 128)
+  // The fused query select takes an SM per query head for any chunk length: with
+  // more heads than one round holds, short chunks are faster through the
+  // general kernels (whole call, 1000 keys, 16 sequences x 32 heads: 16 tokens 34.1
+  // us against 42.8 fused, 64 39.0 and 43.1, 128 47.9 and 43.2; 1 x 32 heads: 16.5
+  // both at 16, 20.6 and 16.5 at 128).
+  const bool fused = BCP == 1 || BCP > 64 || (int64_t)b * nq <= 128;
+  if (bf && d == 128 && fused)
     e = quoka::launch_qsel_group_fast(strided(Q), b, nq, nkv, BCP, NQ, qidx, qg, nullptr, a.hist, a.status, true, cs);
   if (e == cudaErrorNotSupported) {
     e = quoka::launch_qsel(bf, d, strided(Q), b, nq, BCP, NQ, at<float>(ws, L.qhat), qidx, true, cs);

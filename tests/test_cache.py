@@ -372,6 +372,7 @@ SELECTS = [
     ([20000], 20000, 1, 4, 64, 64, 33, 8, 4000, "bf16", "hnd"),
     ([(71 * i) % 311 for i in range(50)], 310, 3, 3, 128, 16, 1, 1, 40, "bf16", "hnd"),  # 150 rows, ragged
     ([513, 512], 1025, 1, 5, 64, 16, 9, 5, 100, "bf16", "nhd"),
+    ([300] * 5 + [7] * 12, 300, 2, 8, 128, 32, 12, 3, 30, "bf16", "hnd"),  # more query heads than SMs
 ]
 
 
