@@ -497,7 +497,7 @@ quoka_status quoka_get_device_status(const void* ws, void* stream,
  * latched no device fault, else a small code naming the kernel and the wait
  * or check where the first fault happened (diagnostic only; the codes of
  * the scoring kernel are 51-57, those of the attention 11-15, 21-27 and
- * 31-33). ws = NULL as for quoka_get_device_status. Returns as
+ * 31-33, those of the cache's kernels 61-66). ws = NULL as for quoka_get_device_status. Returns as
  * quoka_get_device_status. */
 quoka_status quoka_get_device_fault_site(const void* ws, void* stream,
                                          int32_t* site);

@@ -259,5 +259,7 @@ struct CacheScoreArgs {
   int target = 1;  // ranges asked for (set by the launcher)
 };
 cudaError_t launch_cache_score(int d, const CacheScoreArgs& a, cudaStream_t stream);
+// More than four group means of it (cache_score_tc.cu; called by launch_cache_score).
+cudaError_t launch_cache_score_tc(int d, const CacheScoreArgs& a, cudaStream_t stream);
 
 }  // namespace quoka
