@@ -595,6 +595,8 @@ class QuokaCache:
                 page_table.shape[0] < 1 or page_table.shape[1] < 1:
             raise ValueError("page_table must be (b, max_pages) int32 with contiguous rows")
         b, max_pages = page_table.shape
+        if b > 1 and page_table.stride(0) < max_pages:
+            raise ValueError("the rows of page_table must not overlap")
         _expect(seq_len, "seq_len", torch.int32, (b,), k.device)
         if v.device != k.device or page_table.device != k.device:
             raise ValueError("the cache's tensors must be on one device")

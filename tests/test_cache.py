@@ -829,6 +829,17 @@ def test_cache_refuses_bad_tensors():
             cpu_cache(**kw)
 
 
+def test_cache_refuses_a_page_table_of_overlapping_rows():
+    """Rows of a table are table_stride >= max_pages entries apart: one row for all
+    sequences would be read past its end."""
+    row = torch.zeros(1, 4, dtype=torch.int32)
+    assert cpu_cache(page_table=row, seq_len=torch.zeros(1, dtype=torch.int32))._view.table_stride == 4
+    assert cpu_cache(page_table=torch.zeros(3, 9, dtype=torch.int32)[:, :4])._view.table_stride == 9
+    for table in (row.expand(3, 4), torch.zeros(9, dtype=torch.int32).as_strided((3, 4), (2, 1))):
+        with pytest.raises(ValueError):
+            cpu_cache(page_table=table)
+
+
 def test_calls_refuse_bad_tensors(lib):  # noqa: F811
     m, c = q(), cpu_cache()
     K, Q = torch.zeros(3, 2, 7, 64), torch.zeros(3, 4, 7, 64)
