@@ -736,6 +736,7 @@ __global__ void __launch_bounds__(MT) cache_merge_kernel(const CacheAttnArgs a) 
 // A row takes 512 threads while every row has an SM for itself (its keys are then
 // cut into many ranges), else 128.
 constexpr int kManyRows = 149;
+constexpr int kMostChunk = 16384;  // the longest chunk the C ABI takes
 
 template <typename T, int D, int MT>
 cudaError_t launch_merge(const CacheAttnArgs& a, cudaStream_t stream) {
@@ -752,7 +753,7 @@ cudaError_t launch_merge(const CacheAttnArgs& a, cudaStream_t stream) {
   auto* kern = cache_merge_kernel<T, D, MT>;
   if (mc.dynamicSmemBytes > 16 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mc.dynamicSmemBytes);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostChunk * (int)sizeof(float));
     if (e != cudaSuccess) return e;
   }
   return cudaLaunchKernelEx(&mc, kern, a);
@@ -764,7 +765,9 @@ cudaError_t launch_typed(const CacheAttnArgs& a, cudaStream_t stream) {
   const int tiles8 = RT == 1 ? 1 : R <= 16 ? 2 : R <= 32 ? 4 : 8;
   const size_t smem = smem_bytes<D, sizeof(T) == 2 ? 1 : 2>(tiles8);
   auto* kern = a.kv_idx != nullptr ? cache_slice_kernel<T, D, true, RT> : cache_slice_kernel<T, D, false, RT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (the same bound in every call: another thread's launch may come in between)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem_bytes<D, sizeof(T) == 2 ? 1 : 2>(RT == 1 ? 1 : 8));
   if (e != cudaSuccess) return e;
   Maps maps = {};
   const int page = 1 << a.c.page_log2, box = 1 << box_log2(a.c);
@@ -797,7 +800,7 @@ cudaError_t launch_cache_attn(bool is_bf16, int d, const CacheAttnArgs& args, cu
   CacheAttnArgs a = args;
   const int R = (a.nq / a.c.nkv) * a.BCP;
   const int64_t rows = (int64_t)a.b * a.c.nkv, ranges = cache_attn_ranges(rows, R, a.N);
-  if (R < 1) return cudaErrorInvalidValue;
+  if (R < 1 || a.BCP > kMostChunk) return cudaErrorInvalidValue;
   if (ranges * ((R + kBlockRows - 1) / kBlockRows) > 0x7FFFFFFF || (int64_t)a.b * a.nq * a.BCP > 0x7FFFFFFF) return cudaErrorNotSupported;
   a.target = (int)range_target(rows, split_ctas(R));
   a.ranges = (int)ranges;

@@ -325,7 +325,9 @@ cudaError_t launch_typed(const CacheScoreArgs& args, cudaStream_t stream) {
   auto* kern = cache_score_tc_kernel<D, P>;
   const int groups = ((a.NQ < Pass<P>::kMost ? a.NQ : Pass<P>::kMost) + Pass<P>::kPer - 1) / Pass<P>::kPer;
   const size_t smem = (size_t)kRingBytes + (size_t)32 * groups * D + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (the same bound in every call: another thread's launch may come in between)
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kRingBytes + 32 * kMaxGroups * D + 1024);
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   if (!encode_codes_4d(&map, a.c.k, D, 1 << a.c.page_log2, a.c.nkv, a.c.npages, a.c.sr, a.c.sh, a.c.sp, 1 << box_log2(a.c)))

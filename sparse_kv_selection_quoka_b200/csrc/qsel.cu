@@ -395,7 +395,8 @@ static cudaError_t qsel_typed(Strided Q, int b, int nq, int BCP, int NQ, float* 
                             (size_t)(slice + BCP) * sizeof(float);
     if (cl_bytes <= QSEL_STAGED_MAX_BYTES) {
       auto kern = qsel_cluster_kernel<T, D>;
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cl_bytes);
+      // (here and below the same bound in every call: another thread's launch may come in between)
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QSEL_STAGED_MAX_BYTES);
       if (e != cudaSuccess) return e;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(C, nq, b);
@@ -417,7 +418,7 @@ static cudaError_t qsel_typed(Strided Q, int b, int nq, int BCP, int NQ, float* 
   const size_t staged = blk_bytes + (size_t)BCP * sizeof(float) + (size_t)NQ * sizeof(int);
   if (staged <= QSEL_STAGED_MAX_BYTES) {
     auto kern = qsel_staged_kernel<T, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)staged);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QSEL_STAGED_MAX_BYTES);
     if (e != cudaSuccess) return e;
     kern<<<dim3(nq, b), QSEL_STAGED_THREADS, staged, stream>>>(static_cast<const T*>(Q.data), Q.sb, Q.sh, Q.st,
                                                                BCP, NQ, Qhat, q_idx, (int)normalize);
@@ -426,7 +427,7 @@ static cudaError_t qsel_typed(Strided Q, int b, int nq, int BCP, int NQ, float* 
   const size_t smem = (size_t)BCP * sizeof(float) + (size_t)NQ * sizeof(int);
   auto kern = qsel_kernel<T, D>;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QSEL_STAGED_MAX_BYTES);
     if (e != cudaSuccess) return e;
   }
   kern<<<dim3(nq, b), QSEL_THREADS, smem, stream>>>(static_cast<const T*>(Q.data), Q.sb, Q.sh, Q.st,

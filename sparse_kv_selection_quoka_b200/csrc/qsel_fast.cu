@@ -351,8 +351,9 @@ cudaError_t launch_qsel_group_fast(Strided Q, int b, int nq, int nkv, int BCP, i
     return cudaErrorNotSupported;
   if (nkv > 65535 || b > 65535) return cudaErrorNotSupported;
   const size_t smem = (size_t)BCP * 256;
+  // (the same bound in every call: another thread's launch may come in between)
   cudaError_t e = cudaFuncSetAttribute(qsel_fast_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(smem < 1024 ? 1024 : smem));
+                                       QF_MAX_BCP * 256);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(G, nkv, b);

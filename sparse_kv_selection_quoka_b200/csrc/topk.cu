@@ -728,7 +728,9 @@ cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, 
   if (slice > TOPK_MAX_SLICE) return cudaErrorInvalidValue;
   const size_t smem = ((size_t)slice + 2 * TOPK_LIST_MAX) * sizeof(uint32_t);
   auto kern = C == 1 ? topk_kernel<false> : topk_kernel<true>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (the same bound in every call: another thread's launch may come in between)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (TOPK_MAX_SLICE + 2 * TOPK_LIST_MAX) * (int)sizeof(uint32_t));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(C, nkv, b);

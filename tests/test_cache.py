@@ -2,6 +2,7 @@
 against plain 64-bit forms, their edge cases, their refusals, and the calls
 together as a serving loop makes them."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -763,6 +764,57 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
+@gpu
+def test_two_threads_at_once(lib):  # noqa: F811
+    """The C entry points from two threads (ctypes lets go of the interpreter's
+    lock), each on a stream of its own, with sizes that need different amounts of
+    shared memory of the same kernels: no call is refused, and the results are
+    those of one thread."""
+    m = q()
+    sizes = [(2900, 200, 8), (9000, 500, 24)]  # keys, chunk of the select, its NQ
+    jobs = []
+    for k, (n, BCP, NQ) in enumerate(sizes):
+        c = Pages([n], [n], 2, 128, 64, 60 + k, scales=(-9, -5)).cuda()
+        Qs, Qa = randn(61 + k, 1, 4, BCP, 128).to(torch.bfloat16).cuda(), randn(63 + k, 1, 4, 8 + 12 * k, 128).cuda()
+        idx, cnt, _, _ = m.quoka_cache_select(Qs, c, n, NQ, 100)
+        O, _ = m.quoka_cache_attn(Qa, c, n)
+        jobs.append((c, n, NQ, Qs, Qa, idx, cnt, O))
+    torch.cuda.synchronize()
+    faults = []
+
+    def work(k):
+        try:
+            c, n, NQ, Qs, Qa, idx, cnt, O = jobs[k]
+            tv = m._lib.tensor_view
+            stream = torch.cuda.Stream()
+            idx1, cnt1, O1 = torch.zeros_like(idx), torch.zeros_like(cnt), torch.zeros_like(O)
+            wn = lib.quoka_select_workspace_size(1, 4, 2, 128, n, Qs.shape[2], NQ, 100, 1)
+            an = lib.quoka_cache_attn_workspace_size(1, 4, 2, 128, Qa.shape[2], n, 0)
+            ws, wa = (torch.zeros(x, dtype=torch.uint8, device="cuda") for x in (wn, an))
+            torch.cuda.synchronize()
+            p, B, vs, va = (lambda t: ctypes.c_void_p(t.data_ptr())), ctypes.byref, tv(Qs), tv(Qa)
+            for _ in range(300):
+                r = lib.quoka_cache_select(B(vs), B(c._view), n, NQ, 100, p(idx1), p(cnt1), None, None, p(ws), wn,
+                                           ctypes.c_void_p(stream.cuda_stream))
+                r2 = lib.quoka_cache_attn(B(va), B(c._view), n, None, None, n, None, None, 128**-0.5, p(O1), None, p(wa), an,
+                                          ctypes.c_void_p(stream.cuda_stream))
+                if r or r2:
+                    faults.append((k, r, r2))
+                    break
+            stream.synchronize()
+            if not (torch.equal(idx, idx1) and torch.equal(cnt, cnt1) and torch.equal(O, O1)):
+                faults.append((k, "results"))
+        except BaseException as e:  # (a thread's failure is the test's)
+            faults.append((k, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not faults
 
 
 @gpu
