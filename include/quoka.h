@@ -41,7 +41,8 @@
  *     quoka_select_ex and quoka_prefill_chunk in their first kernel,
  *     quoka_cache_select in the kernel that makes its group means,
  *     quoka_gather_kv, quoka_decode_attn and the other cache calls in a
- *     one-thread kernel of their own, the other calls with an 8-byte memset; a kernel latches only
+ *     one-thread kernel of their own (quoka_cache_attn with few query rows in
+ *     its first), the other calls with an 8-byte memset; a kernel latches only
  *     after the kernel before it in the call has completed. The word
  *     reports the faults of the latest call.
  *   - Calls on different streams with different workspaces may run
@@ -388,7 +389,8 @@ quoka_status quoka_combine_partials(const void* O_parts, const float* lse_parts,
  * Faults that only the device can see latch QUOKA_ERR_BOUNDS in ws and read
  * no memory: a table entry outside [0, npages) (the rows of that page count
  * as zeros), a seq_len outside [0, max_len] (taken as the nearer bound), a
- * key index outside [0, seq_len) (a row of zeros). */
+ * key index outside [0, seq_len) (a row of zeros). A call for no keys at all
+ * (max_len or N 0) need not look at seq_len. */
 typedef struct {
   void* k;
   void* v;
@@ -471,8 +473,9 @@ quoka_status quoka_cache_gather(const quoka_cache* cache, int max_len,
  * NULL: without them).
  *   Q (b, nq, BCP, d); Kc, Vc (b, nkv, BCP, d), dtype of Q (every row of Vc
  *   finite, those of padding too: a chunk of many bf16 rows multiplies rows
- *   that the mask leaves out by zero); O out (b, nq, BCP, d), contiguous; lse out (b, nq, BCP) float or NULL. A row
- *   that sees no key gives O = 0, lse = -inf.
+ *   that the mask leaves out by zero); O out (b, nq, BCP, d), contiguous; lse
+ *   out (b, nq, BCP) float or NULL. A row that sees no key gives O = 0,
+ *   lse = -inf. An index listed twice counts twice.
  *   ws at least quoka_cache_attn_workspace_size() bytes, 256-byte aligned. */
 size_t quoka_cache_attn_workspace_size(int b, int nq, int nkv, int d, int BCP,
                                        int N, quoka_dtype dtype);

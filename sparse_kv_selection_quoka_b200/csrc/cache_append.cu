@@ -119,8 +119,8 @@ __device__ __forceinline__ void rotate(const RotArgs& r, const float (&cs)[8], c
   }
 }
 
-// New tokens of sequence bi: positions [start, end). Lengths and counts out
-// of range, and tokens past the cache or the angle table, are latched and
+// New tokens of sequence bi: positions [start, end). Negative lengths, counts
+// out of range, and tokens past the cache or the angle table, are latched and
 // left out.
 __device__ __forceinline__ void new_range(const CacheAppendArgs& a, int bi, int* start, int* end) {
   const int len = __ldcg(a.c.seq_len + bi);
@@ -129,7 +129,7 @@ __device__ __forceinline__ void new_range(const CacheAppendArgs& a, int bi, int*
   bool bad = n != want;
   if (len < 0 || len > a.limit) {
     *start = *end = 0;
-    bad = true;
+    bad = bad || len < 0 || n > 0;  // (no tokens: the angles need not reach the length)
   } else {
     *start = len;
     *end = (int)min((int64_t)len + n, (int64_t)a.limit);

@@ -780,8 +780,8 @@ quoka_status quoka_cache_append(const quoka_cache* cache, const quoka_tensor* K,
   if (Kr != nullptr && !aligned16(Kr)) return QUOKA_ERR_INVALID_ARG;
   if (BCP > kMaxBCP || nq > kMaxHeads) return QUOKA_ERR_UNSUPPORTED;
   // the rotation reads both columns of a pair: it cannot run in place
-  const size_t es = elt_size(K->dtype), kb = (size_t)(cache->b * cache->nkv * BCP * cache->d) * es;
-  const size_t qb = (size_t)(cache->b * nq * BCP * cache->d) * es;
+  const size_t es = elt_size(K->dtype), kb = (size_t)cache->b * cache->nkv * BCP * cache->d * es;
+  const size_t qb = (size_t)cache->b * nq * BCP * cache->d * es;
   const quoka_tensor* ins[3] = {K, V, Q};
   for (const quoka_tensor* t : ins) {
     if (t == nullptr) continue;
@@ -987,6 +987,7 @@ quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, i
   t.status = status;
   t.no_chunk = no_chunk ? 1 : 0;
   t.tc_d64 = 1;
+  if (BCP == 1) t.Q.st = t.Q.sh;  // (the only row: any stride)
   t.pack = cache_attn_packs(nq, nkv, BCP) && t.Q.sh == BCP * t.Q.st ? 1 : 0;
   t.nsplit = cache_attn_nsplit(b, nq, nkv, BCP, N, no_chunk, t.pack != 0);
   if (t.nsplit > 1) {

@@ -319,6 +319,21 @@ def test_append_leaves_out_what_does_not_fit():
     assert same_codes(dev.k.cpu(), c.k) and same_codes(dev.v.cpu(), c.v)
 
 
+@gpu
+def test_append_of_no_tokens_needs_no_angles():
+    """A sequence without new tokens may be longer than the table of angles."""
+    c = Pages([30, 4], [64, 40], 1, 64, 16, 8)
+    K, V = randn(1, 2, 1, 5, 64), randn(2, 2, 1, 5, 64)
+    cos, sin = angles(10, 64)
+    dev = c.cuda(torch.uint8)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    new = torch.tensor([0, 5], dtype=torch.int32).cuda()
+    q().quoka_cache_append(dev, K.cuda(), V.cuda(), None, cos.cuda(), sin.cuda(), new_len=new, ws=ws)
+    assert q().quoka_get_device_status(ws) == 0
+    append(c, K, V, cos, sin, False, [0, 5])
+    assert same_codes(dev.k.cpu(), c.k) and torch.equal(dev.k_scale.cpu(), c.k_scale)
+
+
 # ------------------------------------------------------------ gather
 
 GATHERS = [
@@ -512,6 +527,29 @@ def test_attention(k):
                                   None if Vc is None else strided(Vc), want_lse=True, ws=ws)
     assert q().quoka_get_device_status(ws) == 0
     check_attention(O, lse, attention(c, Q, Kc, Vc, idx, counts), dt, d, (N or max_len) + BCP, nq // nkv * BCP <= 32)
+
+
+@gpu
+@pytest.mark.parametrize("dt,d,BCP,nq,N", [("bf16", 128, 1, 8, 0), ("bf16", 128, 40, 4, 0), ("bf16", 64, 40, 4, 50),
+                                           ("f32", 64, 9, 4, 0), ("bf16", 128, 1, 70, 0)])
+def test_attention_of_broadcast_rows(dt, d, BCP, nq, N):
+    """Queries and chunk rows that several sequences and heads share by a stride
+    of 0, and a single query row between others (its row stride says nothing)."""
+    c = Pages([130, 77], [130, 77], 2 if nq < 70 else 1, d, 32, 12, scales=(-9, -5))
+    t, nkv = TYPES[dt], c.nkv
+    idx = counts = None
+    if N:
+        idx, counts = index_lists([130, 77], nkv, N, 3)
+    Q, K, V = (randn(s, 1, 1, BCP, d).to(t).cuda() for s in (1, 2, 3))
+    if BCP == 1:  # (b, 1, nq, d) seen as (b, nq, 1, d)
+        Q = randn(1, 2, 1, nq, d).to(t).cuda().transpose(1, 2)
+    else:
+        Q = Q.expand(2, nq, BCP, d)
+    K, V = K.expand(2, nkv, BCP, d), V.expand(2, nkv, BCP, d)
+    up = lambda x: None if x is None else x.cuda()
+    O, lse = q().quoka_cache_attn(Q, c.cuda(), 130, up(idx), up(counts), K, V, want_lse=True)
+    want = attention(c, Q.cpu(), K.cpu(), V.cpu(), idx, counts)
+    check_attention(O, lse, want, dt, d, (N or 130) + BCP, nq // nkv * BCP <= 32)
 
 
 @gpu
