@@ -30,6 +30,12 @@
 // instead: a search of the key's bits from the top, two at a time, by counting
 // the keys at or above three thresholds (one block barrier a step), then one
 // scan that places the picks. 18 rows of 64 keys 7.2 -> 5.3 us, 4 of 905 7.6 -> 6.2.
+// With the scoring kernel's histogram and slices of at most 8192 keys the keys
+// stay in registers too (topk_hist_kernel below): one pass over them and one
+// cluster barrier. The whole cache selection: 16 sequences x 8 heads of up to 8191
+// keys 34.9 -> 28.7 us, 8 rows of 32768 keys 27.1 -> 24.7 (most of the time of the
+// kernel above went to its many short phases, each a barrier and a stretch of
+// code run once).
 // When a bucket holds more candidates than the gathered list can take, the
 // exact passes run over every slice instead, their histograms summed over
 // the cluster through distributed shared memory.
@@ -692,6 +698,300 @@ topk_small_kernel(const float* __restrict__ S, int64_t T, int bsa, const int32_t
   if (tid == 0) kv_count[row] = take;
 }
 
+constexpr int TOPK_HIST_THREADS = 512;
+constexpr int TOPK_HIST_SLICE = 8192;  // keys of a CTA at most: 16 a thread
+constexpr int TOPK_DIRECT = 512;       // candidates that are ranked directly
+
+struct TopkHistShared {
+  uint32_t wsum[TOPK_HIST_THREADS / 32], wcount[TOPK_HIST_THREADS / 32];
+  uint2 wstep[2][TOPK_HIST_THREADS / 32];
+  uint32_t bin, above;
+  uint32_t count[TOPK_MAX_CLUSTER];    // per rank: keys above the bucket << 16 | keys in it
+  uint2 step[2][TOPK_MAX_CLUSTER];     // per rank: counts of a step of the search
+  uint32_t part[4 * TOPK_DIRECT];      // per rank: its candidates, in index order
+  __align__(16) uint32_t list[TOPK_DIRECT + 4];
+  uint32_t taken[TOPK_DIRECT / 32];    // bit i: candidate i is picked
+};
+
+// The select for rows whose first digit is known (`ghist`) and whose slices fit
+// the registers: warp w holds the 32 KPT keys from 32 KPT w, lane l every 32nd of
+// them, so that loads are coalesced at any alignment and a ballot orders 32
+// keys. One pass over the keys splits them at the bucket; every CTA pushes its
+// counts and candidates into the shared memory of all CTAs of the row, so that
+// after one cluster barrier the rest is local: candidate i is picked when fewer
+// than `need` candidates are greater, or equal and before it, and a key's
+// output position is the keys above the bucket and the picked candidates
+// before it.
+template <int KPT, bool CLUSTER>
+__global__ void __launch_bounds__(TOPK_HIST_THREADS)
+topk_hist_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const uint32_t* __restrict__ ghist,
+                 const int32_t* __restrict__ row_len, int32_t* __restrict__ kv_idx, int32_t* __restrict__ kv_count,
+                 const int* __restrict__ status) {
+  constexpr int WARPS = TOPK_HIST_THREADS / 32;
+  constexpr int PART = CLUSTER ? 4 * TOPK_DIRECT / TOPK_MAX_CLUSTER : TOPK_DIRECT;  // of a rank
+  __shared__ TopkHistShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = CLUSTER ? (int)cluster.num_blocks() : 1, c = CLUSTER ? (int)cluster.block_rank() : 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t lower = (1u << lane) - 1u;
+  const int j = blockIdx.y, bi = blockIdx.z, nkv = gridDim.y;
+  const int64_t row = (int64_t)bi * nkv + j;
+  // (row_len: an input of the call; every CTA of the row leaves here together)
+  const int Tr = row_len != nullptr ? (int)max((int64_t)0, min((int64_t)__ldg(row_len + bi), T)) : (int)T;
+  const int take = min(bsa, Tr), lo = c * slice, n = max(0, min(slice, Tr - lo));
+  pdl_trigger();
+  if (take == 0) {
+    pdl_wait();
+    if (c == 0 && tid == 0) kv_count[row] = 0;
+    return;
+  }
+  if (CLUSTER) cluster_arrive();  // (a CTA is written to only once it runs)
+  if (tid == 0) sh.bin = sh.above = 0u;  // (what stays if a histogram does not fit the scores)
+  pdl_wait();  // the scores and their histogram come from the previous kernel
+  const int fault = status != nullptr ? __ldcg(status) : 0;
+  // thread t owns the 8 bins from the 8 t-th highest down
+  const uint4* Hg = reinterpret_cast<const uint4*>(ghist + row * TOPK_BINS) + (TOPK_BINS / 4 - 2 - 2 * tid);
+  const uint4 h0 = __ldcg(Hg + 1), h1 = __ldcg(Hg);
+  float x[KPT];
+  const int e0 = warp * 32 * KPT + lane;  // this lane's first key of the slice
+  const float* Sr = S + row * T + lo + e0;
+#pragma unroll
+  for (int u = 0; u < KPT; ++u) x[u] = e0 + 32 * u < n ? __ldcg(Sr + 32 * u) : 0.f;
+  if (fault != 0) {  // (the same word in every CTA: they leave together)
+    if (CLUSTER) cluster_wait();
+    if (c == 0 && tid == 0) kv_count[row] = 0;
+    return;
+  }
+  // 1. the bucket that holds the take-th largest score
+  {
+    const uint32_t mine[8] = {h0.w, h0.z, h0.y, h0.x, h1.w, h1.z, h1.y, h1.x};
+    uint32_t tot = 0u;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) tot += mine[u];
+    uint32_t incl = tot;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh.wsum[warp] = incl;
+    __syncthreads();
+    incl += __reduce_add_sync(0xffffffffu, lane < warp ? sh.wsum[lane] : 0u);
+    uint32_t acc = incl - tot;
+    if (incl >= (uint32_t)take && acc < (uint32_t)take) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (acc < (uint32_t)take && acc + mine[u] >= (uint32_t)take) {
+          sh.bin = (uint32_t)(TOPK_BINS - 1 - 8 * tid - u);
+          sh.above = acc;
+        }
+        acc += mine[u];
+      }
+    }
+    __syncthreads();
+  }
+  const uint32_t b0 = sh.bin, need = (uint32_t)take - sh.above;
+  // 2. the keys above the bucket, and the candidates in it
+  const float f0 = (float)b0;
+  uint32_t gtm[KPT], cm[KPT], mine = 0u;
+#pragma unroll
+  for (int u = 0; u < KPT; ++u) {
+    const bool in = e0 + 32 * u < n;
+    // score_bin(x) before its conversion: floor(y) > b0 is y >= b0 + 1
+    float y = fminf(fmaxf((x[u] + 1.f) * 2048.f, 0.f), 4095.f);
+    if (x[u] != x[u]) y = __float_as_uint(x[u]) >> 31 ? 0.f : 4095.f;
+    gtm[u] = __ballot_sync(0xffffffffu, in && y >= f0 + 1.f);
+    cm[u] = __ballot_sync(0xffffffffu, in && y >= f0) & ~gtm[u];
+    mine += (uint32_t)__popc(gtm[u]) << 16 | (uint32_t)__popc(cm[u]);
+  }
+  // (both counts in one word: a slice has at most 8192 keys)
+  if (lane == 0) sh.wcount[warp] = mine;
+  if (CLUSTER) cluster_wait();
+  __syncthreads();
+  auto before_warp = [&](uint32_t* all) {
+    const uint32_t v = lane < WARPS ? sh.wcount[lane] : 0u;
+    *all = __reduce_add_sync(0xffffffffu, v);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? v : 0u);
+  };
+  // the counts of this CTA to every rank; returns those of the warps before
+  auto push_counts = [&]() {
+    uint32_t all;
+    const uint32_t before = before_warp(&all);
+    if (tid < C) *(CLUSTER ? cluster.map_shared_rank(&sh.count[c], tid) : &sh.count[0]) = all;
+    return before;
+  };
+  auto meet = [&]() {
+    if (CLUSTER) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  };
+  uint32_t before = push_counts();
+  {
+    uint32_t p = before & 0xFFFFu;
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) {
+      if (cm[u] == 0u) continue;
+      const uint32_t at = p + (uint32_t)__popc(cm[u] & lower);
+      if (cm[u] >> lane & 1u && at < (uint32_t)PART) {
+        uint32_t* dst = &sh.part[c * PART + at];
+        for (int r = 0; r < C; ++r) *(CLUSTER ? cluster.map_shared_rank(dst, r) : dst) = score_key(x[u]);
+      }
+      p += (uint32_t)__popc(cm[u]);
+    }
+  }
+  meet();
+  // every rank's counts: lane r holds rank r's
+  auto ranks = [&](uint32_t* gt, uint32_t* eq, uint32_t* gt_all, uint32_t* eq_incl) {
+    const uint32_t v = lane < C ? sh.count[lane] : 0u;
+    *eq = v & 0xFFFFu;
+    *gt = __reduce_add_sync(0xffffffffu, lane < c ? v >> 16 : 0u);
+    *gt_all = __reduce_add_sync(0xffffffffu, v >> 16);
+    uint32_t incl = *eq;
+#pragma unroll
+    for (int o = 1; o < TOPK_MAX_CLUSTER; o <<= 1) {
+      const uint32_t w = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += w;
+    }
+    *eq_incl = incl;
+  };
+  uint32_t gt_base, nr, gt_all, incl;
+  ranks(&gt_base, &nr, &gt_all, &incl);
+  const uint32_t nl = __shfl_sync(0xffffffffu, incl, TOPK_MAX_CLUSTER - 1);  // candidates of the row
+  int32_t* dst = kv_idx + row * bsa;
+  if (nl <= (uint32_t)TOPK_DIRECT && __all_sync(0xffffffffu, nr <= (uint32_t)PART)) {
+    // 3. candidate i (in index order over the ranks) against all others
+    const uint32_t starts = incl - nr;
+    {
+      int r = 0;
+      uint32_t at = (uint32_t)tid;
+#pragma unroll
+      for (int i = 1; i < TOPK_MAX_CLUSTER; ++i) {
+        const uint32_t first = __shfl_sync(0xffffffffu, starts, i);
+        if (CLUSTER && i < C && (uint32_t)tid >= first) {
+          r = i;
+          at = (uint32_t)tid - first;
+        }
+      }
+      if ((uint32_t)tid < nl) sh.list[tid] = sh.part[r * PART + (int)at];
+      else if ((uint32_t)tid < nl + 4u) sh.list[tid] = 0u;
+      if (nl + 4u > (uint32_t)TOPK_DIRECT && tid < 4) sh.list[TOPK_DIRECT + tid] = 0u;
+    }
+    __syncthreads();
+    bool picked = false;
+    if ((uint32_t)tid < nl) {
+      const uint32_t k = sh.list[tid];
+      uint32_t ahead = 0u;
+#pragma unroll 1
+      for (uint32_t i = 0; i < nl; i += 4u) {
+        const uint4 o = *reinterpret_cast<const uint4*>(sh.list + i);
+        const int d = tid - (int)i;  // (keys before this one count when equal)
+        ahead += (o.x > k || (o.x == k && d > 0)) + (o.y > k || (o.y == k && d > 1)) +
+                 (o.z > k || (o.z == k && d > 2)) + (o.w > k || (o.w == k && d > 3));
+      }
+      picked = ahead < need;
+    }
+    const uint32_t word = __ballot_sync(0xffffffffu, picked);
+    if (lane == 0) sh.taken[warp] = word;
+    __syncthreads();
+    // 4. the picks, at their places
+    const uint32_t w = lane < TOPK_DIRECT / 32 ? sh.taken[lane] : 0u;
+    uint32_t wpre = (uint32_t)__popc(w);  // picked candidates of the words before
+#pragma unroll
+    for (int o = 1; o <= TOPK_DIRECT / 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, wpre, o);
+      if (lane >= o) wpre += v;
+    }
+    wpre -= (uint32_t)__popc(w);
+    auto candidate = [&](uint32_t p, uint32_t* before_p) {  // is p picked, and how many before it
+      const uint32_t wd = __shfl_sync(0xffffffffu, w, p >> 5), pre = __shfl_sync(0xffffffffu, wpre, p >> 5);
+      *before_p = pre + (uint32_t)__popc(wd & ((1u << (p & 31u)) - 1u));
+      return (wd >> (p & 31u) & 1u) != 0u;
+    };
+    uint32_t cpos = __shfl_sync(0xffffffffu, starts, c) + (before & 0xFFFFu), cpicked;
+    candidate(cpos, &cpicked);
+    uint32_t pos0 = gt_base + (before >> 16) + cpicked;  // the first place of a group of 32 keys
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) {
+      uint32_t m = gtm[u];
+      if (cm[u] != 0u) {
+        uint32_t unused;
+        const bool p = candidate(cpos + (uint32_t)__popc(cm[u] & lower), &unused);
+        m |= __ballot_sync(0xffffffffu, p) & cm[u];
+        cpos += (uint32_t)__popc(cm[u]);
+      }
+      const uint32_t pos = pos0 + (uint32_t)__popc(m & lower);
+      if ((m >> lane & 1u) && pos < (uint32_t)take) dst[pos] = lo + e0 + 32 * u;
+      pos0 += (uint32_t)__popc(m);
+    }
+  } else {
+    // Many candidates: the take-th largest key by its bits from the top, two at
+    // a time, counting the keys at or above three thresholds; then the keys
+    // above it and, in index order, the first of those equal to it.
+    uint32_t k[KPT];
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) k[u] = e0 + 32 * u < n ? score_key(x[u]) : 0u;  // (0: below every threshold)
+    uint32_t ustar = 0u;
+#pragma unroll 1
+    for (int shift = 30, p = 0; shift >= 0; shift -= 2, p ^= 1) {
+      const uint32_t t1 = ustar | 1u << shift, t2 = ustar | 2u << shift, t3 = ustar | 3u << shift;
+      uint32_t c12 = 0u, c3 = 0u;
+#pragma unroll
+      for (int u = 0; u < KPT; ++u) {
+        c12 += (k[u] >= t1 ? 1u : 0u) + (k[u] >= t2 ? 0x10000u : 0u);
+        c3 += k[u] >= t3 ? 1u : 0u;
+      }
+      c12 = __reduce_add_sync(0xffffffffu, c12);
+      c3 = __reduce_add_sync(0xffffffffu, c3);
+      if (lane == 0) sh.wstep[p][warp] = make_uint2(c12, c3);
+      __syncthreads();
+      const uint2 v = lane < WARPS ? sh.wstep[p][lane] : make_uint2(0u, 0u);
+      c12 = __reduce_add_sync(0xffffffffu, v.x);
+      c3 = __reduce_add_sync(0xffffffffu, v.y);
+      uint32_t c1 = c12 & 0xFFFFu, c2 = c12 >> 16;
+      if (CLUSTER) {
+        // (written again two steps on, behind a barrier that follows the reads)
+        if (tid < C) *cluster.map_shared_rank(&sh.step[p][c], tid) = make_uint2(c12, c3);
+        meet();
+        const uint2 y = lane < C ? sh.step[p][lane] : make_uint2(0u, 0u);
+        c1 = __reduce_add_sync(0xffffffffu, y.x & 0xFFFFu);
+        c2 = __reduce_add_sync(0xffffffffu, y.x >> 16);
+        c3 = __reduce_add_sync(0xffffffffu, y.y);
+      }
+      if (c3 >= (uint32_t)take) ustar = t3;
+      else if (c2 >= (uint32_t)take) ustar = t2;
+      else if (c1 >= (uint32_t)take) ustar = t1;
+    }
+    mine = 0u;
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) {
+      const bool in = e0 + 32 * u < n;
+      gtm[u] = __ballot_sync(0xffffffffu, in && k[u] > ustar);
+      cm[u] = __ballot_sync(0xffffffffu, in && k[u] == ustar);
+      mine += (uint32_t)__popc(gtm[u]) << 16 | (uint32_t)__popc(cm[u]);
+    }
+    if (lane == 0) sh.wcount[warp] = mine;
+    __syncthreads();
+    before = push_counts();
+    meet();
+    ranks(&gt_base, &nr, &gt_all, &incl);
+    const uint32_t need_eq = (uint32_t)take - gt_all;
+    uint32_t gpos = gt_base + (before >> 16), cpos = __shfl_sync(0xffffffffu, incl - nr, c) + (before & 0xFFFFu);
+#pragma unroll
+    for (int u = 0; u < KPT; ++u) {
+      const uint32_t p = cpos + (uint32_t)__popc(cm[u] & lower);
+      const bool pick = (gtm[u] >> lane & 1u) || ((cm[u] >> lane & 1u) && p < need_eq);
+      const uint32_t pos = gpos + (uint32_t)__popc(gtm[u] & lower) + min(p, need_eq);
+      if (pick && pos < (uint32_t)take) dst[pos] = lo + e0 + 32 * u;
+      gpos += (uint32_t)__popc(gtm[u]);
+      cpos += (uint32_t)__popc(cm[u]);
+    }
+  }
+  if (c == 0 && tid == 0) kv_count[row] = take;
+}
+
 }  // namespace
 
 int64_t topk_max_T() { return (int64_t)TOPK_MAX_CLUSTER * TOPK_MAX_SLICE; }
@@ -724,6 +1024,26 @@ cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, 
   if (C > fit) C = fit;
   if (C > TOPK_MAX_CLUSTER) C = TOPK_MAX_CLUSTER;
   if (C < 1) C = 1;
+  const int part = (int)((T + C - 1) / C + 31) & ~31;
+  if (hist != nullptr && part <= TOPK_HIST_SLICE) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C, nkv, b);
+    cfg.blockDim = dim3(TOPK_HIST_THREADS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = C > 1 ? 2 : 1;
+    auto* kern = part <= TOPK_HIST_SLICE / 2 ? (C > 1 ? topk_hist_kernel<8, true> : topk_hist_kernel<8, false>)
+                                             : (C > 1 ? topk_hist_kernel<16, true> : topk_hist_kernel<16, false>);
+    return cudaLaunchKernelEx(&cfg, kern, S_agg, T, bsa, part, hist, row_len, kv_idx, kv_count,
+                              static_cast<const int*>(status));
+  }
   const int slice = (int)((T + C - 1) / C);
   if (slice > TOPK_MAX_SLICE) return cudaErrorInvalidValue;
   const size_t smem = ((size_t)slice + 2 * TOPK_LIST_MAX) * sizeof(uint32_t);

@@ -866,6 +866,47 @@ def test_topk_of_many_rows(rows, T, BSA):
     assert (cnt == BSA).all() and torch.equal(idx.long(), want)
 
 
+TIES = [
+    # lens, kinds of keys (0: all different), how many keys in a row are of one kind, BSA
+    ([3000, 2100, 0, 1], 0, 1, 700),
+    ([8191, 5000, 900], 0, 1, 2048),
+    ([8192, 4097], 150, 1, 3000),       # some fifty equal keys at the threshold
+    ([8000], 7, 1, 1234),               # over a thousand
+    ([32768], 0, 1, 4096),              # a cluster of CTAs
+    ([30001], 120, 1, 4001),
+    ([30000], 60, 500, 7777),           # equal keys lie together: in the slices of one or two CTAs
+    ([32000, 17], 5, 1, 9999),
+    ([20000], 1, 1, 19999),             # all equal
+    ([50000], 0, 1, 1),
+    ([70000], 300, 7, 12345),           # more than the registers hold
+    ([9000] * 80, 400, 3, 500),
+]
+
+
+@gpu
+@pytest.mark.parametrize("k", range(len(TIES)))
+def test_select_takes_the_first_of_equal_scores(k):
+    """Picks against a stable sort of the call's own scores."""
+    lens, kinds, run, BSA = TIES[k]
+    b, d, page, most = len(lens), 64, 128, max(lens)
+    npp = (most + page - 1) // page
+    g = torch.Generator().manual_seed(k)
+    rows = torch.randint(0, 119, (kinds or b * npp * page, d), generator=g, dtype=torch.uint8)
+    rows |= torch.randint(0, 2, rows.shape, generator=g, dtype=torch.uint8) << 7
+    if kinds:
+        rows = rows[torch.randint(0, kinds, ((b * npp * page + run - 1) // run,), generator=g).repeat_interleave(run)[:b * npp * page]]
+    codes = rows.reshape(b * npp, 1, page, d).cuda()
+    scale, table = torch.ones(b * npp, 1, device="cuda"), torch.arange(b * npp, dtype=torch.int32).reshape(b, npp).cuda()
+    c = q().QuokaCache(codes, codes.clone(), scale, scale.clone(), table, torch.tensor(lens, dtype=torch.int32).cuda())
+    Q = randn(k, b, 2, 5, d).cuda()
+    idx, count, _, s = q().quoka_cache_select(Q, c, most, 2, BSA, want_s_agg=True)
+    for i, n in enumerate(lens):
+        m = min(n, BSA)
+        assert int(count[i, 0]) == m
+        want = s[i, 0, :n].sort(descending=True, stable=True).indices[:m].sort().values
+        assert torch.equal(idx[i, 0, :m].long(), want)
+
+
 @gpu
 def test_long_table_offsets_pass_32_bits():
     """A pool of more than 2^32 bytes, with the pages of a sequence at both ends."""
