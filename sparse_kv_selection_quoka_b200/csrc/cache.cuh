@@ -110,26 +110,34 @@ __host__ __forceinline__ int64_t range_grid(int64_t rows, int N, int ctas, int l
 
 // Range `cta`, or, for -1 - row, the first range of that row (called by one warp;
 // written to *out). keys(row): a row's keys, at most 2^30. Rows are cut into equal
-// runs of at most max(least, total / target) keys, rounded up to `step`.
+// runs of at most max(least, total / target) keys, rounded up to `step`. held:
+// shared memory for a length per row.
 template <typename Keys>
 __device__ __forceinline__ void find_range(int rows, int target, int least, int step, int cta, int lane, Keys&& keys,
-                                           Range* out) {
+                                           int* held, Range* out) {
   if (rows > kRangeRows) {
     const int row = cta < 0 ? -1 - cta : cta;
     if (lane == 0) *out = Range{row, 0, keys(row), row, 1};
     return;
   }
   int64_t total = 0;
-  for (int i = lane; i < rows; i += 32) total += keys(i);
+#pragma unroll 4
+  for (int i = lane; i < rows; i += 32) {
+    const int n = keys(i);
+    total += n;
+    held[i] = n;  // (read again by this lane only)
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int most = (int)min(max((int64_t)least, (total + target - 1) / target), (int64_t)1 << 30);
+  const int64_t even = total < 0x7FFFFFFF - target ? (int64_t)((unsigned)(total + target - 1) / (unsigned)target)
+                                                   : (total + target - 1) / target;
+  const int most = (int)min(max((int64_t)least, even), (int64_t)1 << 30);
   if (lane == 0) out->row = -1;
   __syncwarp();
   int before = 0;  // ranges of the rows before
 #pragma unroll 1
   for (int i0 = 0; i0 < rows; i0 += 32) {
-    const int i = i0 + lane, n = i < rows ? keys(i) : 0;
+    const int i = i0 + lane, n = i < rows ? held[i] : 0;
     const int parts = i < rows ? max(1, (n + most - 1) / most) : 0;
     const int all = __reduce_add_sync(0xffffffffu, parts);
     if (cta < 0 ? -1 - cta < i0 + 32 : cta < before + all) {  // among these 32 rows

@@ -286,7 +286,8 @@ cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
   }
   if (warp == 4)
     find_range(a.b * a.c.nkv, a.target, kSplitKeys, 64, range, lane, [&](int row) { return row_keys<IDX>(a, row); },
-               &sh.range);
+               reinterpret_cast<int*>(ring), &sh.range);
+  if (warp == 4) sm100::fence_proxy_async_smem();  // (the ring's copies come behind the lengths)
   __syncthreads();
   const int row = sh.range.row, k0 = sh.range.k0, k1 = sh.range.k1;
   if (row < 0) return;
@@ -614,6 +615,7 @@ __global__ void __launch_bounds__(MT) cache_merge_kernel(const CacheAttnArgs a) 
   __shared__ float sw[kMaxParts];
   __shared__ float red[2][kWarps];
   __shared__ Range found;
+  __shared__ int lens[32];
   extern __shared__ float sc[];  // the chunk's keys: scores, then weights
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c4 = tid % C4, grp = tid / C4;
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(MT) cache_merge_kernel(const CacheAttnArgs a) 
   if (nrows <= 32) {
     if (tid < 32)
       find_range(nrows, a.target, kSplitKeys, 64, -1 - row_of, lane,
-                 [&](int i) { return a.kv_idx != nullptr ? row_keys<true>(a, i) : row_keys<false>(a, i); }, &found);
+                 [&](int i) { return a.kv_idx != nullptr ? row_keys<true>(a, i) : row_keys<false>(a, i); }, lens, &found);
     __syncthreads();
     parts = make_int2(found.first, found.parts);
     pdl_wait();

@@ -50,7 +50,7 @@ struct Shared {
   uint64_t full[kStages], empty[kStages];
   int abort;
   Range range;
-  uint32_t hist[TOPK_HIST_BINS];
+  alignas(16) uint32_t hist[TOPK_HIST_BINS];
 };
 
 // Dynamic shared memory: the ring, then the group means' fragments [k-step][lane]
@@ -122,10 +122,12 @@ cache_score_kernel(const __grid_constant__ CUtensorMap map, const CacheScoreArgs
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = tid; i < TOPK_HIST_BINS; i += kThreads) sh.hist[i] = 0u;
+  for (int i = tid; i < TOPK_HIST_BINS / 4; i += kThreads) reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (warp == 4)
     find_range(a.b * a.c.nkv, a.target, kSplitKeys, kStage, blockIdx.x, lane,
-               [&](int i) { return min(max(__ldcg(a.c.seq_len + i / a.c.nkv), 0), a.max_len); }, &sh.range);
+               [&](int i) { return min(max(__ldcg(a.c.seq_len + i / a.c.nkv), 0), a.max_len); },
+               reinterpret_cast<int*>(ring), &sh.range);
+  if (warp == 4) sm100::fence_proxy_async_smem();  // (the ring's copies come behind the lengths)
   __syncthreads();
   const int k0 = sh.range.k0, k1 = sh.range.k1;
   if (sh.range.row < 0) {
@@ -260,9 +262,13 @@ cache_score_kernel(const __grid_constant__ CUtensorMap map, const CacheScoreArgs
   __syncthreads();
   pdl_wait();  // (the loader's threads: the histogram's zeros)
   uint32_t* hist = a.hist + row * TOPK_HIST_BINS;
-  for (int i = tid; i < TOPK_HIST_BINS; i += kThreads) {
-    const uint32_t n = sh.hist[i];
-    if (n != 0u) atomicAdd(hist + i, n);
+  for (int i = tid; i < TOPK_HIST_BINS / 4; i += kThreads) {
+    const uint4 n = reinterpret_cast<const uint4*>(sh.hist)[i];
+    if ((n.x | n.y | n.z | n.w) == 0u) continue;
+    if (n.x != 0u) atomicAdd(hist + 4 * i, n.x);
+    if (n.y != 0u) atomicAdd(hist + 4 * i + 1, n.y);
+    if (n.z != 0u) atomicAdd(hist + 4 * i + 2, n.z);
+    if (n.w != 0u) atomicAdd(hist + 4 * i + 3, n.w);
   }
 }
 

@@ -65,7 +65,7 @@ struct Shared {
   uint32_t tmem;
   int abort;
   Range range;
-  uint32_t hist[TOPK_HIST_BINS];
+  alignas(16) uint32_t hist[TOPK_HIST_BINS];
 };
 
 // Group means of a pass: per group of 32 columns, and how many groups.
@@ -126,12 +126,13 @@ __device__ __forceinline__ void load_rows(const CacheScoreArgs& a, const CUtenso
 template <int D, int P>
 __device__ __forceinline__ void stage_pieces(const float* qg, uint8_t* qs, int n, int groups, int tid) {
   constexpr int CPR = D / 16, kPer = Pass<P>::kPer;
-  for (int e = tid; e < groups * kPer * CPR; e += 128) {
-    const int slot = e / CPR, c = e % CPR;
-    const float* src = qg + (int64_t)(slot < n ? slot : 0) * D + 16 * c;
-    float x[16];
+#pragma unroll 1
+  for (int e = tid; e < groups * kPer * (D / 8); e += 128) {  // 8 columns of a slot
+    const int slot = e / (D / 8), c = e % (D / 8);
+    const float* src = qg + (int64_t)(slot < n ? slot : 0) * D + 8 * c;
+    float x[8];
 #pragma unroll
-    for (int u = 0; u < 16; u += 4) {
+    for (int u = 0; u < 8; u += 4) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(src + u));
       x[u] = v.x * 256.f;
       x[u + 1] = v.y * 256.f;
@@ -141,16 +142,16 @@ __device__ __forceinline__ void stage_pieces(const float* qg, uint8_t* qs, int n
     const int row = 32 * (slot / kPer) + P * (slot % kPer);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      uint32_t w[4];
+      uint32_t w[2];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < 2; ++u) {
         w[u] = f32x2_to_e4m3x2(x[4 * u], x[4 * u + 1]) | (uint32_t)f32x2_to_e4m3x2(x[4 * u + 2], x[4 * u + 3]) << 16;
         float t[4];
         e4m3x4_to_f32(w[u], t);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[4 * u + i] = (x[4 * u + i] - t[i]) * 16.f;  // (exact)
       }
-      *reinterpret_cast<uint4*>(qs + at_chunk<D>(row + p, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint2*>(qs + at_chunk<D>(row + p, c >> 1) + 8 * (c & 1)) = make_uint2(w[0], w[1]);
     }
   }
   if constexpr (32 % P != 0) {
@@ -189,10 +190,12 @@ __global__ void __launch_bounds__(kThreads, 2) cache_score_tc_kernel(const __gri
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = tid; i < TOPK_HIST_BINS; i += kThreads) sh.hist[i] = 0u;
+  for (int i = tid; i < TOPK_HIST_BINS / 4; i += kThreads) reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (warp == kLoadWarp)
     find_range(a.b * a.c.nkv, a.target, kSplitKeys, kStage, blockIdx.x, lane,
-               [&](int i) { return min(max(__ldcg(a.c.seq_len + i / a.c.nkv), 0), a.max_len); }, &sh.range);
+               [&](int i) { return min(max(__ldcg(a.c.seq_len + i / a.c.nkv), 0), a.max_len); },
+               reinterpret_cast<int*>(ring), &sh.range);
+  if (warp == kLoadWarp) sm100::fence_proxy_async_smem();  // (the ring's copies come behind the lengths)
   __syncthreads();
   const int k0 = sh.range.k0, k1 = sh.range.k1;
   if (sh.range.row < 0) {
@@ -310,9 +313,13 @@ __global__ void __launch_bounds__(kThreads, 2) cache_score_tc_kernel(const __gri
   }
   pdl_wait();  // (the loader's and the issuer's threads: the histogram's zeros)
   uint32_t* hist = a.hist + row * TOPK_HIST_BINS;
-  for (int i = tid; i < TOPK_HIST_BINS; i += kThreads) {
-    const uint32_t n = sh.hist[i];
-    if (n != 0u) atomicAdd(hist + i, n);
+  for (int i = tid; i < TOPK_HIST_BINS / 4; i += kThreads) {
+    const uint4 n = reinterpret_cast<const uint4*>(sh.hist)[i];
+    if ((n.x | n.y | n.z | n.w) == 0u) continue;
+    if (n.x != 0u) atomicAdd(hist + 4 * i, n.x);
+    if (n.y != 0u) atomicAdd(hist + 4 * i + 1, n.y);
+    if (n.z != 0u) atomicAdd(hist + 4 * i + 2, n.z);
+    if (n.w != 0u) atomicAdd(hist + 4 * i + 3, n.w);
   }
 }
 
