@@ -10,8 +10,9 @@
 // or a quoka_status when the library refused.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -125,10 +126,14 @@ struct Call {
   void on_gpu() const {
     if (dev < 0) throw WrongValue("the cache must be on a CUDA device");
   }
+  // An output (made without the dispatcher, which takes longer than the rest).
   Tensor make(at::ScalarType type, c10::IntArrayRef shape, bool zero = false) const {
-    const auto o = at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)dev);
-    return zero ? at::zeros(shape, o) : at::empty(shape, o);
+    const c10::Device d(at::kCUDA, (c10::DeviceIndex)dev);
+    if (zero) return at::zeros(shape, at::TensorOptions().dtype(type).device(d));
+    return Tensor(at::detail::empty_cuda(shape, type, d, std::nullopt));
   }
+  // A workspace of the current stream for this call (the device guard is set).
+  static c10::DataPtr scratch(size_t bytes) { return c10::cuda::CUDACachingAllocator::get()->allocate(bytes); }
   void* stream() const { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 };
 
@@ -229,14 +234,15 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     call.on_gpu();
     if (max_len < 0 || NQ < 1) return PyLong_FromLong(QUOKA_ERR_INVALID_ARG);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)call.dev);
-    Tensor made_i, made_n, made_q, made_s, made_w;
+    Tensor made_i, made_n, made_q, made_s;
+    c10::DataPtr made_w;
     if (idx == nullptr) ip = (made_i = call.make(at::kInt, {c.b, c.nkv, m})).data_ptr();
     if (cnt == nullptr) np = (made_n = call.make(at::kInt, {c.b, c.nkv})).data_ptr();
     if (qi == nullptr && a[10] == Py_True) qp = (made_q = call.make(at::kInt, {c.b, nq, NQ})).data_ptr();
     if (sa == nullptr && a[11] == Py_True) sp = (made_s = call.make(at::kFloat, {c.b, c.nkv, max_len})).data_ptr();
     if (wp == nullptr) {
       wn = std::max<size_t>(256, g_select_ws(c.b, (int)nq, c.nkv, c.d, max_len, (int)BCP, NQ, std::max(0, BSA), qv.dtype));
-      wp = (made_w = call.make(at::kByte, {(int64_t)wn})).data_ptr();
+      wp = (made_w = Call::scratch(wn)).get();
     }
     const quoka_status st = g_select(&qv, &c, max_len, NQ, BSA, m ? (int32_t*)ip : nullptr, (int32_t*)np, (int32_t*)qp,
                                      max_len ? (float*)sp : nullptr, wp, wn, call.stream());
@@ -314,12 +320,13 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* wp = call.workspace(tensor(a[12], "ws"), &wn);
     call.on_gpu();
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)call.dev);
-    Tensor made_o, made_l, made_w;
+    Tensor made_o, made_l;
+    c10::DataPtr made_w;
     if (O == nullptr) op = (made_o = call.make(Q.scalar_type(), Q.sizes())).data_ptr();
     if (lse == nullptr && a[11] == Py_True) lp = (made_l = call.make(at::kFloat, {c.b, nq, BCP})).data_ptr();
     if (wp == nullptr) {
       wn = std::max<size_t>(256, g_attn_ws(c.b, (int)nq, c.nkv, c.d, (int)BCP, list.n, qv.dtype));
-      wp = (made_w = call.make(at::kByte, {(int64_t)wn})).data_ptr();
+      wp = (made_w = Call::scratch(wn)).get();
     }
     const quoka_status st = g_attn(&qv, &c, max_len, list.idx, list.cnt, list.n, Kc ? &kcv : nullptr, Kc ? &vcv : nullptr,
                                    (float)scale, op, (float*)lp, wp, wn, call.stream());
