@@ -153,13 +153,14 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
     return __ldcg(table + (tau >> plog));
   };
   auto held = [&](int p) { return p >= 0 && p < a.c.npages; };
+  int s = IDX ? 1 : 0;  // (listed rows: the computing warps load stage 0)
   int tau[3][NU], pg[2][NU];
   float ks[NU], vs[NU];
 #pragma unroll
   for (int u = 0; u < NU; ++u) {
     ks[u] = vs[u] = 1.f;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) tau[i][u] = tau_of(i, u);
+    for (int i = 0; i < 3; ++i) tau[i][u] = tau_of(s + i, u);
     pg[0][u] = page_of(tau[0][u]);
     pg[1][u] = page_of(tau[1][u]);
     if (held(pg[0][u])) {
@@ -167,7 +168,6 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
       vs[u] = __ldcg(a.c.v_scale + (int64_t)pg[0][u] * a.c.nkv + j);
     }
   }
-  int s = 0;
   for (; s < nst; ++s) {
     // the lookups of the stages to come
     int tau3[NU], pg2[NU];
@@ -257,6 +257,74 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
   if (__any_sync(0xffffffffu, bad) && lane == 0 && sh.fault == 0) sh.fault = 6;  // QUOKA_ERR_BOUNDS
 }
 
+// Stage 0 of listed rows, by the four computing warps, 32 rows each: their chain
+// index -> page -> row is the longest of a CTA with few keys, and one warp would
+// take as long again to issue the copies. Returns the stages there are (the
+// caller waits for its copies, and at a barrier for those of the others).
+template <int D>
+__device__ __forceinline__ int load_first(const CacheAttnArgs& a, Shared& sh, uint8_t* ring, int warp, int lane, int bi,
+                                          int j, int k0, int k1) {
+  using R = Ring<D>;
+  constexpr int CPR = D / 16, RPI = 32 / CPR;
+  if (k0 >= k1) return 0;
+  const int key = k0 + 32 * warp + lane;
+  const bool here = key < k1;
+  int tau = -1, p = -1;
+  if (here) tau = __ldcg(a.kv_idx + ((int64_t)bi * a.c.nkv + j) * a.N + key);
+  const int len = min(max(__ldcg(a.c.seq_len + bi), 0), a.max_len);
+  if (tau >= 0 && tau < len) p = __ldcg(a.c.page_table + (int64_t)bi * a.c.table_stride + (tau >> a.c.page_log2));
+  const bool held = p >= 0 && p < a.c.npages;
+  int64_t off = -1;
+  float ks = 1.f, vs = 1.f;
+  if (held) {
+    ks = __ldcg(a.c.k_scale + (int64_t)p * a.c.nkv + j);
+    vs = __ldcg(a.c.v_scale + (int64_t)p * a.c.nkv + j);
+    off = p * a.c.sp + (int64_t)(tau & ((1 << a.c.page_log2) - 1)) * a.c.sr;
+  }
+  const int c = lane % CPR, r0 = lane / CPR;
+  const uint8_t* kb = a.c.k + j * a.c.sh + 16 * c;
+  const uint8_t* vb = a.c.v + j * a.c.sh + 16 * c;
+  const uint32_t dst = sm100::smem_u32(ring);
+#pragma unroll
+  for (int i = 0; i < 32 / RPI; ++i) {
+    const int r = i * RPI + r0;
+    const int64_t o = __shfl_sync(0xffffffffu, off, r);
+    const int64_t so = o >= 0 ? o : 0;
+    const uint32_t n = o >= 0 ? 16u : 0u, at = at_chunk<D>(32 * warp + r, c);
+    sm100::cp_async_16(dst + at, kb + so, n);
+    sm100::cp_async_16(dst + R::kBytes + at, vb + so, n);
+  }
+  bool bad = here && !held;  // (reads as zeros)
+  const int ek = held ? scale_exp(ks, &bad) : 0, ev = held ? scale_exp(vs, &bad) : 0;
+  sh.ex[0][32 * warp + lane] = (uint32_t)(ek + 64) | (uint32_t)(ev + 64) << 16;
+  if (__any_sync(0xffffffffu, bad) && lane == 0) sh.fault = 6;  // QUOKA_ERR_BOUNDS
+  return (k1 - k0 + kStage - 1) / kStage;
+}
+
+// 16 elements of a query row.
+__device__ __forceinline__ void load_row16(const bf16* q, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(q) + i);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[8 * i + 2 * k] = __uint_as_float(u[k] << 16);
+      x[8 * i + 2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+    }
+  }
+}
+__device__ __forceinline__ void load_row16(const float* q, float (&x)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(q) + i);
+    x[4 * i] = w.x;
+    x[4 * i + 1] = w.y;
+    x[4 * i + 2] = w.z;
+    x[4 * i + 3] = w.w;
+  }
+}
+
 // One CTA per range and block of 64 query rows. RT: 8-row query tiles of a warp.
 template <typename T, int D, bool IDX, int RT>
 __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2)
@@ -313,44 +381,45 @@ cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
     if (want != len && lane == 0) sh.fault = 6;  // QUOKA_ERR_BOUNDS
     load_rows<D, IDX>(a, maps, sh, ring, lane, bi, j, len, k0, k1);
   } else {
-    // ---- query rows: row r is head j G + (rb + r) / BCP, chunk position (rb + r) % BCP; a
-    // warp takes four rows at a time, their loads together
-    for (int r4 = warp; r4 < tiles * RT * 8; r4 += 16) {
-      float x[4][D / 32];
+    const int nst0 = IDX ? load_first<D>(a, sh, ring, warp, lane, bi, j, k0, k1) : 0;
+    // ---- query rows: row r is head j G + (rb + r) / BCP, chunk position (rb + r) % BCP. A
+    // lane takes a 16-column chunk of a row, a warp RPW rows at a time.
+    constexpr int CPR = D / 16, RPW = 32 / CPR;
+    const int ch = lane % CPR;
+    for (int r = RPW * warp + lane / CPR; r < tiles * RT * 8; r += 4 * RPW) {
+      float x[16];
+      if (r < Rb) {
+        const int h = (rb + r) / a.BCP, t = rb + r - h * a.BCP;
+        const T* q = static_cast<const T*>(a.Q.data) + bi * a.Q.sb + (int64_t)(j * G + h) * a.Q.sh + (int64_t)t * a.Q.st;
+        load_row16(q + 16 * ch, x);
+      } else {
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int r = r4 + 4 * y;
-        const T* q = static_cast<const T*>(a.Q.data) + bi * a.Q.sb + (int64_t)(j * G + (rb + r) / a.BCP) * a.Q.sh +
-                     (int64_t)((rb + r) % a.BCP) * a.Q.st;
-        // lane: columns [D / 32 * lane, + D / 32)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) x[y][i] = r < Rb ? to_f32(q[D / 32 * lane + i]) : 0.f;
+        for (int i = 0; i < 16; ++i) x[i] = 0.f;
       }
+      float top = 0.f;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int r = r4 + 4 * y;
-        if (r < tiles * RT * 8) {
-          float top = 0.f;
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) top = fmaxf(top, fabsf(x[y][i]));
+      for (int o_ = CPR / 2; o_ > 0; o_ >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o_));
+      int e = (int)(__float_as_uint(top) >> 23) - 127 - 13;  // top * 2^-e lies in [2^13, 2^14)
+      e = min(max(e, -100), 114);                            // (zero and tiny rows, infinities)
+      const float f = exp2i(-e);
+      if (ch == 0) rowf[r] = exp2i(e) * a.scale * kLog2e;
+      // word w of chunk ch belongs to k-step 4 (ch / 4) + w and lane 4 (r % 8) + ch % 4
+      uint32_t* dst = qs + (((r >> 3) * KS + 4 * (ch >> 2)) * 32 + (r & 7) * 4 + (ch & 3)) * (2 * SPLIT);
 #pragma unroll
-          for (int o_ = 16; o_ > 0; o_ >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o_));
-          int e = (int)(__float_as_uint(top) >> 23) - 127 - 13;  // top * 2^-e lies in [2^13, 2^14)
-          e = min(max(e, -100), 114);                            // (zero and tiny rows, infinities)
-          const float f = exp2i(-e);
-          if (lane == 0) rowf[r] = exp2i(e) * a.scale * kLog2e;
-#pragma unroll
-          for (int i = 0; i < D / 32; i += 2) {
-            const int d = D / 32 * lane + i;
-            // column d belongs to chunk d / 16 = t + 4 * (ks / 4), word (d % 16) / 4 = ks % 4 of it
-            const int ch = d >> 4, ks = 4 * (ch >> 2) + ((d & 15) >> 2), reg = (d >> 1) & 1;
-            uint32_t* dst = qs + (((r >> 3) * KS + ks) * 32 + (r & 7) * 4 + (ch & 3)) * (2 * SPLIT) + reg;
-            const uint32_t hi = pack_h2(x[y][i] * f, x[y][i + 1] * f);
-            *dst = hi;
-            if constexpr (SPLIT == 2) dst[2] = rest_h2(x[y][i] * f, x[y][i + 1] * f, hi);
-          }
-        }
+      for (int w = 0; w < 4; ++w) {
+        const float y0 = x[4 * w] * f, y1 = x[4 * w + 1] * f, y2 = x[4 * w + 2] * f, y3 = x[4 * w + 3] * f;
+        const uint32_t h0 = pack_h2(y0, y1), h1 = pack_h2(y2, y3);
+        if constexpr (SPLIT == 2)
+          *reinterpret_cast<uint4*>(dst + w * 32 * 4) = make_uint4(h0, h1, rest_h2(y0, y1, h0), rest_h2(y2, y3, h1));
+        else
+          *reinterpret_cast<uint2*>(dst + w * 32 * 2) = make_uint2(h0, h1);
       }
+    }
+    if (nst0 > 0) {  // the first stage's copies, which this warp issued
+      sm100::cp_async_commit();
+      sm100::cp_async_wait<0>();
     }
     sm100::named_barrier_sync(1, 128);
     float f[RT][2];
@@ -516,7 +585,9 @@ cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
     const int nst = (k1 - k0 + kStage - 1) / kStage;
     for (int i = 0; i < nst; ++i) {
       const int st = i % kStages;
-      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&sh.full[st], (i / kStages) & 1, &sh.abort))) {
+      // (of listed rows stage 0 is there: slot 0 is filled by the loader one time less)
+      const uint32_t parity = (i / kStages - (IDX && st == 0 ? 1 : 0)) & 1;
+      if ((!IDX || i > 0) && !__all_sync(0xffffffffu, sm100::mbar_wait(&sh.full[st], parity, &sh.abort))) {
         if (lane == 0) {
           sh.abort = 1;
           sh.fault = 5;  // QUOKA_ERR_TIMEOUT
