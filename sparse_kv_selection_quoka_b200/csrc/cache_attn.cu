@@ -632,21 +632,28 @@ cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
   for (int e = tid; e < Rb * (D / 4); e += kThreads) {
     const int r = e / (D / 4), c4 = e % (D / 4);
     const int tl = r / TR, rr = r % TR;
-    float M = -INFINITY;
-    for (int k = 0; k < kgroups; ++k) M = fmaxf(M, ml[((k * tiles + tl) * TR + rr) * 2]);
+    // (all four groups' loads together; a group that is not there repeats the last one's)
+    float mk[4], lk[4], M = -INFINITY;
+    float4 y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int w = (min(k, kgroups - 1) * tiles + tl) * TR + rr;
+      mk[k] = ml[w * 2];
+      lk[k] = k < kgroups ? ml[w * 2 + 1] : 0.f;
+      y[k] = *reinterpret_cast<const float4*>(os + w * D + 4 * c4);
+      M = fmaxf(M, mk[k]);
+    }
     float L = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < kgroups; ++k) {
-      const int w = k * tiles + tl;
-      const float lw = ml[(w * TR + rr) * 2 + 1];
-      if (lw == 0.f) continue;  // the warp saw no key (not so for NaN scores: they come through)
-      const float fw = exp2f(ml[(w * TR + rr) * 2] - M);
-      const float4 y = *reinterpret_cast<const float4*>(os + (w * TR + rr) * D + 4 * c4);
-      L = fmaf(fw, lw, L);
-      x.x = fmaf(fw, y.x, x.x);
-      x.y = fmaf(fw, y.y, x.y);
-      x.z = fmaf(fw, y.z, x.z);
-      x.w = fmaf(fw, y.w, x.w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (lk[k] == 0.f) continue;  // the warp saw no key (not so for NaN scores: they come through)
+      const float fw = exp2f(mk[k] - M);
+      L = fmaf(fw, lk[k], L);
+      x.x = fmaf(fw, y[k].x, x.x);
+      x.y = fmaf(fw, y[k].y, x.y);
+      x.z = fmaf(fw, y[k].z, x.z);
+      x.w = fmaf(fw, y[k].w, x.w);
     }
     const float inv = L != 0.f ? 1.f / L : 0.f;
     const int64_t at = (int64_t)range * R + rb + r;
