@@ -44,11 +44,7 @@ constexpr int QF_WARPS = QF_THREADS / 32;
 constexpr int QF_MAX_BCP = 512;
 constexpr int QF_MAX_NQ = 32;
 constexpr int QF_MAX_G = 8;
-// Up to so many winners are ranked directly instead of by the merge tree (NQ = 4, 512
-// rows: a selection over 32768 cached keys 23.3 -> 22.8 us).
-constexpr int QF_RANKED = 8;
 constexpr int QF_CHUNKS = QF_D / 8;  // 16-byte chunks per bf16 row
-static_assert(QF_WARPS % 2 == 0 && QF_WARPS * QF_RANKED <= (QF_WARPS - 1) * 32, "ranked keys lie over the lists");
 static_assert(QF_MAX_NQ * (QF_D / 4) % QF_THREADS == 0, "group-mean units per thread");
 
 struct __align__(16) QfShared {
@@ -56,7 +52,7 @@ struct __align__(16) QfShared {
   alignas(16) float colpart[QF_WARPS][QF_D];  // per-warp column sums
   alignas(16) float mq[QF_D];
   float nrm[QF_MAX_BCP];             // |Q[t]| (clamped)
-  alignas(16) uint64_t lists[QF_WARPS][32];       // sorted (key, position) lists of the merge tree
+  uint64_t lists[QF_WARPS][32];       // sorted (key, position) lists of the merge tree
   float mq_norm;
 };
 static_assert(offsetof(QfShared, qhat) % 16 == 0 && sizeof(float) * QF_D % 16 == 0, "float4 rows of qhat");
@@ -201,45 +197,26 @@ qsel_fast_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
   }
   // 4. per-warp sort, then a merge tree over the warps' lists
   key = warp_sort_desc(key, lane);
-  if (NQ <= QF_RANKED) {
-    // few winners: the warps' first NQ keys are ranked against each other (keys
-    // differ, but for the rows past the chunk, which are never among the winners)
-    uint64_t* cand = sh.lists[1];
-    if (lane < NQ) cand[warp * NQ + lane] = key;
-    __syncthreads();
-    if (tid < QF_WARPS * NQ) {
-      const uint64_t mine = cand[tid];
-      int rank = 0;
-#pragma unroll 4
-      for (int i = 0; i < QF_WARPS * NQ; i += 2) {
-        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(cand + i);
-        rank += (o.x > mine) + (o.y > mine);
-      }
-      if (rank < NQ) sh.lists[0][rank] = mine;
-    }
-    __syncthreads();
-  } else {
-    sh.lists[warp][lane] = key;
-    __syncthreads();
-    // warps 0-3 fold lists 4w+1 .. 4w+3 into list 4w; then warp 0 folds the
-    // four results into list 0
-    if (warp < 4) {
-      uint64_t m = sh.lists[4 * warp][lane];
+  sh.lists[warp][lane] = key;
+  __syncthreads();
+  // warps 0-3 fold lists 4w+1 .. 4w+3 into list 4w; then warp 0 folds the
+  // four results into list 0
+  if (warp < 4) {
+    uint64_t m = sh.lists[4 * warp][lane];
 #pragma unroll 1
-      for (int u = 1; u < 4; ++u) m = warp_merge_top(m, sh.lists[4 * warp + u], lane);
-      __syncwarp();
-      sh.lists[4 * warp][lane] = m;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      uint64_t m = sh.lists[0][lane];
-#pragma unroll 1
-      for (int u = 1; u < 4; ++u) m = warp_merge_top(m, sh.lists[4 * u], lane);
-      __syncwarp();
-      sh.lists[0][lane] = m;
-    }
-    __syncthreads();
+    for (int u = 1; u < 4; ++u) m = warp_merge_top(m, sh.lists[4 * warp + u], lane);
+    __syncwarp();
+    sh.lists[4 * warp][lane] = m;
   }
+  __syncthreads();
+  if (warp == 0) {
+    uint64_t m = sh.lists[0][lane];
+#pragma unroll 1
+    for (int u = 1; u < 4; ++u) m = warp_merge_top(m, sh.lists[4 * u], lane);
+    __syncwarp();
+    sh.lists[0][lane] = m;
+  }
+  __syncthreads();
   // 5. normalise the winners (thread = rank i, chunk cc), rank order
   {
     const int i = tid >> 4, cc = tid & 15;
