@@ -120,33 +120,30 @@ __device__ __forceinline__ void drain_ring(Smem& sm, uint64_t* full, int nload, 
 }
 
 // One thread per ring (K or V): the tiles 0 .. nT - 1 (selected tiles from
-// the gathered maps, then chunk tiles, or the other way round: `first` tiles of
-// the one kind come first), each into the next stage of its ring once that
-// stage is released. The stages tile kt needs are released by the
+// the gathered maps, then chunk tiles), each into the next stage of its ring
+// once that stage is released. The stages tile kt needs are released by the
 // QK^T (K) and the PV (V) of tile kt - 3; the MMA order (QK0(2i), PV1(2i-1),
 // QK1(2i+1), PV0(2i)) issues the PV of a tile right after the QK^T of the
 // next one, so both come before the QK^T of tile kt - 1: the loads never
 // wait on a product that waits on a later load. With a thread per ring, a K
 // load never queues behind a V stage that is released later.
 template <bool IS_V, int HD>
-__device__ __forceinline__ void load_kv(Smem& sm, const Maps& maps, int nT, int kt_base, int first, bool chunk_first,
-                                        int j, int bi, int* status) {
+__device__ __forceinline__ void load_kv(Smem& sm, const Maps& maps, int nT, int kt_base, int ntile_sel, int j,
+                                        int bi, int* status) {
   constexpr int ST = IS_V ? VST : KST;
   uint64_t* const full = IS_V ? sm.v_full : sm.k_full;
   uint64_t* const empty = IS_V ? sm.v_empty : sm.k_empty;
   int nl = 0;
   for (int kt = 0; kt < nT; ++kt) {
-    const int g = kt_base + kt;
-    const bool sel_tile = g < first != chunk_first;
+    const bool sel_tile = kt_base + kt < ntile_sel;
     const int s = kt % ST;
-    if (chunk_first && sel_tile) pdl_wait();  // the gathered rows come from the previous kernel
     if (kt >= ST && !mbar_wait(&empty[s], ((kt / ST) - 1) & 1, &sm.abort, sm.wait_ns)) {
       record_abort(sm, status, IS_V ? 14 : 11);
       break;
     }
     const CUtensorMap* m = IS_V ? (sel_tile ? &maps.vs : &maps.vc) : (sel_tile ? &maps.ks : &maps.kc);
     load_tile<HD>(smem_u32(IS_V ? sm.v[s] : sm.k[s]), m, &full[s],
-                  (g < first ? g : g - first) * N, j, bi);
+              (sel_tile ? kt_base + kt : kt_base + kt - ntile_sel) * N, j, bi);
     nl = kt + 1;
   }
   drain_ring<ST>(sm, full, nl, status, IS_V ? 15 : 12);
@@ -212,16 +209,11 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     load_tile<HD>(smem_u32(sm.q), &maps.q, &sm.q_full, t0, h, bi);
   }
 
-  // The gathered rows and their counts come from the previous kernel. With
-  // chunk_first the counts are inputs of the call and the chunk's own keys come
-  // first, while that kernel still runs: only the loads of gathered tiles wait.
-  const bool cf = a.chunk_first != 0;
-  if (!cf) pdl_wait();
+  pdl_wait();  // the gathered rows and their counts come from the previous kernel
   const int64_t kvrow = (int64_t)bi * a.nkv + j;
-  const int nsel = a.bsa > 0 ? max(0, min(__ldcg(a.seq_count != nullptr ? a.seq_count + bi : a.kv_count + kvrow), a.bsa)) : 0;
+  const int nsel = a.bsa > 0 ? max(0, min(__ldcg(a.kv_count + kvrow), a.bsa)) : 0;
   const int nchunk = a.no_chunk ? 0 : a.pack ? a.BCP : min(a.BCP, t0 + 128);
   const int ntile_sel = (nsel + N - 1) / N;
-  const int first = cf ? (nchunk + N - 1) / N : ntile_sel;  // tiles of the kind that comes first
   const int nT_all = ntile_sel + (nchunk + N - 1) / N;  // key tiles (0 only without the chunk's keys)
   // this CTA's key tiles: range `split` of nsplit (all of them when 1)
   const int kt_base = (int)((int64_t)nT_all * split / a.nsplit);
@@ -230,10 +222,10 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
 
   if (warp == LOAD_WARP) {
     // ------------------------------------------------------------ TMA loads
-    if (lane == 0) load_kv<false, HD>(sm, maps, nT, kt_base, first, cf, j, bi, a.status);
+    if (lane == 0) load_kv<false, HD>(sm, maps, nT, kt_base, ntile_sel, j, bi, a.status);
     __syncwarp();
   } else if (warp == VLOAD_WARP) {
-    if (lane == 0) load_kv<true, HD>(sm, maps, nT, kt_base, first, cf, j, bi, a.status);
+    if (lane == 0) load_kv<true, HD>(sm, maps, nT, kt_base, ntile_sel, j, bi, a.status);
     __syncwarp();
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issue
@@ -307,24 +299,27 @@ attn_tma_kernel(const __grid_constant__ Maps maps, const AttnArgs a) {
     float m = -INFINITY, l = 0.f;
     bool alive = true;
     const int nmine = (nT - w + 1) / 2;  // key tiles of this warpgroup (warpgroup-uniform)
+    // the range's selected tiles come first (none when it starts past them);
+    // selected key numbers relative to the range's first key
+    const int sel_rel = ntile_sel - kt_base;
+    const int nsel_rel = nsel - kt_base * N;
     for (int i = 0; i < nmine && alive; ++i) {
       alive = warp_wait(&sm.s_full[w], i & 1, sm, a.status, 31 + w);
       if (!alive) break;
       tc_fence_after();
       const int kt = 2 * i + w;  // (within this CTA's key range)
-      const int g = kt_base + kt;
-      const bool sel_tile = g < first != cf;
-      // key c of the tile is key number base_n + c of its list; it is visible
-      // to row t when it is a selected key below nsel, or a chunk key at a
-      // position p < nchunk not after the row's
-      const int base_n = (g < first ? g : g - first) * N;
-      const int lim = sel_tile ? nsel : min(nchunk, pos + 1);
+      const bool sel_tile = kt < sel_rel;
+      // key c of the tile is key number base_n + c of its list (selected
+      // keys counted from the range's first one); it is visible to row t
+      // when it is a selected key below nsel, or a chunk key at a position
+      // p < nchunk not after the row's
+      const int base_n = (sel_tile ? kt : kt - sel_rel) * N;
+      const int lim = sel_tile ? nsel_rel : min(nchunk, pos + 1);
       softmax_tile_split<PV_PARTS, HD>(S, tmem + lane_off + 256u + 128u * w, i > 0, base_n, lim,
                                                      qscale, m, l, sm.p_part[w]);
     }
 
     // ------------------------------------------------ combine and store
-    if (cf) pdl_wait();  // (long done; this kernel ends behind the one before)
     // (both warpgroups reach the named barriers below, whatever happened
     // in the loop)
     if (alive) alive = warp_wait(&sm.o_final, 0, sm, a.status, 33);

@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kThreads) cache_gather_kernel(const CacheGathe
   if (a.kv_idx != nullptr && n < a.N) tau = __ldcg(a.kv_idx + row * a.N + n);
   const int want = __ldcg(a.c.seq_len + bi), len = min(max(want, 0), a.max_len);
   const int cnt = a.kv_idx != nullptr ? min(max(__ldcg(a.kv_count + row), 0), a.N) : len;
+  if (a.count_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) a.count_out[row] = cnt;
   bool bad = want != len;
   int64_t off = -1;
   float kf = 1.f, vf = 1.f;

@@ -110,11 +110,6 @@ struct AttnArgs {
   // one another without a gap: Q.sh = BCP * Q.st), cut into 128-row tiles across
   // heads (tensor-core attention over gathered rows only)
   int pack = 0;
-  // 1: kv_count (or seq_count) is an input of the call, not made by the kernel
-  // before; the chunk's own keys are then taken first, while that kernel still
-  // gathers the selected rows (tensor-core attention over gathered rows only)
-  int chunk_first = 0;
-  const int32_t* seq_count = nullptr;  // (b): rows of every KV head of a batch entry, instead of kv_count
   int tc_d64 = 0;           // 1: launch_attn_tc also takes d = 64 (rows already gathered)
   uint64_t wait_ns = 0;     // bound of every wait (set by the launcher from wait_hooks())
   int inject = 0;           // test hook (set by the launcher from wait_hooks())
@@ -215,6 +210,7 @@ struct CacheGatherArgs {
   int N;
   void* Ksel;
   void* Vsel;
+  int32_t* count_out;  // (b, nkv) or null: the rows there are
   int* status;
 };
 cudaError_t launch_cache_gather(bool bf16, int d, const CacheGatherArgs& a, bool pdl, cudaStream_t stream);

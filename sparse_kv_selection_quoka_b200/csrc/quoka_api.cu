@@ -500,10 +500,10 @@ int cache_attn_nsplit(int64_t b, int64_t nq, int64_t nkv, int64_t BCP, int64_t N
 
 // Workspace of quoka_cache_attn: the status words, then either the partials
 // of the key ranges (few query rows, or fp32) or the dequantised keys and values
-// and the partials of the tensor-core attention.
+// with their counts and the partials of the tensor-core attention.
 struct CacheAttnWs {
   bool few;
-  size_t o_parts, lse_parts, row_parts, faults, ksel, vsel, aparts, aparts_bytes, total;
+  size_t o_parts, lse_parts, row_parts, faults, ksel, vsel, count, aparts, aparts_bytes, total;
 };
 
 CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t BCP, int64_t N, quoka_dtype dtype,
@@ -526,6 +526,7 @@ CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t
   } else {
     w.ksel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
     w.vsel = take((size_t)(b * nkv * N * d) * elt_size(dtype));
+    w.count = take((size_t)(b * nkv) * 4);
     // (whether rows can be packed depends on Q's strides: room for either)
     const int n = std::max(cache_attn_nsplit(b, nq, nkv, BCP, N, no_chunk, false),
                            cache_attn_packs(nq, nkv, BCP) ? cache_attn_nsplit(b, nq, nkv, BCP, N, no_chunk, true) : 1);
@@ -959,6 +960,7 @@ quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, i
     g.N = N;
     g.Ksel = at<void>(ws, w.ksel);
     g.Vsel = at<void>(ws, w.vsel);
+    g.count_out = at<int32_t>(ws, w.count);
     g.status = status;
     const cudaError_t e = quoka::launch_cache_gather(bf, (int)d, g, true, cs);
     if (e != cudaSuccess) return cuda_status(e);
@@ -977,9 +979,7 @@ quoka_status quoka_cache_attn(const quoka_tensor* Q, const quoka_cache* cache, i
   t.BCP = (int)BCP;
   t.T = N;
   t.kv_idx = nullptr;
-  t.kv_count = kv_count;
-  t.seq_count = kv_idx == nullptr ? a.c.seq_len : nullptr;
-  t.chunk_first = 1;
+  t.kv_count = at<int32_t>(ws, w.count);
   t.bsa = N;
   t.scale = scale;
   t.O = O;
