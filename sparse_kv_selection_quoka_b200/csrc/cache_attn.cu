@@ -28,7 +28,8 @@
 // looks the rows up (list entry, page, scales: each a stage ahead of the next,
 // so that no lookup is waited for) and copies 128 keys at a time into a ring of
 // stages: listed rows with cp.async, runs of keys by boxes of up to 64 with
-// TMA; a row that is not there reads as zeros. Four warps compute. They
+// TMA; a row that is not there reads as zeros. Four warps compute (and copy the
+// first stage of listed rows: a CTA may have no other). They
 // share the query tiles (8 rows, or 16 where there are more) and take a
 // stage's 32-key steps in turn.
 // Keys are the rows of the first product S^T = K Q^T, columns of the head those
@@ -47,7 +48,8 @@
 // d = 128: 61.5 us for 337.9 MB, 5.5 TB/s, and 6 us for the join (187 us when every
 // warp loaded its own fragments from global memory, 76.6 with a cp.async ring);
 // the products left out of that kernel, it took 66 us. One sequence of 4096
-// listed keys: 9.2 us, a chain of count, list, table, rows; join 6.5.
+// listed keys: 8.4 us a call, a chain of count, list, table, rows (9.7 when the
+// loader alone fetched the first stage and a warp took a query row at a time).
 #include <algorithm>
 
 #include "cache.cuh"

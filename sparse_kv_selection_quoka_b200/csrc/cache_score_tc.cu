@@ -28,9 +28,9 @@
 // digit) is counted in shared memory and added to the row's at the end.
 // Bound by its latency chain a tile (product, accumulator load, release) and the
 // fixed costs of a range (pieces, TMEM, histogram). Measured: 32768 keys, 8 heads,
-// d = 128: selection with 32 group means 33.9 us, 48.1 with mma.sync products;
-// 8 group means 31.5 both; 4 30.7 against 28.7, so that few stay there. 444 ranges
-// instead of 296: 3 us more.
+// d = 128: selection with 5 group means 24.7 us, 8 26.5, 32 28.9 (mma.sync products
+// took 14 us more), 64 43.0, 128 61.8; 4 24.7 against 22.8 with mma.sync, so that few
+// stay there. 444 ranges instead of 296: 3 us more.
 // Every wait is bounded; one that gives up records QUOKA_ERR_TIMEOUT and the CTA
 // unwinds (copies and products drained, TMEM freed).
 #include "cache.cuh"

@@ -837,9 +837,9 @@ quoka_status quoka_cache_select(const quoka_tensor* Q, const quoka_cache* cache,
   cudaError_t e = cudaErrorNotSupported;
   // The fused query select takes an SM per query head for any chunk length: with
   // more heads than one round holds, short chunks are faster through the
-  // general kernels (whole call, 1000 keys, 16 sequences x 32 heads: 16 tokens 34.1
-  // us against 42.8 fused, 64 39.0 and 43.1, 128 47.9 and 43.2; 1 x 32 heads: 16.5
-  // both at 16, 20.6 and 16.5 at 128).
+  // general kernels (whole call, 1000 keys, 16 sequences x 32 heads: 16 tokens 33.2
+  // us against 41.9 fused, 64 38.4 and 42.1, 128 47.0 and 41.9; 1 x 32 heads: 14.6
+  // both at 16, 19.5 and 14.7 at 128).
   const bool fused = BCP == 1 || BCP > 64 || (int64_t)b * nq <= 128;
   if (bf && d == 128 && fused)
     e = quoka::launch_qsel_group_fast(strided(Q), b, nq, nkv, BCP, NQ, qidx, qg, nullptr, a.hist, a.status, true, cs);

@@ -26,19 +26,18 @@
 //      keys == u* needed to reach BSA: each warp owns a contiguous segment of
 //      the slice, counts its picks, one block scan gives every warp its
 //      offset, and the warp writes its picks in order with ballots.
+// When a bucket holds more candidates than the gathered list can take, the
+// exact passes run over every slice instead, their histograms summed over
+// the cluster through distributed shared memory.
 // Rows of at most TOPK_SMALL keys take one small CTA with the keys in registers
 // instead: a search of the key's bits from the top, two at a time, by counting
 // the keys at or above three thresholds (one block barrier a step), then one
 // scan that places the picks. 18 rows of 64 keys 7.2 -> 5.3 us, 4 of 905 7.6 -> 6.2.
 // With the scoring kernel's histogram and slices of at most 8192 keys the keys
 // stay in registers too (topk_hist_kernel below): one pass over them and one
-// cluster barrier. The whole cache selection: 16 sequences x 8 heads of up to 8191
-// keys 34.9 -> 28.7 us, 8 rows of 32768 keys 27.1 -> 24.7 (most of the time of the
-// kernel above went to its many short phases, each a barrier and a stretch of
-// code run once).
-// When a bucket holds more candidates than the gathered list can take, the
-// exact passes run over every slice instead, their histograms summed over
-// the cluster through distributed shared memory.
+// cluster barrier. 128 rows of up to 8191 keys 11.2 -> 7.6 us, 8 rows of 32768 10.3
+// -> 6.6 (most of the time of the kernel above goes to its many short phases, each
+// a barrier and a stretch of code run once).
 #include <cooperative_groups.h>
 
 #include <algorithm>
