@@ -39,7 +39,7 @@
  *     takes `ws` clears that word (and the fault-site word after it) on
  *     `stream` before any of its kernels can latch a fault: quoka_select,
  *     quoka_select_ex and quoka_prefill_chunk in their first kernel,
- *     quoka_cache_select in the kernel that makes its group means,
+ *     quoka_cache_select(_padded) in the kernel that makes the group means,
  *     quoka_gather_kv, quoka_decode_attn and the other cache calls in a
  *     one-thread kernel of their own (quoka_cache_attn with few query rows in
  *     its first), the other calls with an 8-byte memset; a kernel latches only
@@ -455,6 +455,20 @@ quoka_status quoka_cache_select(const quoka_tensor* Q, const quoka_cache* cache,
                                 int max_len, int NQ, int BSA, int32_t* kv_idx,
                                 int32_t* kv_count, int32_t* q_idx, float* s_agg,
                                 void* ws, size_t ws_bytes, void* stream);
+
+/* The same for a padded chunk (quoka_cache_append with new_len): the queries of
+ * sequence s are the rows t < new_len[s] of Q (new_len (b) int32, device, in
+ * [0, BCP]); the rows behind are not read and may hold anything. The mean and
+ * the choice of step (a)-(b) are over the queries. A sequence with fewer than NQ
+ * of them keeps them all (q_idx is -1 from there on); one without any selects
+ * nothing: kv_count 0, s_agg not written. A new_len outside [0, BCP] latches
+ * QUOKA_ERR_BOUNDS. quoka_cache_select takes every row of Q as a query, and rows
+ * of padding would be among those it chooses. */
+quoka_status quoka_cache_select_padded(const quoka_tensor* Q, const int32_t* new_len,
+                                       const quoka_cache* cache, int max_len, int NQ,
+                                       int BSA, int32_t* kv_idx, int32_t* kv_count,
+                                       int32_t* q_idx, float* s_agg, void* ws,
+                                       size_t ws_bytes, void* stream);
 
 /* Step (f) over the cache: Ksel[b, j, n] = the value of key kv_idx[b, j, n]
  * for n < kv_count[b, j], and the same for V; with kv_idx and kv_count NULL,

@@ -63,6 +63,7 @@ EXPORTS = (
     "quoka_debug_set_wait_hooks",
     "quoka_cache_append",
     "quoka_cache_select",
+    "quoka_cache_select_padded",
     "quoka_cache_gather",
     "quoka_cache_attn_workspace_size",
     "quoka_cache_attn",
@@ -175,6 +176,8 @@ def load() -> ctypes.CDLL:
         lib.quoka_cache_append.argtypes = [_C, _T, _T, _T, _P, _P, _I64, _I, ctypes.c_uint32, _P, _P, _P, _P, _SZ, _P]
         lib.quoka_cache_select.restype = _I
         lib.quoka_cache_select.argtypes = [_T, _C, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]
+        lib.quoka_cache_select_padded.restype = _I
+        lib.quoka_cache_select_padded.argtypes = [_T, _P, _C, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]
         lib.quoka_cache_gather.restype = _I
         lib.quoka_cache_gather.argtypes = [_C, _I, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]
         lib.quoka_cache_attn_workspace_size.restype = _SZ
@@ -630,8 +633,8 @@ def _binding():
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)
             module.bind(*(ctypes.cast(f, _P).value for f in (
-                lib.quoka_cache_append, lib.quoka_cache_select, lib.quoka_cache_gather, lib.quoka_cache_attn,
-                lib.quoka_select_workspace_size, lib.quoka_cache_attn_workspace_size)))
+                lib.quoka_cache_append, lib.quoka_cache_select, lib.quoka_cache_select_padded, lib.quoka_cache_gather,
+                lib.quoka_cache_attn, lib.quoka_select_workspace_size, lib.quoka_cache_attn_workspace_size)))
             _cache = module
     return _cache
 
@@ -673,18 +676,21 @@ def quoka_cache_append(cache, K, V, Q=None, cos=None, sin=None, *, interleaved=F
     return r
 
 
-def quoka_cache_select(Q, cache, max_len: int, NQ: int, BSA: int, *, kv_idx=None, kv_count=None, q_idx=None,
+def quoka_cache_select(Q, cache, max_len: int, NQ: int, BSA: int, *, new_len=None, kv_idx=None, kv_count=None, q_idx=None,
                        s_agg=None, want_q_idx=False, want_s_agg=False, ws=None, stream=None):
     """Steps (a)-(e) over the cached keys. Returns (kv_idx (b, nkv,
     min(BSA, max_len)) int32 ascending, kv_count (b, nkv) int32, q_idx or
     None, s_agg (b, nkv, max_len) or None); max_len bounds cache.seq_len.
-    Entries past a count, and scores past a sequence's end, are not written."""
+    Entries past a count, and scores past a sequence's end, are not written.
+    new_len (b) int32: of a padded chunk (as quoka_cache_append's), the rows of
+    Q that are queries; fewer than NQ are all kept (q_idx -1 from there on), and
+    a sequence without any has a count of 0. Without it every row is a query."""
     if stream is not None:
         with _on(cache, stream):
-            return quoka_cache_select(Q, cache, max_len, NQ, BSA, kv_idx=kv_idx, kv_count=kv_count, q_idx=q_idx,
+            return quoka_cache_select(Q, cache, max_len, NQ, BSA, new_len=new_len, kv_idx=kv_idx, kv_count=kv_count, q_idx=q_idx,
                                       s_agg=s_agg, want_q_idx=want_q_idx, want_s_agg=want_s_agg, ws=ws)
     r = (_cache or _binding()).select(cache._handle, cache._device, Q, max_len, NQ, BSA, kv_idx, kv_count, q_idx, s_agg,
-                                      bool(want_q_idx), bool(want_s_agg), ws)
+                                      bool(want_q_idx), bool(want_s_agg), ws, new_len)
     if type(r) is int:
         raise QuokaError(r, "quoka_cache_select")
     return r

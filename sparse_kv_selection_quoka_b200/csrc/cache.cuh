@@ -159,6 +159,18 @@ __device__ __forceinline__ void find_range(int rows, int target, int least, int 
   }
 }
 
+// Keys of sequence bi that a selection scores: none without a query.
+__device__ __forceinline__ int scored_keys(const CacheScoreArgs& a, int bi) {
+  const int n = min(max(__ldcg(a.c.seq_len + bi), 0), a.max_len);
+  return a.new_len != nullptr && __ldcg(a.new_len + bi) <= 0 ? 0 : n;
+}
+
+// Latches lengths and counts of a sequence that are out of range (of a selection).
+__device__ __forceinline__ void check_scored(const CacheScoreArgs& a, int bi) {
+  const int want = __ldcg(a.c.seq_len + bi), live = a.new_len != nullptr ? __ldcg(a.new_len + bi) : 0;
+  if (want < 0 || want > a.max_len || live < 0 || live > a.BCP) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
+}
+
 // Rows of a box of the pools' tensor maps: a run of keys that starts on a
 // multiple of 64 splits into boxes of one page each.
 __host__ __device__ __forceinline__ int box_log2(const CacheView& c) { return c.page_log2 < 6 ? c.page_log2 : 6; }

@@ -37,6 +37,7 @@ struct WrongValue : std::runtime_error {
 
 decltype(&quoka_cache_append) g_append;
 decltype(&quoka_cache_select) g_select;
+decltype(&quoka_cache_select_padded) g_select_padded;
 decltype(&quoka_cache_gather) g_gather;
 decltype(&quoka_cache_attn) g_attn;
 decltype(&quoka_select_workspace_size) g_select_ws;
@@ -212,10 +213,10 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// handle, device, Q, max_len, NQ, BSA, kv_idx, kv_count, q_idx, s_agg, want_q_idx, want_s_agg, ws
+// handle, device, Q, max_len, NQ, BSA, kv_idx, kv_count, q_idx, s_agg, want_q_idx, want_s_agg, ws, new_len
 // -> (kv_idx, kv_count, q_idx, s_agg)
 PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("select", n, 13, [&]() -> PyObject* {
+  return guarded("select", n, 14, [&]() -> PyObject* {
     const Call call(a[0], a[1]);
     const auto& c = call.c;
     const Tensor& Q = required(a[2], "Q");
@@ -231,6 +232,8 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* sp = sa ? call.plain(*sa, "s_agg", at::kFloat, {c.b, c.nkv, max_len}) : nullptr;
     size_t wn;
     void* wp = call.workspace(tensor(a[12], "ws"), &wn);
+    const Tensor* fresh = tensor(a[13], "new_len");
+    const int32_t* live = fresh ? (const int32_t*)call.plain(*fresh, "new_len", at::kInt, {c.b}) : nullptr;
     call.on_gpu();
     if (max_len < 0 || NQ < 1) return PyLong_FromLong(QUOKA_ERR_INVALID_ARG);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)call.dev);
@@ -244,8 +247,11 @@ PyObject* select(PyObject*, PyObject* const* a, Py_ssize_t n) {
       wn = std::max<size_t>(256, g_select_ws(c.b, (int)nq, c.nkv, c.d, max_len, (int)BCP, NQ, std::max(0, BSA), qv.dtype));
       wp = (made_w = Call::scratch(wn)).get();
     }
-    const quoka_status st = g_select(&qv, &c, max_len, NQ, BSA, m ? (int32_t*)ip : nullptr, (int32_t*)np, (int32_t*)qp,
-                                     max_len ? (float*)sp : nullptr, wp, wn, call.stream());
+    int32_t* ix = m ? (int32_t*)ip : nullptr;
+    float* sx = max_len ? (float*)sp : nullptr;
+    const quoka_status st =
+        live ? g_select_padded(&qv, live, &c, max_len, NQ, BSA, ix, (int32_t*)np, (int32_t*)qp, sx, wp, wn, call.stream())
+             : g_select(&qv, &c, max_len, NQ, BSA, ix, (int32_t*)np, (int32_t*)qp, sx, wp, wn, call.stream());
     if (st != QUOKA_OK) return PyLong_FromLong(st);
     return Py_BuildValue("(NNNN)", out(a[6], made_i), out(a[7], made_n), out(a[8], made_q), out(a[9], made_s));
   });
@@ -337,13 +343,14 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // The addresses of the entry points.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded("bind", n, 6, [&]() -> PyObject* {
+  return guarded("bind", n, 7, [&]() -> PyObject* {
     g_append = reinterpret_cast<decltype(g_append)>(PyLong_AsVoidPtr(a[0]));
     g_select = reinterpret_cast<decltype(g_select)>(PyLong_AsVoidPtr(a[1]));
-    g_gather = reinterpret_cast<decltype(g_gather)>(PyLong_AsVoidPtr(a[2]));
-    g_attn = reinterpret_cast<decltype(g_attn)>(PyLong_AsVoidPtr(a[3]));
-    g_select_ws = reinterpret_cast<decltype(g_select_ws)>(PyLong_AsVoidPtr(a[4]));
-    g_attn_ws = reinterpret_cast<decltype(g_attn_ws)>(PyLong_AsVoidPtr(a[5]));
+    g_select_padded = reinterpret_cast<decltype(g_select_padded)>(PyLong_AsVoidPtr(a[2]));
+    g_gather = reinterpret_cast<decltype(g_gather)>(PyLong_AsVoidPtr(a[3]));
+    g_attn = reinterpret_cast<decltype(g_attn)>(PyLong_AsVoidPtr(a[4]));
+    g_select_ws = reinterpret_cast<decltype(g_select_ws)>(PyLong_AsVoidPtr(a[5]));
+    g_attn_ws = reinterpret_cast<decltype(g_attn_ws)>(PyLong_AsVoidPtr(a[6]));
     Py_RETURN_NONE;
   });
 }

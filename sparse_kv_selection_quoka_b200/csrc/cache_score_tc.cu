@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_score_tc_kernel(const __gri
   for (int i = tid; i < TOPK_HIST_BINS / 4; i += kThreads) reinterpret_cast<uint4*>(sh.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (warp == kLoadWarp)
     find_range(a.b * a.c.nkv, a.target, kSplitKeys, kStage, blockIdx.x, lane,
-               [&](int i) { return min(max(__ldcg(a.c.seq_len + i / a.c.nkv), 0), a.max_len); },
+               [&](int i) { return scored_keys(a, i / a.c.nkv); },
                reinterpret_cast<int*>(ring), &sh.range);
   if (warp == kLoadWarp) sm100::fence_proxy_async_smem();  // (the ring's copies come behind the lengths)
   __syncthreads();
@@ -204,10 +204,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_score_tc_kernel(const __gri
   }
   const int64_t row = sh.range.row;
   const int bi = sh.range.row / a.c.nkv, j = sh.range.row % a.c.nkv;
-  if (tid == 0) {
-    const int want = __ldcg(a.c.seq_len + bi);
-    if (want < 0 || want > a.max_len) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
-  }
+  if (tid == 0) check_scored(a, bi);
   if (k0 >= k1) {
     pdl_wait();
     return;

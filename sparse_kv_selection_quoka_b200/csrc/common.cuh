@@ -90,6 +90,12 @@ __device__ __forceinline__ void clear_status(int* status) {
   }
 }
 
+// Queries of sequence bi in a chunk of BCP rows: all of them, or, of a padded chunk,
+// the first new_len[bi] (null: not padded; kept to [0, BCP]).
+__device__ __forceinline__ int live_queries(const int32_t* new_len, int bi, int BCP) {
+  return new_len == nullptr ? BCP : min(max(__ldg(new_len + bi), 0), BCP);
+}
+
 // 12-bit bucket of a score, linear over [-1, 1] (cosine-type scores lie
 // there): floor((s + 1) * 2048) clamped to [0, 4095]. Non-decreasing in the
 // score's key order (every step rounds monotonically; a NaN goes to the end

@@ -30,9 +30,12 @@ struct Strided {
 // Step (a)+(b)+(c, first half): one CTA per (batch, query head). Writes the
 // chosen chunk positions in rank order and the chosen queries Qhat
 // (b, nq, NQ, d) fp32, L2-normalised when `normalize` (the cosine score;
-// raw for the dot-product score).
+// raw for the dot-product score). `new_len`, when not null, holds each batch
+// entry's number of queries (b, kept to [0, BCP]): the rows behind are padding.
+// Ranks without a query repeat rank 0 and have position -1.
 cudaError_t launch_qsel(bool bf16, int d, Strided Q, int b, int nq, int BCP, int NQ,
-                        float* Qhat, int32_t* q_idx, bool normalize, cudaStream_t stream);
+                        float* Qhat, int32_t* q_idx, bool normalize, cudaStream_t stream,
+                        const int32_t* new_len = nullptr);
 
 // Step (c, second half): Q_group (b, nkv, NQ, d) fp32 = mean over the G
 // heads of each group of Qhat at the same rank; optionally also the bf16
@@ -49,11 +52,11 @@ cudaError_t launch_qgroup(int d, const float* Qhat, int b, int nq, int nkv, int 
 // bf16, d = 128, BCP <= 512, NQ <= 32, G <= 8, or a one-query chunk
 // (BCP = 1, G <= 32): writes q_idx (rank order, when not null), Qg and
 // Qg_hilo as launch_qgroup does, zeroes `hist` and clears the status words
-// when given; `normalize` as for launch_qsel. Returns
+// when given; `normalize` and `new_len` as for launch_qsel. Returns
 // cudaErrorNotSupported for other shapes.
 cudaError_t launch_qsel_group_fast(Strided Q, int b, int nq, int nkv, int BCP, int NQ, int32_t* q_idx,
                                    float* Qg, uint16_t* Qg_hilo, uint32_t* hist, int* status, bool normalize,
-                                   cudaStream_t stream);
+                                   cudaStream_t stream, const int32_t* new_len = nullptr);
 
 // Step (d) on the CUDA cores (fp32 arithmetic; any input dtype). key_norm:
 // divide by |k| (cosine score) or not (dot-product score).
@@ -80,10 +83,12 @@ int64_t topk_max_T();
 // `hist`, when not null, is the (b * nkv, TOPK_HIST_BINS) histogram of the
 // scores' value buckets made by the scoring kernel; the first pass is then
 // skipped. `row_len`, when not null, holds each batch entry's own number of
-// keys (b, clamped to [0, T]): its rows pick min(bsa, row_len) of them.
+// keys (b, clamped to [0, T]): its rows pick min(bsa, row_len) of them, or, when
+// `new_len` is given too, none where it is not positive.
 cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa,
                         const uint32_t* hist, int32_t* kv_idx, int32_t* kv_count, int* status,
-                        bool pdl, cudaStream_t stream, const int32_t* row_len = nullptr);
+                        bool pdl, cudaStream_t stream, const int32_t* row_len = nullptr,
+                        const int32_t* new_len = nullptr);
 
 // Step (f): gather of the selected K and V rows into contiguous
 // (b, nkv, bsa, d) buffers. Rows past kv_count, and rows whose index is out
@@ -256,6 +261,8 @@ struct CacheScoreArgs {
   float* S_agg;
   uint32_t* hist;
   int* status;
+  const int32_t* new_len = nullptr;  // (b) or null: queries of a padded chunk of BCP rows;
+  int BCP = 0;                       // no key of a sequence without any is scored
   int target = 1;  // ranges asked for (set by the launcher)
 };
 cudaError_t launch_cache_score(int d, const CacheScoreArgs& a, cudaStream_t stream);

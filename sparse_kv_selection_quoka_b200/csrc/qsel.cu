@@ -11,6 +11,11 @@
 // order. [QUOKA §2.3] the kept queries are L2-normalised and averaged over
 // the G query heads of each KV head, rank by rank.
 //
+// A padded chunk (new_len): only a sequence's first new_len rows are queries.
+// Ranks that there is no query for repeat rank 0, which leaves the scores'
+// maximum over the ranks as it is, and have position -1. What a sequence
+// without queries leaves in Qhat is not used: no key of it is scored.
+//
 // (QUOKA = the technical write-up "QUOKA: how it reshapes LLM prefill
 // efficiency", bqwf.cn news item 915859; § numbers are the write-up's.)
 #include <cooperative_groups.h>
@@ -28,7 +33,7 @@ constexpr int QSEL_WARPS = QSEL_THREADS / 32;
 template <typename T, int D>
 __global__ void __launch_bounds__(QSEL_THREADS)
 qsel_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int BCP, int NQ,
-            float* __restrict__ Qhat, int32_t* __restrict__ q_idx, int normalize) {
+            const int32_t* __restrict__ new_len, float* __restrict__ Qhat, int32_t* __restrict__ q_idx, int normalize) {
   extern __shared__ float smem[];
   float* SQ = smem;
   int* sel = reinterpret_cast<int*>(smem + BCP);
@@ -39,6 +44,7 @@ qsel_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int 
   const int h = blockIdx.x, bi = blockIdx.y, nq = gridDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* Qh = Q + bi * sQb + h * sQh;
+  const int n = live_queries(new_len, bi, BCP);
 
   // (a) mean over the chunk's tokens: column c = tid % D, token groups of
   // QSEL_THREADS / D rows; partial sums combined in a fixed order.
@@ -46,7 +52,7 @@ qsel_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int 
   {
     const int c = tid % D, grp = tid / D;
     float acc = 0.f;
-    for (int t = grp; t < BCP; t += NGRP) acc += to_f32(Qh[(int64_t)t * sQt + c]);
+    for (int t = grp; t < n; t += NGRP) acc += to_f32(Qh[(int64_t)t * sQt + c]);
     part[tid] = acc;
   }
   for (int i = tid; i < NQ; i += QSEL_THREADS) sel[i] = 0;
@@ -55,7 +61,7 @@ qsel_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int 
     float s = 0.f;
 #pragma unroll
     for (int g = 0; g < NGRP; ++g) s += part[g * D + tid];
-    mq[tid] = s / (float)BCP;
+    mq[tid] = s / (float)n;
   }
   __syncthreads();
   if (warp == 0) {
@@ -67,7 +73,7 @@ qsel_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int 
   __syncthreads();
 
   // (a) SQ[t] = -(q_t . MQ) / max(|q_t| |MQ|, 1e-8), one warp per token.
-  for (int t = warp; t < BCP; t += QSEL_WARPS) {
+  for (int t = warp; t < n; t += QSEL_WARPS) {
     const T* q = Qh + (int64_t)t * sQt;
     float dot = 0.f, qq = 0.f;
 #pragma unroll
@@ -84,10 +90,10 @@ qsel_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int 
 
   // (b) rank of token t = number of tokens that beat it (larger SQ, or equal
   // SQ at a lower position); ranks below NQ are kept.
-  for (int t = tid; t < BCP; t += QSEL_THREADS) {
+  for (int t = tid; t < n; t += QSEL_THREADS) {
     const float v = SQ[t];
     int r = 0;
-    for (int u = 0; u < BCP; ++u) {
+    for (int u = 0; u < n; ++u) {
       const float w = SQ[u];
       r += (w > v) | ((w == v) & (u < t));
     }
@@ -97,7 +103,7 @@ qsel_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int 
 
   // (c) L2-normalise the kept queries: one warp per rank.
   for (int i = warp; i < NQ; i += QSEL_WARPS) {
-    const int t = sel[i];
+    const int t = sel[i < n ? i : 0];
     const T* q = Qh + (int64_t)t * sQt;
     float v[D / 32];
     float qq = 0.f;
@@ -111,7 +117,7 @@ qsel_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int 
     float* dst = Qhat + (((int64_t)bi * nq + h) * NQ + i) * D;
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) dst[lane + 32 * k] = v[k] / nrm;
-    if (lane == 0 && q_idx != nullptr) q_idx[((int64_t)bi * nq + h) * NQ + i] = t;
+    if (lane == 0 && q_idx != nullptr) q_idx[((int64_t)bi * nq + h) * NQ + i] = i < n ? t : -1;
   }
 }
 
@@ -126,7 +132,8 @@ constexpr size_t QSEL_STAGED_MAX_BYTES = 192 * 1024;
 template <typename T, int D>
 __global__ void __launch_bounds__(QSEL_STAGED_THREADS)
 qsel_staged_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int BCP, int NQ,
-                   float* __restrict__ Qhat, int32_t* __restrict__ q_idx, int normalize) {
+                   const int32_t* __restrict__ new_len, float* __restrict__ Qhat, int32_t* __restrict__ q_idx,
+                   int normalize) {
   extern __shared__ __align__(16) uint8_t qs_raw[];
   T* blk = reinterpret_cast<T*>(qs_raw);
   const size_t blk_bytes = ((size_t)BCP * D * sizeof(T) + 15) & ~size_t(15);
@@ -139,11 +146,12 @@ qsel_staged_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQ
   const int h = blockIdx.x, bi = blockIdx.y, nq = gridDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* Qh = Q + bi * sQb + h * sQh;
+  const int n = live_queries(new_len, bi, BCP);
 
   // stage: row t, 16-byte vector v of the row
   constexpr int VPR = D * (int)sizeof(T) / 16;  // vectors per row
 #pragma unroll 8
-  for (int e = tid; e < BCP * VPR; e += QSEL_STAGED_THREADS) {
+  for (int e = tid; e < n * VPR; e += QSEL_STAGED_THREADS) {
     const int t = e / VPR, v = e % VPR;
     reinterpret_cast<uint4*>(blk + (size_t)t * D)[v] =
         __ldg(reinterpret_cast<const uint4*>(Qh + (int64_t)t * sQt) + v);
@@ -156,7 +164,7 @@ qsel_staged_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQ
   {
     const int c = tid % D, grp = tid / D;
     float acc = 0.f;
-    for (int t = grp; t < BCP; t += NGRP) acc += to_f32(blk[(size_t)t * D + c]);
+    for (int t = grp; t < n; t += NGRP) acc += to_f32(blk[(size_t)t * D + c]);
     part[tid] = acc;
   }
   __syncthreads();
@@ -164,7 +172,7 @@ qsel_staged_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQ
     float sum = 0.f;
 #pragma unroll
     for (int g = 0; g < NGRP; ++g) sum += part[g * D + tid];
-    mq[tid] = sum / (float)BCP;
+    mq[tid] = sum / (float)n;
   }
   __syncthreads();
   if (warp == 0) {
@@ -176,7 +184,7 @@ qsel_staged_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQ
   __syncthreads();
 
   // (a) SQ[t] = -(q_t . MQ) / max(|q_t| |MQ|, 1e-8), one warp per token
-  for (int t = warp; t < BCP; t += QSEL_STAGED_WARPS) {
+  for (int t = warp; t < n; t += QSEL_STAGED_WARPS) {
     const T* q = blk + (size_t)t * D;
     float dot = 0.f, qq = 0.f;
 #pragma unroll
@@ -193,10 +201,10 @@ qsel_staged_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQ
 
   // (b) rank of token t = number of tokens that beat it (larger SQ, or equal
   // SQ at a lower position)
-  for (int t = tid; t < BCP; t += QSEL_STAGED_THREADS) {
+  for (int t = tid; t < n; t += QSEL_STAGED_THREADS) {
     const float v = SQ[t];
     int r = 0;
-    for (int u = 0; u < BCP; ++u) {
+    for (int u = 0; u < n; ++u) {
       const float w = SQ[u];
       r += (w > v) | ((w == v) & (u < t));
     }
@@ -206,7 +214,7 @@ qsel_staged_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQ
 
   // (c) L2-normalise the kept queries, one warp per rank
   for (int i = warp; i < NQ; i += QSEL_STAGED_WARPS) {
-    const int t = sel[i];
+    const int t = sel[i < n ? i : 0];
     const T* q = blk + (size_t)t * D;
     float v[D / 32];
     float qq = 0.f;
@@ -220,7 +228,7 @@ qsel_staged_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQ
     float* dst = Qhat + (((int64_t)bi * nq + h) * NQ + i) * D;
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) dst[lane + 32 * k] = v[k] / nrm;
-    if (lane == 0 && q_idx != nullptr) q_idx[((int64_t)bi * nq + h) * NQ + i] = t;
+    if (lane == 0 && q_idx != nullptr) q_idx[((int64_t)bi * nq + h) * NQ + i] = i < n ? t : -1;
   }
 }
 
@@ -238,7 +246,8 @@ constexpr int QSEL_CL_MAX = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(QSEL_CL_THREADS)
 qsel_cluster_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int BCP, int NQ,
-                    int slice, float* __restrict__ Qhat, int32_t* __restrict__ q_idx, int normalize) {
+                    int slice, const int32_t* __restrict__ new_len, float* __restrict__ Qhat,
+                    int32_t* __restrict__ q_idx, int normalize) {
   pdl_trigger();  // the group mean's launch overlaps this kernel
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
@@ -256,8 +265,9 @@ qsel_cluster_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
 
   const int h = blockIdx.y, bi = blockIdx.z, nq = gridDim.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = live_queries(new_len, bi, BCP);
   const int r0 = c * slice;
-  const int nrows = max(0, min(slice, BCP - r0));
+  const int nrows = max(0, min(slice, n - r0));
   const T* Qh = Q + bi * sQb + h * sQh;
 
   constexpr int VPR = D * (int)sizeof(T) / 16;  // 16-byte vectors per row
@@ -288,7 +298,7 @@ qsel_cluster_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
   if (tid < D) {
     float sum = 0.f;
     for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(colsum, r)[tid];
-    mq[tid] = sum / (float)BCP;
+    mq[tid] = sum / (float)n;
   }
   __syncthreads();
   if (warp == 0) {
@@ -314,7 +324,7 @@ qsel_cluster_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
     if (lane == 0) SQloc[t] = -dot / fmaxf(sqrtf(qq) * mq_norm, 1e-8f);
   }
   cluster.sync();
-  for (int t = tid; t < BCP; t += QSEL_CL_THREADS) SQall[t] = cluster.map_shared_rank(SQloc, t / slice)[t % slice];
+  for (int t = tid; t < n; t += QSEL_CL_THREADS) SQall[t] = cluster.map_shared_rank(SQloc, t / slice)[t % slice];
   __syncthreads();
 
   // (b) rank of each own row over all BCP scores (4 threads per row), and
@@ -327,7 +337,7 @@ qsel_cluster_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
     const float v = SQall[t];
     int rk = 0;
     if (ok) {
-      for (int u = sub; u < BCP; u += 4) {
+      for (int u = sub; u < n; u += 4) {
         const float w = SQall[u];
         rk += (w > v) | ((w == v) & (u < t));
       }
@@ -349,8 +359,13 @@ qsel_cluster_kernel(const T* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
       float* dst = Qhat + (((int64_t)bi * nq + h) * NQ + rk) * D;
       for (int k = sub; k < D; k += 4) dst[k] = to_f32(q[k]) / nrm;
       if (sub == 0 && q_idx != nullptr) q_idx[((int64_t)bi * nq + h) * NQ + rk] = t;
+      if (rk == 0)
+        for (int i = n; i < NQ; ++i)
+          for (int k = sub; k < D; k += 4) dst[(int64_t)i * D + k] = to_f32(q[k]) / nrm;
     }
   }
+  if (c == 0 && q_idx != nullptr)
+    for (int i = n + tid; i < NQ; i += QSEL_CL_THREADS) q_idx[((int64_t)bi * nq + h) * NQ + i] = -1;
   cluster.sync();  // keep this CTA's shared memory alive for remote readers
 }
 
@@ -386,7 +401,7 @@ qgroup_kernel(const float* __restrict__ Qhat, int nq, int NQ, float* __restrict_
 
 template <typename T, int D>
 static cudaError_t qsel_typed(Strided Q, int b, int nq, int BCP, int NQ, float* Qhat,
-                              int32_t* q_idx, bool normalize, cudaStream_t stream) {
+                              int32_t* q_idx, bool normalize, cudaStream_t stream, const int32_t* new_len) {
   {
     int C = (BCP + 127) / 128;
     if (C > QSEL_CL_MAX) C = QSEL_CL_MAX;
@@ -411,7 +426,7 @@ static cudaError_t qsel_typed(Strided Q, int b, int nq, int BCP, int NQ, float* 
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       return cudaLaunchKernelEx(&cfg, kern, static_cast<const T*>(Q.data), Q.sb, Q.sh, Q.st, BCP, NQ, slice,
-                                Qhat, q_idx, (int)normalize);
+                                new_len, Qhat, q_idx, (int)normalize);
     }
   }
   const size_t blk_bytes = ((size_t)BCP * D * sizeof(T) + 15) & ~size_t(15);
@@ -421,7 +436,7 @@ static cudaError_t qsel_typed(Strided Q, int b, int nq, int BCP, int NQ, float* 
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)QSEL_STAGED_MAX_BYTES);
     if (e != cudaSuccess) return e;
     kern<<<dim3(nq, b), QSEL_STAGED_THREADS, staged, stream>>>(static_cast<const T*>(Q.data), Q.sb, Q.sh, Q.st,
-                                                               BCP, NQ, Qhat, q_idx, (int)normalize);
+                                                               BCP, NQ, new_len, Qhat, q_idx, (int)normalize);
     return cudaGetLastError();
   }
   const size_t smem = (size_t)BCP * sizeof(float) + (size_t)NQ * sizeof(int);
@@ -431,18 +446,18 @@ static cudaError_t qsel_typed(Strided Q, int b, int nq, int BCP, int NQ, float* 
     if (e != cudaSuccess) return e;
   }
   kern<<<dim3(nq, b), QSEL_THREADS, smem, stream>>>(static_cast<const T*>(Q.data), Q.sb, Q.sh, Q.st,
-                                                    BCP, NQ, Qhat, q_idx, (int)normalize);
+                                                    BCP, NQ, new_len, Qhat, q_idx, (int)normalize);
   return cudaGetLastError();
 }
 
 cudaError_t launch_qsel(bool is_bf16, int d, Strided Q, int b, int nq, int BCP, int NQ,
-                        float* Qhat, int32_t* q_idx, bool normalize, cudaStream_t stream) {
+                        float* Qhat, int32_t* q_idx, bool normalize, cudaStream_t stream, const int32_t* new_len) {
   if (is_bf16) {
-    if (d == 128) return qsel_typed<bf16, 128>(Q, b, nq, BCP, NQ, Qhat, q_idx, normalize, stream);
-    if (d == 64) return qsel_typed<bf16, 64>(Q, b, nq, BCP, NQ, Qhat, q_idx, normalize, stream);
+    if (d == 128) return qsel_typed<bf16, 128>(Q, b, nq, BCP, NQ, Qhat, q_idx, normalize, stream, new_len);
+    if (d == 64) return qsel_typed<bf16, 64>(Q, b, nq, BCP, NQ, Qhat, q_idx, normalize, stream, new_len);
   } else {
-    if (d == 128) return qsel_typed<float, 128>(Q, b, nq, BCP, NQ, Qhat, q_idx, normalize, stream);
-    if (d == 64) return qsel_typed<float, 64>(Q, b, nq, BCP, NQ, Qhat, q_idx, normalize, stream);
+    if (d == 128) return qsel_typed<float, 128>(Q, b, nq, BCP, NQ, Qhat, q_idx, normalize, stream, new_len);
+    if (d == 64) return qsel_typed<float, 64>(Q, b, nq, BCP, NQ, Qhat, q_idx, normalize, stream, new_len);
   }
   return cudaErrorNotSupported;
 }

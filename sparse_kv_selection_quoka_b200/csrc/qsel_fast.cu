@@ -103,8 +103,8 @@ __device__ __forceinline__ void cl_wait() { asm volatile("barrier.cluster.wait.a
 
 __global__ void __launch_bounds__(QF_THREADS, 1)
 qsel_fast_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t sQt, int nq, int BCP, int NQ,
-                 int32_t* __restrict__ q_idx, float* __restrict__ Qg, bf16* __restrict__ Qg_hilo,
-                 uint32_t* __restrict__ hist, int* __restrict__ status, int normalize) {
+                 const int32_t* __restrict__ new_len, int32_t* __restrict__ q_idx, float* __restrict__ Qg,
+                 bf16* __restrict__ Qg_hilo, uint32_t* __restrict__ hist, int* __restrict__ status, int normalize) {
   extern __shared__ __align__(16) uint8_t qf_raw[];
   uint8_t* qs = qf_raw;  // [BCP][256 B], chunk c of row t at slot (c ^ (t & 15))
   __shared__ QfShared sh;
@@ -115,6 +115,7 @@ qsel_fast_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
   const int h = j * G + g;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bf16* Qh = Q + bi * sQb + h * sQh;
+  const int n = live_queries(new_len, bi, BCP);  // the rows that are queries
   clear_status(status);  // the call's first kernel
   pdl_trigger();  // the scoring kernel may launch and start streaming K
 
@@ -126,12 +127,12 @@ qsel_fast_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
 #pragma unroll
     for (int m = 0; m < QF_MAX_BCP / 32; ++m) {
       const int t = rg + 32 * m;
-      v[m] = t < BCP ? __ldg(reinterpret_cast<const uint4*>(Qh + (int64_t)t * sQt) + cc) : make_uint4(0, 0, 0, 0);
+      v[m] = t < n ? __ldg(reinterpret_cast<const uint4*>(Qh + (int64_t)t * sQt) + cc) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int m = 0; m < QF_MAX_BCP / 32; ++m) {
       const int t = rg + 32 * m;
-      if (t < BCP) reinterpret_cast<uint4*>(qs + (size_t)t * 256)[cc ^ (t & 15)] = v[m];
+      if (t < n) reinterpret_cast<uint4*>(qs + (size_t)t * 256)[cc ^ (t & 15)] = v[m];
       const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&v[m]);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -154,7 +155,7 @@ qsel_fast_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < QF_WARPS; ++w) s += sh.colpart[w][tid];
-    sh.mq[tid] = s / (float)BCP;
+    sh.mq[tid] = s / (float)n;
   }
   __syncthreads();
   if (warp == 0) {
@@ -166,10 +167,10 @@ qsel_fast_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
   }
   __syncthreads();
   // 3. one thread per row: SQ and |Q[t]|
-  uint64_t key = 0u;  // rows past the chunk sort last
+  uint64_t key = 0u;  // rows past the queries sort last
   {
     const int t = tid;
-    if (t < BCP) {
+    if (t < n) {
       float dot4[4] = {0.f, 0.f, 0.f, 0.f}, qq4[4] = {0.f, 0.f, 0.f, 0.f};
       const uint4* row = reinterpret_cast<const uint4*>(qs + (size_t)t * 256);
 #pragma unroll
@@ -217,11 +218,13 @@ qsel_fast_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
     sh.lists[0][lane] = m;
   }
   __syncthreads();
-  // 5. normalise the winners (thread = rank i, chunk cc), rank order
+  // 5. normalise the winners (thread = rank i, chunk cc), rank order. Ranks that a
+  // padded chunk has no query for repeat rank 0 (the scores' maximum over ranks
+  // stays what it is); without any query no key is scored.
   {
     const int i = tid >> 4, cc = tid & 15;
-    if (i < NQ) {
-      const int t = (int)(~(uint32_t)sh.lists[0][i]);
+    if (i < NQ && n > 0) {
+      const int t = (int)(~(uint32_t)sh.lists[0][i < n ? i : 0]);
       const uint4 raw = reinterpret_cast<const uint4*>(qs + (size_t)t * 256)[cc ^ (t & 15)];
       const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&raw);
       const float nrm = normalize ? sh.nrm[t] : 1.f;
@@ -231,7 +234,9 @@ qsel_fast_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int64_t s
         sh.qhat[i][cc * 8 + 2 * u] = f.x / nrm;
         sh.qhat[i][cc * 8 + 2 * u + 1] = f.y / nrm;
       }
-      if (cc == 0 && q_idx != nullptr) q_idx[((int64_t)bi * nq + h) * NQ + i] = t;
+      if (cc == 0 && q_idx != nullptr) q_idx[((int64_t)bi * nq + h) * NQ + i] = i < n ? t : -1;
+    } else if (i < NQ && cc == 0 && q_idx != nullptr) {
+      q_idx[((int64_t)bi * nq + h) * NQ + i] = -1;
     }
   }
   // 6. the group mean over the cluster's G heads
@@ -300,9 +305,9 @@ constexpr int Q1_THREADS = 128;
 constexpr int Q1_MAX_G = 32;
 
 __global__ void __launch_bounds__(Q1_THREADS)
-qsel_one_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int nq, int G, int32_t* __restrict__ q_idx,
-                float* __restrict__ Qg, bf16* __restrict__ Qg_hilo, uint32_t* __restrict__ hist,
-                int* __restrict__ status, int normalize) {
+qsel_one_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int nq, int G,
+                const int32_t* __restrict__ new_len, int32_t* __restrict__ q_idx, float* __restrict__ Qg,
+                bf16* __restrict__ Qg_hilo, uint32_t* __restrict__ hist, int* __restrict__ status, int normalize) {
   __shared__ __align__(16) float qhat[Q1_MAX_G][QF_D];
   const int j = blockIdx.x, bi = blockIdx.y, nkv = gridDim.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -316,7 +321,7 @@ qsel_one_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int nq, in
     const float qq = warp_sum((f[0] * f[0] + f[1] * f[1]) + (f[2] * f[2] + f[3] * f[3]));
     const float nrm = normalize ? fmaxf(sqrtf(qq), 1e-12f) : 1.f;
     reinterpret_cast<float4*>(qhat[g])[lane] = make_float4(f[0] / nrm, f[1] / nrm, f[2] / nrm, f[3] / nrm);
-    if (lane == 0 && q_idx != nullptr) q_idx[(int64_t)bi * nq + h] = 0;
+    if (lane == 0 && q_idx != nullptr) q_idx[(int64_t)bi * nq + h] = live_queries(new_len, bi, 1) - 1;
   }
   __syncthreads();
   const int64_t row = (int64_t)bi * nkv + j;
@@ -339,12 +344,12 @@ qsel_one_kernel(const bf16* __restrict__ Q, int64_t sQb, int64_t sQh, int nq, in
 
 cudaError_t launch_qsel_group_fast(Strided Q, int b, int nq, int nkv, int BCP, int NQ, int32_t* q_idx, float* Qg,
                                    uint16_t* Qg_hilo, uint32_t* hist, int* status, bool normalize,
-                                   cudaStream_t stream) {
+                                   cudaStream_t stream, const int32_t* new_len) {
   const int G = nq / nkv;
   if (BCP == 1 && NQ == 1 && G >= 1 && G <= Q1_MAX_G && b <= 65535) {
     qsel_one_kernel<<<dim3(nkv, b), Q1_THREADS, 0, stream>>>(static_cast<const bf16*>(Q.data), Q.sb, Q.sh, nq, G,
-                                                             q_idx, Qg, reinterpret_cast<bf16*>(Qg_hilo), hist,
-                                                             status, (int)normalize);
+                                                             new_len, q_idx, Qg, reinterpret_cast<bf16*>(Qg_hilo),
+                                                             hist, status, (int)normalize);
     return cudaGetLastError();
   }
   if (BCP < 1 || BCP > QF_MAX_BCP || NQ < 1 || NQ > QF_MAX_NQ || NQ > BCP || G < 1 || G > QF_MAX_G)
@@ -368,7 +373,7 @@ cudaError_t launch_qsel_group_fast(Strided Q, int b, int nq, int nkv, int BCP, i
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, qsel_fast_kernel, static_cast<const bf16*>(Q.data), Q.sb, Q.sh, Q.st, nq, BCP,
-                            NQ, q_idx, Qg, reinterpret_cast<bf16*>(Qg_hilo), hist, status, (int)normalize);
+                            NQ, new_len, q_idx, Qg, reinterpret_cast<bf16*>(Qg_hilo), hist, status, (int)normalize);
 }
 
 }  // namespace quoka

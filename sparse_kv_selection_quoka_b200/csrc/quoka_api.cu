@@ -537,6 +537,65 @@ CacheAttnWs cache_attn_ws(int64_t b, int64_t nq, int64_t nkv, int64_t d, int64_t
   return w;
 }
 
+// Steps (a)-(e) over the cache; new_len: null, or the queries of a padded chunk.
+quoka_status run_cache_select(const quoka_tensor* Q, const int32_t* new_len, const quoka_cache* cache, int max_len,
+                              int NQ, int BSA, int32_t* kv_idx, int32_t* kv_count, int32_t* q_idx, float* s_agg,
+                              void* ws, size_t ws_bytes, void* stream) {
+  quoka::CacheScoreArgs a = {};
+  quoka_status st = validate_cache(cache, &a.c);
+  if (st != QUOKA_OK) return st;
+  if (Q == nullptr || (Q->dtype != QUOKA_F32 && Q->dtype != QUOKA_BF16)) return QUOKA_ERR_INVALID_ARG;
+  int64_t qs[4] = {cache->b, -1, -1, cache->d};
+  if (!check_tensor(Q, Q->dtype, qs)) return QUOKA_ERR_INVALID_ARG;
+  const int b = cache->b, nkv = cache->nkv, d = cache->d;
+  if (qs[1] < 1 || qs[2] < 1 || qs[1] % nkv != 0 || NQ < 1 || NQ > qs[2] || BSA < 0) return QUOKA_ERR_INVALID_ARG;
+  if (max_len < 0 || max_len > cache_room(cache) || kv_count == nullptr) return QUOKA_ERR_INVALID_ARG;
+  if (qs[1] > kMaxHeads || qs[2] > kMaxBCP || max_len > quoka::topk_max_T()) return QUOKA_ERR_UNSUPPORTED;
+  const int nq = (int)qs[1], BCP = (int)qs[2], bsa_eff = std::min(BSA, max_len);
+  if (bsa_eff > 0 && kv_idx == nullptr) return QUOKA_ERR_INVALID_ARG;
+  const WsLayout L = ws_layout(b, nq, nkv, d, max_len, NQ, bsa_eff, false);
+  st = check_ws(ws, ws_bytes, L.select_total);
+  if (st != QUOKA_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const bool bf = Q->dtype == QUOKA_BF16;
+  float* qg = at<float>(ws, L.qgroup);
+  int32_t* qidx = q_idx != nullptr ? q_idx : at<int32_t>(ws, L.qidx);
+  a.status = at<int>(ws, L.status);
+  a.hist = at<uint32_t>(ws, L.hist);
+  // (the status words and the histogram are cleared by the kernel that makes the group means)
+  cudaError_t e = cudaErrorNotSupported;
+  // The fused query select takes an SM per query head for any chunk length: with
+  // more heads than one round holds, short chunks are faster through the
+  // general kernels (whole call, 1000 keys, 16 sequences x 32 heads: 16 tokens 33.2
+  // us against 41.9 fused, 64 38.4 and 42.1, 128 47.0 and 41.9; 1 x 32 heads: 14.6
+  // both at 16, 19.5 and 14.7 at 128).
+  const bool fused = BCP == 1 || BCP > 64 || (int64_t)b * nq <= 128;
+  if (bf && d == 128 && fused)
+    e = quoka::launch_qsel_group_fast(strided(Q), b, nq, nkv, BCP, NQ, qidx, qg, nullptr, a.hist, a.status, true, cs,
+                                      new_len);
+  if (e == cudaErrorNotSupported) {
+    e = quoka::launch_qsel(bf, d, strided(Q), b, nq, BCP, NQ, at<float>(ws, L.qhat), qidx, true, cs, new_len);
+    if (e != cudaSuccess) return cuda_status(e);
+    e = quoka::launch_qgroup(d, at<float>(ws, L.qhat), b, nq, nkv, NQ, qg, nullptr, a.hist, a.status, cs);
+  }
+  if (e != cudaSuccess) return cuda_status(e);
+  a.b = b;
+  a.max_len = max_len;
+  a.Qg = qg;
+  a.NQ = NQ;
+  a.new_len = new_len;
+  a.BCP = BCP;
+  a.S_agg = s_agg != nullptr ? s_agg : at<float>(ws, L.sagg);
+  if (max_len > 0) {
+    e = quoka::launch_cache_score(d, a, cs);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  if (bsa_eff > 0)
+    return cuda_status(quoka::launch_topk(a.S_agg, b, nkv, max_len, bsa_eff, a.hist, kv_idx, kv_count, a.status, true,
+                                          cs, cache->seq_len, new_len));
+  return cudaMemsetAsync(kv_count, 0, sizeof(int32_t) * b * nkv, cs) == cudaSuccess ? QUOKA_OK : QUOKA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -812,56 +871,15 @@ quoka_status quoka_cache_select(const quoka_tensor* Q, const quoka_cache* cache,
                                 int32_t* kv_idx, int32_t* kv_count, int32_t* q_idx, float* s_agg, void* ws,
                                 size_t ws_bytes, void* stream) {
   quoka::NvtxRange nvtx_range("quoka_cache_select");
-  quoka::CacheScoreArgs a = {};
-  quoka_status st = validate_cache(cache, &a.c);
-  if (st != QUOKA_OK) return st;
-  if (Q == nullptr || (Q->dtype != QUOKA_F32 && Q->dtype != QUOKA_BF16)) return QUOKA_ERR_INVALID_ARG;
-  int64_t qs[4] = {cache->b, -1, -1, cache->d};
-  if (!check_tensor(Q, Q->dtype, qs)) return QUOKA_ERR_INVALID_ARG;
-  const int b = cache->b, nkv = cache->nkv, d = cache->d;
-  if (qs[1] < 1 || qs[2] < 1 || qs[1] % nkv != 0 || NQ < 1 || NQ > qs[2] || BSA < 0) return QUOKA_ERR_INVALID_ARG;
-  if (max_len < 0 || max_len > cache_room(cache) || kv_count == nullptr) return QUOKA_ERR_INVALID_ARG;
-  if (qs[1] > kMaxHeads || qs[2] > kMaxBCP || max_len > quoka::topk_max_T()) return QUOKA_ERR_UNSUPPORTED;
-  const int nq = (int)qs[1], BCP = (int)qs[2], bsa_eff = std::min(BSA, max_len);
-  if (bsa_eff > 0 && kv_idx == nullptr) return QUOKA_ERR_INVALID_ARG;
-  const WsLayout L = ws_layout(b, nq, nkv, d, max_len, NQ, bsa_eff, false);
-  st = check_ws(ws, ws_bytes, L.select_total);
-  if (st != QUOKA_OK) return st;
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const bool bf = Q->dtype == QUOKA_BF16;
-  float* qg = at<float>(ws, L.qgroup);
-  int32_t* qidx = q_idx != nullptr ? q_idx : at<int32_t>(ws, L.qidx);
-  a.status = at<int>(ws, L.status);
-  a.hist = at<uint32_t>(ws, L.hist);
-  // (the status words and the histogram are cleared by the kernel that makes the group means)
-  cudaError_t e = cudaErrorNotSupported;
-  // The fused query select takes an SM per query head for any chunk length: with
-  // more heads than one round holds, short chunks are faster through the
-  // general kernels (whole call, 1000 keys, 16 sequences x 32 heads: 16 tokens 33.2
-  // us against 41.9 fused, 64 38.4 and 42.1, 128 47.0 and 41.9; 1 x 32 heads: 14.6
-  // both at 16, 19.5 and 14.7 at 128).
-  const bool fused = BCP == 1 || BCP > 64 || (int64_t)b * nq <= 128;
-  if (bf && d == 128 && fused)
-    e = quoka::launch_qsel_group_fast(strided(Q), b, nq, nkv, BCP, NQ, qidx, qg, nullptr, a.hist, a.status, true, cs);
-  if (e == cudaErrorNotSupported) {
-    e = quoka::launch_qsel(bf, d, strided(Q), b, nq, BCP, NQ, at<float>(ws, L.qhat), qidx, true, cs);
-    if (e != cudaSuccess) return cuda_status(e);
-    e = quoka::launch_qgroup(d, at<float>(ws, L.qhat), b, nq, nkv, NQ, qg, nullptr, a.hist, a.status, cs);
-  }
-  if (e != cudaSuccess) return cuda_status(e);
-  a.b = b;
-  a.max_len = max_len;
-  a.Qg = qg;
-  a.NQ = NQ;
-  a.S_agg = s_agg != nullptr ? s_agg : at<float>(ws, L.sagg);
-  if (max_len > 0) {
-    e = quoka::launch_cache_score(d, a, cs);
-    if (e != cudaSuccess) return cuda_status(e);
-  }
-  if (bsa_eff > 0)
-    return cuda_status(quoka::launch_topk(a.S_agg, b, nkv, max_len, bsa_eff, a.hist, kv_idx, kv_count, a.status, true,
-                                          cs, cache->seq_len));
-  return cudaMemsetAsync(kv_count, 0, sizeof(int32_t) * b * nkv, cs) == cudaSuccess ? QUOKA_OK : QUOKA_ERR_CUDA;
+  return run_cache_select(Q, nullptr, cache, max_len, NQ, BSA, kv_idx, kv_count, q_idx, s_agg, ws, ws_bytes, stream);
+}
+
+quoka_status quoka_cache_select_padded(const quoka_tensor* Q, const int32_t* new_len, const quoka_cache* cache,
+                                       int max_len, int NQ, int BSA, int32_t* kv_idx, int32_t* kv_count,
+                                       int32_t* q_idx, float* s_agg, void* ws, size_t ws_bytes, void* stream) {
+  quoka::NvtxRange nvtx_range("quoka_cache_select_padded");
+  if (new_len == nullptr) return QUOKA_ERR_INVALID_ARG;
+  return run_cache_select(Q, new_len, cache, max_len, NQ, BSA, kv_idx, kv_count, q_idx, s_agg, ws, ws_bytes, stream);
 }
 
 quoka_status quoka_cache_gather(const quoka_cache* cache, int max_len, const int32_t* kv_idx,

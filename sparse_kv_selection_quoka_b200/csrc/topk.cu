@@ -131,11 +131,18 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// Keys of a row of batch entry bi (row_len null: T).
+__device__ __forceinline__ int64_t keys_of(const int32_t* row_len, const int32_t* new_len, int bi, int64_t T) {
+  if (row_len == nullptr) return T;
+  if (new_len != nullptr && __ldg(new_len + bi) <= 0) return 0;
+  return max((int64_t)0, min((int64_t)__ldg(row_len + bi), T));
+}
+
 template <bool CLUSTER>
 __global__ void __launch_bounds__(TOPK_THREADS)
 topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const uint32_t* __restrict__ ghist,
-            const int32_t* __restrict__ row_len, int32_t* __restrict__ kv_idx, int32_t* __restrict__ kv_count,
-            const int* __restrict__ status) {
+            const int32_t* __restrict__ row_len, const int32_t* __restrict__ new_len, int32_t* __restrict__ kv_idx,
+            int32_t* __restrict__ kv_count, const int* __restrict__ status) {
   extern __shared__ uint32_t smem_dyn[];
   uint32_t* keys = smem_dyn;          // [slice]: this CTA's keys
   uint32_t* glist = smem_dyn + slice;  // [TOPK_LIST_MAX]: all ranks' candidates, in rank order
@@ -150,10 +157,10 @@ topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const ui
   const int64_t row = (int64_t)bi * nkv + j;
   const float* Sr = S + row * T;
   const int64_t lo = (int64_t)c * slice;
-  // the row's keys (per batch entry when row_len is given: an input of the
-  // call, written by no kernel of it) and picks; every CTA of a row's cluster
+  // the row's keys (per batch entry when row_len is given: lengths are inputs of
+  // the call, written by no kernel of it) and picks; every CTA of a row's cluster
   // leaves here together when it has none
-  const int64_t Tr = row_len != nullptr ? max((int64_t)0, min((int64_t)__ldg(row_len + bi), T)) : T;
+  const int64_t Tr = keys_of(row_len, new_len, bi, T);
   const int take_n = (int)min((int64_t)bsa, Tr);
   const int n = (int)max((int64_t)0, min((int64_t)slice, Tr - lo));
   const int n_round = (n + TOPK_THREADS - 1) / TOPK_THREADS * TOPK_THREADS;
@@ -616,14 +623,14 @@ constexpr int TOPK_SMALL_THREADS = 256;
 template <int KPT>
 __global__ void __launch_bounds__(TOPK_SMALL_THREADS)
 topk_small_kernel(const float* __restrict__ S, int64_t T, int bsa, const int32_t* __restrict__ row_len,
-                  int32_t* __restrict__ kv_idx, int32_t* __restrict__ kv_count, const int* __restrict__ status) {
+                  const int32_t* __restrict__ new_len, int32_t* __restrict__ kv_idx, int32_t* __restrict__ kv_count, const int* __restrict__ status) {
   constexpr int WARPS = TOPK_SMALL_THREADS / 32;
   __shared__ uint2 counts[2][WARPS];
   __shared__ uint32_t wsum[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int j = blockIdx.x, bi = blockIdx.y, nkv = gridDim.x;
   const int64_t row = (int64_t)bi * nkv + j;
-  const int n = row_len != nullptr ? (int)max((int64_t)0, min((int64_t)__ldg(row_len + bi), T)) : (int)T;
+  const int n = (int)keys_of(row_len, new_len, bi, T);
   const int take = min(bsa, n);
   pdl_trigger();
   pdl_wait();  // the scores come from the previous kernel
@@ -724,8 +731,8 @@ struct TopkHistShared {
 template <int KPT, bool CLUSTER>
 __global__ void __launch_bounds__(TOPK_HIST_THREADS)
 topk_hist_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const uint32_t* __restrict__ ghist,
-                 const int32_t* __restrict__ row_len, int32_t* __restrict__ kv_idx, int32_t* __restrict__ kv_count,
-                 const int* __restrict__ status) {
+                 const int32_t* __restrict__ row_len, const int32_t* __restrict__ new_len,
+                 int32_t* __restrict__ kv_idx, int32_t* __restrict__ kv_count, const int* __restrict__ status) {
   constexpr int WARPS = TOPK_HIST_THREADS / 32;
   constexpr int PART = CLUSTER ? 4 * TOPK_DIRECT / TOPK_MAX_CLUSTER : TOPK_DIRECT;  // of a rank
   __shared__ TopkHistShared sh;
@@ -735,8 +742,8 @@ topk_hist_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, con
   const uint32_t lower = (1u << lane) - 1u;
   const int j = blockIdx.y, bi = blockIdx.z, nkv = gridDim.y;
   const int64_t row = (int64_t)bi * nkv + j;
-  // (row_len: an input of the call; every CTA of the row leaves here together)
-  const int Tr = row_len != nullptr ? (int)max((int64_t)0, min((int64_t)__ldg(row_len + bi), T)) : (int)T;
+  // (lengths are inputs of the call; every CTA of the row leaves here together)
+  const int Tr = (int)keys_of(row_len, new_len, bi, T);
   const int take = min(bsa, Tr), lo = c * slice, n = max(0, min(slice, Tr - lo));
   pdl_trigger();
   if (take == 0) {
@@ -997,7 +1004,7 @@ int64_t topk_max_T() { return (int64_t)TOPK_MAX_CLUSTER * TOPK_MAX_SLICE; }
 
 cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, const uint32_t* hist,
                         int32_t* kv_idx, int32_t* kv_count, int* status, bool pdl, cudaStream_t stream,
-                        const int32_t* row_len) {
+                        const int32_t* row_len, const int32_t* new_len) {
   // (every wait in the kernel is a hardware barrier phase that all threads
   // reach; `status` is only read, to skip the select after an earlier fault)
   if (bsa <= 0 || T <= 0 || bsa > T || T > topk_max_T()) return cudaErrorInvalidValue;
@@ -1013,7 +1020,7 @@ cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, small, S_agg, T, bsa, row_len, kv_idx, kv_count, static_cast<const int*>(status));
+    return cudaLaunchKernelEx(&cfg, small, S_agg, T, bsa, row_len, new_len, kv_idx, kv_count, static_cast<const int*>(status));
   }
   int C = (int)((T + TOPK_SLICE_TARGET - 1) / TOPK_SLICE_TARGET);
   // no more CTAs than SMs while the slices allow it: two on an SM only slow
@@ -1040,7 +1047,7 @@ cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, 
     cfg.numAttrs = C > 1 ? 2 : 1;
     auto* kern = part <= TOPK_HIST_SLICE / 2 ? (C > 1 ? topk_hist_kernel<8, true> : topk_hist_kernel<8, false>)
                                              : (C > 1 ? topk_hist_kernel<16, true> : topk_hist_kernel<16, false>);
-    return cudaLaunchKernelEx(&cfg, kern, S_agg, T, bsa, part, hist, row_len, kv_idx, kv_count,
+    return cudaLaunchKernelEx(&cfg, kern, S_agg, T, bsa, part, hist, row_len, new_len, kv_idx, kv_count,
                               static_cast<const int*>(status));
   }
   const int slice = (int)((T + C - 1) / C);
@@ -1072,7 +1079,7 @@ cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, 
   }
   cfg.attrs = attr;
   cfg.numAttrs = na;
-  return cudaLaunchKernelEx(&cfg, kern, S_agg, T, bsa, slice, hist, row_len, kv_idx, kv_count,
+  return cudaLaunchKernelEx(&cfg, kern, S_agg, T, bsa, slice, hist, row_len, new_len, kv_idx, kv_count,
                             static_cast<const int*>(status));
 }
 

@@ -453,6 +453,95 @@ def test_select(k):
                 assert (want[i][j][best] >= last - 2 * tol).all()
 
 
+PADDED = [
+    # lens, new, nkv, nq, d, page, BCP, NQ, BSA, dtype, what the rows of padding hold
+    ([300, 47, 129, 200], [33, 1, 0, 100], 2, 8, 128, 64, 100, 4, 50, "bf16", 0.0),
+    ([300, 47, 129, 200], [33, 1, 0, 100], 2, 8, 128, 64, 100, 4, 50, "bf16", float("nan")),
+    ([90, 31, 0, 77], [1, 0, 1, 1], 2, 6, 128, 32, 1, 1, 20, "bf16", float("nan")),
+    ([500, 400, 300, 10], [129, 20, 3, 200], 1, 3, 64, 16, 200, 30, 64, "f32", 0.0),     # a cluster a head
+    ([260, 250], [3990, 2], 1, 2, 128, 128, 4000, 5, 40, "f32", float("inf")),          # rows from global memory
+    ([1500, 130, 64], [90, 16, 5], 2, 4, 128, 64, 90, 17, 200, "bf16", -30.0),          # group means in pieces
+    ([3000, 2500, 2900], [0, 7, 12], 2, 4, 64, 32, 12, 3, 600, "bf16", 0.0),            # the larger top-k
+    ([70000, 66000], [3, 0], 1, 1, 64, 128, 5, 2, 300, "f32", 1e30),                    # the largest
+]
+
+
+@gpu
+@pytest.mark.parametrize("k", range(len(PADDED)))
+def test_select_of_a_padded_chunk(k):
+    """Rows behind new_len are no queries, whatever they hold: the choice is that
+    of the sequence's own chunk, the scores those of the chosen (the bounds of
+    test_select), and a sequence without queries selects nothing."""
+    lens, new, nkv, nq, d, page, BCP, NQ, BSA, dt, fill = PADDED[k]
+    b, max_len = len(lens), max(lens)
+    c = Pages(lens, lens, nkv, d, page, 160 + k)
+    Q = (randn(170 + k, b, nq, BCP, d) + 1.0).to(TYPES[dt])
+    for i, m in enumerate(new):
+        Q[i, :, m:] = fill
+    kv_idx = torch.full((b, nkv, min(BSA, max_len)), -7, dtype=torch.int32, device="cuda")
+    s_agg = torch.full((b, nkv, max_len), 5.0, device="cuda")
+    size = q().quoka_select_workspace_size(b, nq, nkv, d, max_len, BCP, NQ, BSA, TYPES[dt])
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    idx, count, q_idx, s = q().quoka_cache_select(Q.cuda(), c.cuda(), max_len, NQ, BSA, kv_idx=kv_idx, s_agg=s_agg, ws=ws,
+                                                  new_len=torch.tensor(new, dtype=torch.int32).cuda(), want_q_idx=True)
+    assert q().quoka_get_device_status(ws) == 0
+    tol = (2 * d + 16) * 2.0**-22 + (2.0**-16 if NQ > 24 else 0.0)
+    for i, (L, m) in enumerate(zip(lens, new)):
+        take = min(BSA, L) if m else 0
+        assert (count[i] == take).all() and (idx[i, :, take:] == -7).all()
+        keep = min(NQ, m)
+        assert (q_idx[i, :, keep:] == -1).all()
+        if m == 0:
+            assert (s[i] == 5.0).all()
+            continue
+        own = Q[i:i + 1, :, :m]
+        SQ = -torch.nn.functional.cosine_similarity(own.double(), own.double().mean(2, keepdim=True), dim=-1, eps=1e-300)
+        at = q_idx[i:i + 1, :, :keep].cpu()
+        P.check_q_idx(at.numpy(), SQ.numpy(), SQ.sort(dim=-1, descending=True, stable=True).indices[..., :keep].numpy())
+        one = Pages.__new__(Pages)
+        one.__dict__.update(c.__dict__, table=c.table[i:i + 1], lens=lens[i:i + 1])
+        want = select_oracle(one, own, at)[0]
+        got = s[i].double().cpu()
+        assert (got[:, :L] - want).abs().max() <= tol if L else True
+        assert (got[:, L:] == 5.0).all()
+        for j in range(nkv):
+            best = got[j, :L].sort(descending=True, stable=True).indices[:take].sort().values
+            assert torch.equal(idx[i, j, :take].cpu().long(), best)
+
+
+@gpu
+def test_padded_chunk_in_a_graph_and_out_of_range():
+    """A captured selection follows new_len; a count that is none latches."""
+    m, b, BCP = q(), 3, 70
+    c = Pages([400, 300, 350], [400, 300, 350], 2, 128, 32, 9).cuda()
+    Q = randn(8, b, 4, BCP, 128).to(torch.bfloat16).cuda()
+    new = torch.tensor([70, 70, 70], dtype=torch.int32).cuda()
+    ws = torch.zeros(m.quoka_select_workspace_size(b, 4, 2, 128, 400, BCP, 4, 50, Q.dtype), dtype=torch.uint8, device="cuda")
+    idx, cnt = torch.zeros(b, 2, 50, dtype=torch.int32, device="cuda"), torch.zeros(b, 2, dtype=torch.int32, device="cuda")
+    call = lambda: m.quoka_cache_select(Q, c, 400, 4, 50, new_len=new, kv_idx=idx, kv_count=cnt, ws=ws)
+    call()
+    plain, _, _, _ = m.quoka_cache_select(Q, c, 400, 4, 50)
+    assert torch.equal(idx, plain)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for counts in ([70, 5, 0], [1, 69, 33]):
+        new.copy_(torch.tensor(counts, dtype=torch.int32))
+        Q.normal_()
+        idx.fill_(-7)
+        g.replay()
+        got = idx.clone(), cnt.clone()
+        idx.fill_(-7)
+        call()
+        assert torch.equal(got[0], idx) and torch.equal(got[1], cnt) and m.quoka_get_device_status(ws) == 0
+        assert cnt.tolist() == [[50 if n else 0] * 2 for n in counts]
+    for counts in ([71, 5, 5], [5, 5, -1]):
+        new.copy_(torch.tensor(counts, dtype=torch.int32))
+        call()
+        assert m.quoka_get_device_status(ws) == 6 and (cnt == 0).all()
+
+
 @gpu
 def test_select_ties_go_to_the_lower_index():
     c = Pages([400], [400], 1, 128, 32, 3)
@@ -651,6 +740,51 @@ def test_serving_loop(dt, d):
         assert torch.equal(dev.k_scale.cpu(), c.k_scale) and torch.equal(dev.v_scale.cpu(), c.v_scale)
         dev.seq_len += nl
         c.lens = [n + m for n, m in zip(c.lens, new)]
+
+
+@gpu
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f32", 64)])
+def test_serving_loop_selects_for_its_own_tokens(dt, d):
+    """Padded chunks through append, select and attention: every sequence's
+    selection is that of its own tokens alone, by the definition in 64 bits (the
+    scores' bound of test_select)."""
+    t, nkv, nq, page, NQ, BSA = TYPES[dt], 2, 6, 16, 4, 24
+    c = Pages([0, 0, 0], [160, 160, 160], nkv, d, page, 12)
+    dev = c.cuda(torch.uint8)
+    cos, sin = angles(160, d)
+    for k, (BCP, new) in enumerate([(70, [70, 41, 0]), (40, [33, 40, 1]), (40, [2, 0, 40]), (1, [1, 0, 1]), (5, [5, 3, 1])]):
+        K, V, Q = (randn(300 + 3 * k + u, 3, h, BCP, d).to(t) for u, h in enumerate((nkv, nkv, nq)))
+        nl = torch.tensor(new, dtype=torch.int32).cuda()
+        Kr, Qr = q().quoka_cache_append(dev, K.cuda(), V.cuda(), Q.cuda(), cos.cuda(), sin.cuda(), new_len=nl, want_Kr=True)
+        max_len = max(1, max(c.lens))
+        n = min(NQ, BCP)
+        idx, cnt, at, _ = q().quoka_cache_select(Qr, dev, max_len, n, BSA, new_len=nl, want_q_idx=True)
+        O, lse = q().quoka_cache_attn(Qr, dev, max_len, idx, cnt, Kr, V.cuda(), want_lse=True)
+        want = attention(c, Qr.cpu(), Kr.cpu(), V, idx.cpu(), cnt.cpu())
+        tol = (2 * d + 16) * 2.0**-22
+        for i, m in enumerate(new):
+            take = min(BSA, c.lens[i]) if m else 0
+            assert (cnt[i] == take).all()
+            if m == 0:
+                continue
+            own, keep = Qr[i:i + 1, :, :m].cpu(), min(n, m)
+            assert ((at[i, :, :keep] >= 0) & (at[i, :, :keep] < m)).all() and (at[i, :, keep:] == -1).all()
+            SQ = -torch.nn.functional.cosine_similarity(own.double(), own.double().mean(2, keepdim=True), dim=-1, eps=1e-300)
+            P.check_q_idx(at[i:i + 1, :, :keep].cpu().numpy(), SQ.numpy(),
+                          SQ.sort(dim=-1, descending=True, stable=True).indices[..., :keep].numpy())
+            one = Pages.__new__(Pages)
+            one.__dict__.update(c.__dict__, table=c.table[i:i + 1], lens=c.lens[i:i + 1])
+            true = select_oracle(one, own, at[i:i + 1, :, :keep].cpu())[0]
+            for j in range(nkv):
+                pick = idx[i, j, :take].cpu().long()
+                assert len(set(pick.tolist())) == take
+                if take:
+                    assert (true[j][pick] >= true[j].sort(descending=True).values[take - 1] - 2 * tol).all()
+            check_attention(O[i:i + 1, :, :m], lse[i:i + 1, :, :m], [w[i:i + 1, :, :m] for w in want], dt, d,
+                            idx.shape[2] + BCP, nq // nkv * BCP <= 32)
+        append(c, K, V, cos, sin, False, new)
+        dev.seq_len += nl
+        c.lens = [n_ + m for n_, m in zip(c.lens, new)]
 
 
 @gpu
@@ -1001,6 +1135,23 @@ def test_calls_refuse_bad_tensors(lib):  # noqa: F811
                  lambda: m.quoka_cache_attn(Q, c, 10, lse=torch.zeros(3, 4, 7, dtype=torch.float64))):
         with pytest.raises(TypeError):
             call()
+
+
+def test_padded_select_refuses_bad_counts(lib):  # noqa: F811
+    m, c, Q = q(), cpu_cache(), torch.zeros(3, 4, 7, 64)
+    for new in (torch.zeros(2, dtype=torch.int32), torch.zeros(3, 1, dtype=torch.int32), torch.zeros(6, dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError, match="new_len"):
+            m.quoka_cache_select(Q, c, 10, 1, 1, new_len=new)
+    for new in (torch.zeros(3), [1, 2, 3]):
+        with pytest.raises(TypeError, match="new_len"):
+            m.quoka_cache_select(Q, c, 10, 1, 1, new_len=new)
+    B, buf, ws = ctypes.byref, ctypes.c_void_p(0x200000), ctypes.c_void_p(0x100000)
+
+    def select(new=buf, max_len=100, NQ=2, ws=ws, n=1 << 30, c=_cache()):
+        return lib.quoka_cache_select_padded(B(_view((1, 4, 7, 128))), new, B(c), max_len, NQ, 10, buf, buf, None, None, ws, n, None)
+
+    assert select(new=None) == 1 and select(max_len=129) == 1 and select(NQ=8) == 1 and select(NQ=0) == 1
+    assert select(ws=None) == 3 and select(n=256) == 3 and select(c=_cache(page=24)) == 2 and select(c=_cache(k=None)) == 1
 
 
 def _cache(**kw):
