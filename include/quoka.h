@@ -405,8 +405,11 @@ typedef struct {
   const int32_t* seq_len;
 } quoka_cache;
 
-/* Option of quoka_cache_append: pairs are neighbouring columns. */
+/* Options of quoka_cache_append: pairs are neighbouring columns; rows of Kr and
+ * Qr whose tokens are left out become zeros (without it they stay as they were).
+ * Bit 1 is not used. */
 #define QUOKA_ROTATE_NEIGHBOURS 1u
+#define QUOKA_ZERO_REST 4u
 
 /* Writes a chunk's keys and values behind the tokens each sequence holds,
  * rotating the keys (and the chunk's queries) by their positions.
@@ -424,7 +427,8 @@ typedef struct {
  *   the codes the page holds are brought to it. Codes are rounded to nearest
  *   even and saturate at 448 (infinities too); NaN stays NaN.
  *   new_len (b) int32 or NULL: new tokens of each sequence, in [0, BCP] (NULL:
- *   BCP each). Tokens past it have no effect and are not written, in any output.
+ *   BCP each). Tokens past it have no effect and are not written, in any output
+ *   (QUOKA_ZERO_REST: but as zeros in Kr and Qr).
  *   Kr (b, nkv, BCP, d) or NULL, Qr (b, nq, BCP, d, with Q): out, contiguous,
  *   the rotated keys and queries rounded to their dtype. They must not
  *   overlap K, V or Q (QUOKA_ERR_INVALID_ARG).
@@ -432,7 +436,8 @@ typedef struct {
  * is done. A page that is written belongs to one sequence and one column.
  * Tokens whose position lies past the page table or the angles, a new_len
  * outside [0, BCP] and pages outside the cache latch QUOKA_ERR_BOUNDS in `ws`
- * (which may be NULL) and are left out. */
+ * (which may be NULL) and are left out: of the cache, and, but for those of a
+ * page outside it, of Kr and Qr. */
 quoka_status quoka_cache_append(const quoka_cache* cache, const quoka_tensor* K,
                                 const quoka_tensor* V, const quoka_tensor* Q,
                                 const float* cos, const float* sin,

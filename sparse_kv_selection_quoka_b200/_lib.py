@@ -662,8 +662,9 @@ def quoka_cache_append(cache, K, V, Q=None, cos=None, sin=None, *, interleaved=F
     (npos, rot / 2) float32 (None: no rotation; interleaved: the pairs are
     neighbouring columns). Returns (Kr, Qr): the rotated keys (None unless
     given or wanted) and the rotated Q (b, nq, BCP, d) (None without Q), in
-    their dtype. Tokens from new_len (b) int32 on (None: BCP) are left out;
-    their rows of Kr and Qr stay as they were (zeros when made here).
+    their dtype. Tokens from new_len (b) int32 on (None: BCP), and those that
+    the page table or the angles have no room for, are left out; their rows of
+    Kr and Qr stay as they were (zeros when made here).
     cache.seq_len stays: advance it when the chunk is done."""
     if stream is not None:
         with _on(cache, stream):

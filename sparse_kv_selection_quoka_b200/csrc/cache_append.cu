@@ -119,7 +119,7 @@ __device__ __forceinline__ void rotate(const RotArgs& r, const float (&cs)[8], c
   }
 }
 
-// New tokens of sequence bi: positions [start, end). Negative lengths, counts
+// New tokens of sequence bi: positions [start, end), end <= start + BCP. Negative lengths, counts
 // out of range, and tokens past the cache or the angle table, are latched and
 // left out.
 __device__ __forceinline__ void new_range(const CacheAppendArgs& a, int bi, int* start, int* end) {
@@ -169,14 +169,23 @@ __global__ void __launch_bounds__(NT) cache_append_kernel(const CacheAppendArgs 
       }
     int start, end;
     new_range(a, bi, &start, &end);
-    if (start + t >= end) return;
+    T* o = static_cast<T*>(a.Qr) + ((int64_t)bi * a.nq * a.BCP + t) * D;
+    if (start + t >= end) {
+      if (a.zero_rest != 0) {
+        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int h = h0; h < min(h0 + kQHeads, a.nq); ++h) {
+          store8(o + (int64_t)h * a.BCP * D + 8 * c0, z);
+          store8(o + (int64_t)h * a.BCP * D + 8 * c1, z);
+        }
+      }
+      return;
+    }
     const bool turn = 16 * i < a.rot;
     float cs[8], sn[8];
     if (turn) {
       load8(a.cos + (int64_t)(start + t) * half + 8 * i, cs);
       load8(a.sin + (int64_t)(start + t) * half + 8 * i, sn);
     }
-    T* o = static_cast<T*>(a.Qr) + ((int64_t)bi * a.nq * a.BCP + t) * D;
 #pragma unroll
     for (int k = 0; k < kQHeads; ++k)
       if (h0 + k < a.nq) {
@@ -202,6 +211,15 @@ __global__ void __launch_bounds__(NT) cache_append_kernel(const CacheAppendArgs 
   const int col = (start >> a.c.page_log2) + pt;
   const int p0 = col << a.c.page_log2;
   const int t0 = max(start, p0), t1 = min(end, p0 + (1 << a.c.page_log2));
+  if (a.zero_rest != 0 && !is_v && a.Kr != nullptr) {  // rows of tokens at this page's positions that are left out
+    const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int z1 = min(start + a.BCP, p0 + (1 << a.c.page_log2));
+    for (int t = max(end, p0) + rr; t < z1; t += RPP) {
+      T* o = static_cast<T*>(a.Kr) + (((int64_t)bi * nkv + j) * a.BCP + (t - start)) * D + 16 * i;
+      store8(o, z);
+      store8(o + 8, z);
+    }
+  }
   if (t0 >= t1) return;  // (the same for the whole CTA)
   const int pid = __ldcg(a.c.page_table + (int64_t)bi * a.c.table_stride + col);
   const Strided X = is_v ? a.V : a.K;

@@ -196,18 +196,22 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* wp = call.workspace(tensor(a[12], "ws"), &wn);
     call.on_gpu();
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)call.dev);
+    // Rows that are left out are zeros in what is made here, and stay as they are in
+    // what was given: the kernel's option acts on both.
+    const bool given = Kr != nullptr || Qr != nullptr;
     Tensor made_k, made_q;
     if (Kr == nullptr && a[11] == Py_True) {
-      made_k = call.make(type, K.sizes(), fresh != nullptr);
+      made_k = call.make(type, K.sizes(), given);
       krp = made_k.data_ptr();
     }
     if (Qr == nullptr && Q != nullptr) {
-      made_q = call.make(type, Q->sizes(), fresh != nullptr);
+      made_q = call.make(type, Q->sizes(), given);
       qrp = made_q.data_ptr();
     }
+    const uint32_t flags = (a[7] == Py_True ? QUOKA_ROTATE_NEIGHBOURS : 0u) | (given ? 0u : QUOKA_ZERO_REST);
     const quoka_status st =
         g_append(&c, &kv, &vv, Q ? &qv : nullptr, cp, sp, npos, (int)(2 * half),
-                 a[7] == Py_True ? QUOKA_ROTATE_NEIGHBOURS : 0u, np, krp, qrp, wp, wn, call.stream());
+                 flags, np, krp, qrp, wp, wn, call.stream());
     if (st != QUOKA_OK) return PyLong_FromLong(st);
     return Py_BuildValue("(NN)", out(a[9], made_k), out(a[10], made_q));
   });

@@ -201,6 +201,7 @@ struct CacheAppendArgs {
   int limit;               // positions below it can be appended
   void* Kr;                // (b, nkv, BCP, d) or null
   void* Qr;                // (b, nq, BCP, d) or null (then Q is not read)
+  int zero_rest;           // 1: rows of Kr and Qr whose tokens are left out become zeros
   int* status;
 };
 cudaError_t launch_cache_append(bool bf16, int d, const CacheAppendArgs& a, bool pdl, cudaStream_t stream);

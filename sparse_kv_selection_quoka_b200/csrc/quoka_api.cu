@@ -820,7 +820,7 @@ quoka_status quoka_cache_append(const quoka_cache* cache, const quoka_tensor* K,
   quoka::CacheAppendArgs a = {};
   quoka_status st = validate_cache(cache, &a.c);
   if (st != QUOKA_OK) return st;
-  if ((flags & ~QUOKA_ROTATE_NEIGHBOURS) != 0u || K == nullptr || V == nullptr) return QUOKA_ERR_INVALID_ARG;
+  if ((flags & ~(QUOKA_ROTATE_NEIGHBOURS | QUOKA_ZERO_REST)) != 0u || K == nullptr || V == nullptr) return QUOKA_ERR_INVALID_ARG;
   if (K->dtype != QUOKA_F32 && K->dtype != QUOKA_BF16) return QUOKA_ERR_INVALID_ARG;
   int64_t ks[4] = {cache->b, cache->nkv, -1, cache->d};
   if (!check_tensor(K, K->dtype, ks) || !check_tensor(V, K->dtype, ks)) return QUOKA_ERR_INVALID_ARG;
@@ -864,6 +864,7 @@ quoka_status quoka_cache_append(const quoka_cache* cache, const quoka_tensor* K,
   a.limit = rot > 0 ? (int)std::min<int64_t>(cache_room(cache), npos) : cache_room(cache);
   a.Kr = Kr;
   a.Qr = Qr;
+  a.zero_rest = (flags & QUOKA_ZERO_REST) != 0u ? 1 : 0;
   return cuda_status(quoka::launch_cache_append(K->dtype == QUOKA_BF16, cache->d, a, a.status != nullptr, cs));
 }
 

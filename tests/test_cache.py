@@ -320,6 +320,39 @@ def test_append_leaves_out_what_does_not_fit():
 
 
 @gpu
+@pytest.mark.parametrize("dt,page,nq,BCP", [("bf16", 64, 9, 100), ("f32", 16, 3, 45), ("bf16", 128, 4, 1)])
+def test_append_makes_zeros_of_what_is_left_out(dt, page, nq, BCP):
+    """Rows of Kr and Qr made by the call: zeros for tokens past the page table, the
+    angles or new_len and for all of a sequence whose length is none; the rotated
+    rows for the rest. Rows of tensors that were given stay as they were."""
+    m, t, d, nkv = q(), TYPES[dt], 64, 2
+    cols = 3
+    lens = [0, cols * page - 7, cols * page, -3, 10**9, cols * page - BCP]
+    npos = cols * page - 2
+    new = [BCP, BCP, 0, BCP, BCP, max(0, BCP - 3)]
+    cos, sin = angles(npos, d)
+    K, V, Q = (randn(s, len(lens), h, BCP, d).to(t) for s, h in ((1, nkv), (2, nkv), (3, nq)))
+    for counts in (None, new):
+        nl = None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda()
+        for given in ("", "Kr", "Qr"):
+            dev = Pages([1] * 6, [cols * page] * 6, nkv, d, page, 5).cuda(torch.uint8)
+            dev.seq_len.copy_(torch.tensor(lens, dtype=torch.int32))
+            kw = {"Kr": {"Kr": torch.full_like(K, 9.0).cuda()}, "Qr": {"Qr": torch.full_like(Q, 9.0).cuda()}}.get(given, {})
+            up = K.cuda(), V.cuda(), Q.cuda(), cos.cuda(), sin.cuda()
+            dirt = [torch.full(x.shape, float("nan"), dtype=t, device="cuda") for x in (K, Q)]
+            del dirt  # (what the allocator hands out next)
+            Kr, Qr = m.quoka_cache_append(dev, *up, new_len=nl, want_Kr=True, **kw)
+            for i, n in enumerate(lens):
+                fits = max(0, min(BCP, npos - n)) if 0 <= n <= npos else 0
+                live = fits if counts is None else min(fits, counts[i])
+                for name, got, x in (("Kr", Kr, K), ("Qr", Qr, Q)):
+                    want = torch.full_like(x[i], 9.0 if name == given else 0.0)
+                    if live:
+                        want[:, :live] = rotate(x[i, :, :live].float(), cos[n:n + live], sin[n:n + live], False).to(t)
+                    assert torch.equal(got[i].cpu(), want), (counts, given, i, name)
+
+
+@gpu
 def test_append_of_no_tokens_needs_no_angles():
     """A sequence without new tokens may be longer than the table of angles."""
     c = Pages([30, 4], [64, 40], 1, 64, 16, 8)
