@@ -1,23 +1,27 @@
-// Host helper: the driver's tensor-map encoder, fetched once through the
-// runtime (no link-time dependency on libcuda).
+// Host helper: the driver's tensor-map encoder, fetched through the runtime (no
+// link-time dependency on libcuda) at the first call that finds it, whichever
+// thread makes it; a lookup that fails is made again by the next call.
 #pragma once
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace quoka {
 
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_acquire);
+  if (fn == nullptr) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
+        q == cudaDriverEntryPointSuccess) {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+      known.store(fn, std::memory_order_release);
+    }
   }
   return fn;
 }

@@ -2,11 +2,15 @@
 against plain 64-bit forms, their edge cases, their refusals, and the calls
 together as a serving loop makes them."""
 import ctypes
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
 import torch
 
+from sparse_kv_selection_quoka_b200 import build
 from tests import parity as P
 from tests.test_library import _view, lib  # noqa: F401 (lib is a fixture)
 
@@ -1243,3 +1247,91 @@ def test_entry_points_reject_bad_arguments_on_host(lib):  # noqa: F811
     # outputs over inputs
     assert app(Kr=ctypes.c_void_p(0x60000)) == 1 and app(Kr=ctypes.c_void_p(0x60000 + 256)) == 1
     assert app(Q=Q, Qr=ctypes.c_void_p(0x10000)) == 1
+
+
+def test_tensor_map_encoder_is_found_by_every_thread(tmp_path):
+    """First calls from many threads at once, while the driver takes its time to
+    name the encoder: every one of them gets it (a fake of the runtime's lookup;
+    no GPU). A lookup that fails is made again."""
+    cuda = os.path.join(os.path.dirname(os.path.dirname(build.NVCC)), "include")
+    src = tmp_path / "first.cpp"
+    src.write_text(r"""
+#include <atomic>
+#include "tmap.cuh"
+#include <chrono>
+#include <cstdio>
+#include <thread>
+#include <vector>
+static std::atomic<int> lookups{0}, fail{1};
+static CUresult encode(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                       const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                       CUtensorMapL2promotion, CUtensorMapFloatOOBfill) { return CUDA_SUCCESS; }
+extern "C" cudaError_t cudaGetDriverEntryPoint(const char*, void** p, unsigned long long,
+                                               cudaDriverEntryPointQueryResult* q) {
+  ++lookups;
+  std::this_thread::sleep_for(std::chrono::milliseconds(100));
+  if (fail) return cudaErrorUnknown;
+  *p = (void*)&encode;
+  *q = cudaDriverEntryPointSuccess;
+  return cudaSuccess;
+}
+int main() {
+  if (quoka::tensor_map_encoder() != nullptr) return 1;
+  fail = 0;
+  std::atomic<int> ready{0}, missed{0};
+  std::vector<std::thread> ts;
+  for (int i = 0; i < 8; ++i)
+    ts.emplace_back([&] {
+      ++ready;
+      while (ready < 8) std::this_thread::yield();
+      CUtensorMap m;
+      if (!quoka::encode_codes_4d(&m, nullptr, 128, 64, 2, 3, 128, 8192, 16384, 64)) ++missed;
+    });
+  for (auto& t : ts) t.join();
+  const int n = lookups;
+  quoka::tensor_map_encoder();
+  printf("%d %d\n", (int)missed, (int)lookups - n);
+  return 0;
+}
+""")
+    exe = tmp_path / "first"
+    subprocess.run([os.environ.get("CXX", "g++"), "-std=c++17", "-I", build.CSRC, "-isystem", cuda, str(src), "-o", str(exe),
+                    "-pthread"], check=True, capture_output=True, text=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60).stdout
+    assert out.split() == ["0", "0"], "threads without the encoder; lookups once it is known"
+
+
+FIRST_CALLS = r"""
+import sys, threading, torch
+sys.path.insert(0, sys.argv[1])
+import sparse_kv_selection_quoka_b200 as q
+c = [q.QuokaCache(*(torch.zeros(9, 2, 16, 128, dtype=torch.uint8, device="cuda") + 56 for _ in "kv"),
+                  *(torch.ones(9, 2, device="cuda") for _ in "kv"), torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8),
+                  torch.full((1,), 120, dtype=torch.int32, device="cuda")) for _ in range(4)]
+Q = torch.ones(1, 4, 1, 128, device="cuda", dtype=torch.bfloat16)
+torch.cuda.synchronize()
+gate, out = threading.Barrier(4), [None] * 4
+def work(k):
+    gate.wait()
+    try:
+        s = torch.cuda.Stream()
+        idx, n, _, _ = q.quoka_cache_select(Q, c[k], 120, 1, 10, stream=s)
+        O, _ = q.quoka_cache_attn(Q, c[k], 120, stream=s)
+        s.synchronize()
+        out[k] = (idx.tolist(), n.tolist(), O.float().sum().item())
+    except Exception as e:
+        out[k] = repr(e)
+ts = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+[t.start() for t in ts]
+[t.join() for t in ts]
+assert all(o == ([[list(range(10))] * 2], [[10, 10]], 512.0) for o in out), out
+print("same")
+"""
+
+
+@gpu
+def test_first_calls_of_a_process_from_several_threads():
+    """The package's calls as the first of a process, from four threads at once."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
