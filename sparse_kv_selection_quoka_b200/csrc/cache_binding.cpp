@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <array>
@@ -157,8 +158,8 @@ PyObject* guarded(const char* name, Py_ssize_t have, Py_ssize_t want, F&& f) {
     PyErr_SetString(PyExc_TypeError, e.what());
   } catch (const WrongValue& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // (torch's own types: torch.OutOfMemoryError when there is no room for an output or a workspace)
+    if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

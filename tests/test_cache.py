@@ -1079,6 +1079,25 @@ def test_select_takes_the_first_of_equal_scores(k):
 
 
 @gpu
+def test_no_room_for_an_output_or_a_workspace():
+    """torch.OutOfMemoryError, as of the package's other calls, and the next call
+    works: outputs of 2^40 bytes and more that no device has room for."""
+    m, page, cols = q(), 128, 2**21
+    table = torch.zeros(1, cols, dtype=torch.int32, device="cuda")
+    k = torch.zeros(1, 8, page, 128, dtype=torch.uint8, device="cuda")
+    c = m.QuokaCache(k, k.clone(), torch.ones(1, 8, device="cuda"), torch.ones(1, 8, device="cuda"), table,
+                     torch.full((1,), 5, dtype=torch.int32, device="cuda"))
+    Q = torch.ones(1, 8, 64, 128, device="cuda", dtype=torch.bfloat16)
+    n = page * cols  # 2^28 rows
+    with pytest.raises(torch.OutOfMemoryError):
+        m.quoka_cache_gather(c, n, dtype=torch.float32)
+    with pytest.raises(torch.OutOfMemoryError):
+        m.quoka_cache_attn(Q, c, n)  # (the dequantised rows are its workspace)
+    O, _ = m.quoka_cache_attn(Q, c, 5)
+    assert torch.equal(O, torch.zeros_like(O))
+
+
+@gpu
 def test_long_table_offsets_pass_32_bits():
     """A pool of more than 2^32 bytes, with the pages of a sequence at both ends."""
     page, nkv, d = 128, 8, 128
