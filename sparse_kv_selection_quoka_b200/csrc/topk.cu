@@ -138,7 +138,10 @@ __device__ __forceinline__ int64_t keys_of(const int32_t* row_len, const int32_t
   return max((int64_t)0, min((int64_t)__ldg(row_len + bi), T));
 }
 
-template <bool CLUSTER>
+// ROWS: rows have lengths of their own. An instance apart: with the lengths looked
+// at by every call the select of rows without a histogram took 4 % longer (8 rows of
+// 32768 keys 37.1 -> 38.4 us, with the instance 37.1).
+template <bool CLUSTER, bool ROWS>
 __global__ void __launch_bounds__(TOPK_THREADS)
 topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const uint32_t* __restrict__ ghist,
             const int32_t* __restrict__ row_len, const int32_t* __restrict__ new_len, int32_t* __restrict__ kv_idx,
@@ -160,13 +163,13 @@ topk_kernel(const float* __restrict__ S, int64_t T, int bsa, int slice, const ui
   // the row's keys (per batch entry when row_len is given: lengths are inputs of
   // the call, written by no kernel of it) and picks; every CTA of a row's cluster
   // leaves here together when it has none
-  const int64_t Tr = keys_of(row_len, new_len, bi, T);
-  const int take_n = (int)min((int64_t)bsa, Tr);
+  const int64_t Tr = ROWS ? keys_of(row_len, new_len, bi, T) : T;
+  const int take_n = ROWS ? (int)min((int64_t)bsa, Tr) : bsa;
   const int n = (int)max((int64_t)0, min((int64_t)slice, Tr - lo));
   const int n_round = (n + TOPK_THREADS - 1) / TOPK_THREADS * TOPK_THREADS;
 
   pdl_trigger();
-  if (take_n == 0) {
+  if (ROWS && take_n == 0) {
     pdl_wait();
     if (c == 0 && tid == 0) kv_count[row] = 0;
     return;
@@ -1053,7 +1056,8 @@ cudaError_t launch_topk(const float* S_agg, int b, int nkv, int64_t T, int bsa, 
   const int slice = (int)((T + C - 1) / C);
   if (slice > TOPK_MAX_SLICE) return cudaErrorInvalidValue;
   const size_t smem = ((size_t)slice + 2 * TOPK_LIST_MAX) * sizeof(uint32_t);
-  auto kern = C == 1 ? topk_kernel<false> : topk_kernel<true>;
+  auto* kern = row_len != nullptr ? (C == 1 ? topk_kernel<false, true> : topk_kernel<true, true>)
+                                  : (C == 1 ? topk_kernel<false, false> : topk_kernel<true, false>);
   // (the same bound in every call: another thread's launch may come in between)
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (TOPK_MAX_SLICE + 2 * TOPK_LIST_MAX) * (int)sizeof(uint32_t));
