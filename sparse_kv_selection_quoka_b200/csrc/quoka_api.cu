@@ -826,7 +826,8 @@ quoka_status quoka_cache_append(const quoka_cache* cache, const quoka_tensor* K,
   if (!check_tensor(K, K->dtype, ks) || !check_tensor(V, K->dtype, ks)) return QUOKA_ERR_INVALID_ARG;
   const int64_t BCP = ks[2];
   int64_t nq = 0;
-  if ((Q == nullptr) != (Qr == nullptr)) return QUOKA_ERR_INVALID_ARG;
+  // (a chunk of no tokens has nothing to write: its outputs may be null, as an empty tensor's address is)
+  if (Q == nullptr ? Qr != nullptr : Qr == nullptr && BCP > 0) return QUOKA_ERR_INVALID_ARG;
   if (Q != nullptr) {
     int64_t qs[4] = {cache->b, -1, BCP, cache->d};
     if (!check_tensor(Q, K->dtype, qs) || qs[1] < 1) return QUOKA_ERR_INVALID_ARG;

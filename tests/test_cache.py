@@ -357,6 +357,18 @@ def test_append_makes_zeros_of_what_is_left_out(dt, page, nq, BCP):
 
 
 @gpu
+def test_append_of_an_empty_chunk():
+    c = Pages([5, 0], [20, 20], 2, 64, 16, 3)
+    dev = c.cuda(torch.uint8)
+    K, Q = torch.zeros(2, 2, 0, 64, device="cuda"), torch.zeros(2, 4, 0, 64, device="cuda")
+    cos, sin = (x.cuda() for x in angles(20, 64))
+    for kw in ({}, {"new_len": torch.zeros(2, dtype=torch.int32, device="cuda")}, {"Kr": torch.zeros_like(K)}):
+        Kr, Qr = q().quoka_cache_append(dev, K, K, Q, cos, sin, want_Kr=True, **kw)
+        assert Kr.shape == K.shape and Qr.shape == Q.shape
+    assert torch.equal(dev.k.cpu(), c.k) and torch.equal(dev.k_scale.cpu(), c.k_scale)
+
+
+@gpu
 def test_append_of_no_tokens_needs_no_angles():
     """A sequence without new tokens may be longer than the table of angles."""
     c = Pages([30, 4], [64, 40], 1, 64, 16, 8)
@@ -1266,6 +1278,18 @@ def test_entry_points_reject_bad_arguments_on_host(lib):  # noqa: F811
     # outputs over inputs
     assert app(Kr=ctypes.c_void_p(0x60000)) == 1 and app(Kr=ctypes.c_void_p(0x60000 + 256)) == 1
     assert app(Q=Q, Qr=ctypes.c_void_p(0x10000)) == 1
+
+
+def test_append_of_an_empty_chunk_on_host(lib):  # noqa: F811
+    """Nothing to do, whatever goes with it (an empty tensor's address is null)."""
+    B, none = ctypes.byref, _view((1, 2, 0, 128), data=None)
+
+    def app(Q=None, Qr=None):
+        return lib.quoka_cache_append(B(_cache()), B(none), B(none), Q and B(Q), None, None, 0, 0, 0, None, None, Qr, None, 0,
+                                      None)
+
+    assert app() == 0 and app(Q=_view((1, 4, 0, 128), data=None)) == 0
+    assert app(Q=_view((1, 4, 1, 128))) == 1 and app(Qr=ctypes.c_void_p(0x300000)) == 1
 
 
 def test_tensor_map_encoder_is_found_by_every_thread(tmp_path):
