@@ -667,6 +667,47 @@ def test_attention(k):
     check_attention(O, lse, attention(c, Q, Kc, Vc, idx, counts), dt, d, (N or max_len) + BCP, nq // nkv * BCP <= 32)
 
 
+PACKED = [
+    # lens, max_len, nkv, nq, d, page, BCP, N (0: all keys), chunk keys: contiguous Q, several heads a tile
+    ([300, 0], 300, 1, 4, 128, 64, 200, 0, True),       # seven tiles, two of chunk keys; tiles that begin in another head
+    ([300, 17], 304, 1, 4, 64, 16, 200, 90, True),
+    ([6000, 130, 0], 6000, 1, 3, 128, 128, 70, 0, True),  # two tiles in sixteen ranges, most of them empty of the short rows
+    ([6000, 1], 6000, 1, 3, 64, 32, 70, 0, False),
+    ([5000, 4000], 5000, 2, 6, 64, 64, 50, 1900, True),
+    ([2100], 2100, 2, 80, 128, 32, 1, 0, True),          # a decode step of forty heads a KV head
+    ([700], 700, 1, 8, 128, 16, 130, 0, False),
+]
+
+
+@gpu
+@pytest.mark.parametrize("k", range(len(PACKED)))
+def test_attention_of_packed_heads(k):
+    """Chunks of many bf16 rows whose heads follow one another without a gap: a tile
+    takes rows of several heads. Against the plain form, and, but for the ranges'
+    rounding, what a Q of other strides gives."""
+    lens, max_len, nkv, nq, d, page, BCP, N, chunk = PACKED[k]
+    b, t = len(lens), torch.bfloat16
+    G = nq // nkv
+    assert G * BCP > 32 and nkv * -(-G * BCP // 128) < nq * -(-BCP // 128)
+    c = Pages(lens, lens, nkv, d, page, 180 + k, scales=(-9, -5))
+    for i, n in enumerate(lens):
+        if n % page:
+            p = int(c.table[i, n // page])
+            c.k[p, :, n % page:] = 127
+            c.v[p, :, n % page:] = 127
+    idx, counts = index_lists(lens, nkv, N, k) if N else (None, None)
+    Q = (2 * randn(190 + k, b, nq, BCP, d)).to(t)
+    Kc, Vc = (randn(s + k, b, nkv, BCP, d).to(t) for s in (200, 210)) if chunk else (None, None)
+    size = q().quoka_cache_attn_workspace_size(b, nq, nkv, d, BCP, N or max_len, t)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    up = lambda x: None if x is None else x.cuda()
+    dev, want = c.cuda(), attention(c, Q, Kc, Vc, idx, counts)
+    for rows in (Q.cuda(), strided(Q)):
+        O, lse = q().quoka_cache_attn(rows, dev, max_len, up(idx), up(counts), up(Kc), up(Vc), want_lse=True, ws=ws)
+        assert q().quoka_get_device_status(ws) == 0
+        check_attention(O, lse, want, "bf16", d, (N or max_len) + BCP, False)
+
+
 @gpu
 @pytest.mark.parametrize("dt,d,BCP,nq,N", [("bf16", 128, 1, 8, 0), ("bf16", 128, 40, 4, 0), ("bf16", 64, 40, 4, 50),
                                            ("f32", 64, 9, 4, 0), ("bf16", 128, 1, 70, 0)])
