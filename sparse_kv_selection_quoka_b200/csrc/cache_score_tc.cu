@@ -12,10 +12,12 @@
 //
 // Precision. A group mean's element q (|q| <= 1) is split into P e4m3 pieces,
 //   q = sum_p 2^-(8 + 4 p) piece_p + r,  piece_p = e4m3(2^(8 + 4 p) rest_p),
-// each taking half a step (2^-4) of what is left: |r| <= 2^-4P |q|. P = 5 (2^-20)
-// for up to 24 group means a pass, else 4 (2^-16, what bf16 hi + lo keeps), 32 a
-// pass. Code products are exact and accumulate in fp32; the pieces' columns are
-// added in fp32.
+// A piece of four significant bits leaves at most 2^-4 of its leading power of two,
+// exactly that only where the next piece ends it, else less, so that the next one's
+// leading power is half as large: |r| <= 2^-(5P - 1) |q| (of elements below 2^-14: of
+// 2^-14). P = 5 (2^-24, all of an fp32 number) for up to 24 group means a pass, else
+// 4 (2^-19), 32 a pass. Code products are exact and accumulate in fp32; the pieces'
+// columns are added in fp32.
 //
 // Work split. The keys of every (sequence, KV head) are cut into ranges of near
 // equal length, one CTA each (cache.cuh), two CTAs an SM. Warp 4 loads: boxes of

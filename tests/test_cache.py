@@ -502,6 +502,30 @@ def test_select(k):
                 assert (want[i][j][best] >= last - 2 * tol).all()
 
 
+@gpu
+@pytest.mark.parametrize("NQ", [5, 24, 25, 49, 130])
+def test_select_scores_to_the_last_piece(NQ):
+    """Half of a key's columns are 1, the rest 0; a query is 1 there and beta
+    elsewhere, so that its unit vector has any fraction beta gives it (these leave
+    the most behind four pieces), products and their sums are exact, and the score
+    is sqrt(m / (m + (d - m) beta^2)). Bound, relative: five pieces 2^-24, four (more
+    than 24 group means) 2^-19, rsqrt 2^-22, and 2^-24 for each of: 34 additions of
+    |q|^2, halved by the root, the root, the division, four joins of pieces, two
+    products."""
+    d, m, BCP = 128, 64, max(NQ, 40)
+    beta = [1.39988, 1.30399, 1.3056, 1.35226, 0.98057, 1.18919, 1.12156, 1.39372, 1.32614, 0.50759, 0.60337, 0.66868, 0.80136,
+            0.93802, 0.29239, 0.64385]
+    c = Pages([30] * 16, [30] * 16, 1, d, 16, 5)
+    c.k[:] = 0
+    c.k[..., ::2] = 56  # 1.0
+    Q = torch.ones(16, 1, BCP, d)
+    Q[..., 1::2] = torch.tensor(beta)[:, None, None, None]
+    _, _, _, s = q().quoka_cache_select(Q.cuda(), c.cuda(), 30, NQ, 4, want_s_agg=True)
+    b, piece = torch.tensor(beta).double(), 2.0 ** (-24 if NQ <= 24 else -19)  # (beta as fp32 holds it)
+    want = (m / (m + (d - m) * b * b)).sqrt()[:, None].expand(16, 30)
+    assert ((s[:, 0].double().cpu() / want - 1).abs() <= piece + 2.0**-22 + 25 * 2.0**-24).all()
+
+
 PADDED = [
     # lens, new, nkv, nq, d, page, BCP, NQ, BSA, dtype, what the rows of padding hold
     ([300, 47, 129, 200], [33, 1, 0, 100], 2, 8, 128, 64, 100, 4, 50, "bf16", 0.0),
