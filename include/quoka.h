@@ -532,9 +532,14 @@ quoka_status quoka_get_device_fault_site(const void* ws, void* stream,
  *   inject         QUOKA_DEBUG_INJECT_NONE, or one barrier made to expect
  *                  one arrival more than it ever receives in every launch
  *                  that follows: QUOKA_DEBUG_INJECT_SCORE (the scoring
- *                  kernel's release of its first TMEM accumulator) or
+ *                  kernel's release of its first TMEM accumulator),
  *                  QUOKA_DEBUG_INJECT_ATTN (the attention's first release
- *                  of P to the P V product). The waiting warp gives up after
+ *                  of P to the P V product), QUOKA_DEBUG_INJECT_CACHE_SCORE
+ *                  (the cache scoring's release of its first stage, or, for
+ *                  more than four group means, of its accumulator) or
+ *                  QUOKA_DEBUG_INJECT_CACHE_ATTN (the release of the first
+ *                  stage of the cache attention of few query rows). The
+ *                  waiting warp gives up after
  *                  wait_limit_ns, latches QUOKA_ERR_TIMEOUT and a fault site
  *                  in ws, and the kernel unwinds (in-flight copies and
  *                  products drained, TMEM freed); the outputs of that call
@@ -545,6 +550,8 @@ quoka_status quoka_get_device_fault_site(const void* ws, void* stream,
 #define QUOKA_DEBUG_INJECT_NONE 0u
 #define QUOKA_DEBUG_INJECT_SCORE 1u
 #define QUOKA_DEBUG_INJECT_ATTN 2u
+#define QUOKA_DEBUG_INJECT_CACHE_SCORE 3u
+#define QUOKA_DEBUG_INJECT_CACHE_ATTN 4u
 quoka_status quoka_debug_set_wait_hooks(uint64_t wait_limit_ns, uint32_t inject);
 
 /* A static, human-readable name of a status code. */

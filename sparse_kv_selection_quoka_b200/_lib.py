@@ -442,6 +442,8 @@ def quoka_get_device_fault_site(ws, stream=None) -> int:
 DEBUG_INJECT_NONE = 0
 DEBUG_INJECT_SCORE = 1
 DEBUG_INJECT_ATTN = 2
+DEBUG_INJECT_CACHE_SCORE = 3
+DEBUG_INJECT_CACHE_ATTN = 4
 
 
 def quoka_debug_set_wait_hooks(wait_limit_ns: int = 0, inject: int = DEBUG_INJECT_NONE) -> None:

@@ -185,7 +185,7 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
       }
     }
     const int st = s % kStages;
-    if (s >= kStages && !__all_sync(0xffffffffu, sm100::mbar_wait(&sh.empty[st], (s / kStages - 1) & 1, &sh.abort))) {
+    if (s >= kStages && !__all_sync(0xffffffffu, sm100::mbar_wait(&sh.empty[st], (s / kStages - 1) & 1, &sh.abort, a.wait_ns))) {
       if (lane == 0) {
         sh.abort = 1;
         sh.fault = 5;  // QUOKA_ERR_TIMEOUT
@@ -254,7 +254,7 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Maps& ma
     sm100::cp_async_commit();
     sm100::cp_async_wait<0>();
   } else {  // no copy may be in flight when the CTA goes on, even if a wait gave up
-    for (int i = max(0, s - kStages); i < s; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
+    for (int i = max(0, s - kStages); i < s; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1, a.wait_ns);
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && sh.fault == 0) sh.fault = 6;  // QUOKA_ERR_BOUNDS
 }
@@ -349,7 +349,7 @@ cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       sm100::mbar_init(&sh.full[i], IDX ? 64 : 32);
-      sm100::mbar_init(&sh.empty[i], 4);
+      sm100::mbar_init(&sh.empty[i], a.inject && i == 0 ? 5 : 4);  // (the hook: an arrival that never comes)
     }
     sh.abort = sh.fault = sh.site = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -589,7 +589,7 @@ cache_slice_kernel(const __grid_constant__ Maps maps, const CacheAttnArgs a) {
       const int st = i % kStages;
       // (of listed rows stage 0 is there: slot 0 is filled by the loader one time less)
       const uint32_t parity = (i / kStages - (IDX && st == 0 ? 1 : 0)) & 1;
-      if ((!IDX || i > 0) && !__all_sync(0xffffffffu, sm100::mbar_wait(&sh.full[st], parity, &sh.abort))) {
+      if ((!IDX || i > 0) && !__all_sync(0xffffffffu, sm100::mbar_wait(&sh.full[st], parity, &sh.abort, a.wait_ns))) {
         if (lane == 0) {
           sh.abort = 1;
           sh.fault = 5;  // QUOKA_ERR_TIMEOUT
@@ -886,6 +886,9 @@ cudaError_t launch_cache_attn(bool is_bf16, int d, const CacheAttnArgs& args, cu
   if (ranges * ((R + kBlockRows - 1) / kBlockRows) > 0x7FFFFFFF || (int64_t)a.b * a.nq * a.BCP > 0x7FFFFFFF) return cudaErrorNotSupported;
   a.target = (int)range_target(rows, split_ctas(R));
   a.ranges = (int)ranges;
+  const WaitHooks hooks = wait_hooks();
+  a.wait_ns = hooks.wait_ns;
+  a.inject = hooks.inject == INJECT_CACHE_ATTN ? 1 : 0;
   if (d != 64 && d != 128) return cudaErrorNotSupported;
   if (R <= 8) {
     if (d == 128) return is_bf16 ? launch_typed<bf16, 128, 1>(a, stream) : launch_typed<float, 128, 1>(a, stream);

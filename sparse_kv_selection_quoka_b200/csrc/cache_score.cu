@@ -76,7 +76,7 @@ __device__ __forceinline__ void load_rows(const CacheScoreArgs& a, const CUtenso
   int p0 = page_of(0), p1 = page_of(1), it = 0;
   for (; it < total; ++it) {
     const int p2 = page_of(it + 2), st = it % kStages;
-    if (it >= kStages && !__all_sync(0xffffffffu, sm100::mbar_wait(&sh.empty[st], (it / kStages - 1) & 1, &sh.abort))) {
+    if (it >= kStages && !__all_sync(0xffffffffu, sm100::mbar_wait(&sh.empty[st], (it / kStages - 1) & 1, &sh.abort, a.wait_ns))) {
       if (lane == 0) {
         sh.abort = 1;
         latch_status(a.status, 5 /* QUOKA_ERR_TIMEOUT */);
@@ -97,7 +97,7 @@ __device__ __forceinline__ void load_rows(const CacheScoreArgs& a, const CUtenso
     p1 = p2;
   }
   // no copy may be in flight when the CTA ends, even if a wait gave up
-  for (int i = max(0, it - kStages); i < it; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
+  for (int i = max(0, it - kStages); i < it; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1, a.wait_ns);
   if (bad) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
 }
 
@@ -117,7 +117,7 @@ cache_score_kernel(const __grid_constant__ CUtensorMap map, const CacheScoreArgs
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       sm100::mbar_init(&sh.full[i], 32);
-      sm100::mbar_init(&sh.empty[i], 4);
+      sm100::mbar_init(&sh.empty[i], a.inject && i == 0 ? 5 : 4);  // (the hook: an arrival that never comes)
     }
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -170,7 +170,7 @@ cache_score_kernel(const __grid_constant__ CUtensorMap map, const CacheScoreArgs
     for (int ks = 0; ks < KS; ++ks) qb[ks] = qs[ks * 32 + lane];
     for (int s = 0; s < nst; ++s) {
       const int st = s % kStages;
-      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&sh.full[st], (s / kStages) & 1, &sh.abort))) {
+      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&sh.full[st], (s / kStages) & 1, &sh.abort, a.wait_ns))) {
         if (lane == 0) {
           sh.abort = 1;
           latch_status(a.status, 5 /* QUOKA_ERR_TIMEOUT */);
@@ -297,7 +297,11 @@ cudaError_t launch_typed(const CacheScoreArgs& args, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_cache_score(int d, const CacheScoreArgs& a, cudaStream_t stream) {
+cudaError_t launch_cache_score(int d, const CacheScoreArgs& args, cudaStream_t stream) {
+  CacheScoreArgs a = args;
+  const WaitHooks hooks = wait_hooks();
+  a.wait_ns = hooks.wait_ns;
+  a.inject = hooks.inject == INJECT_CACHE_SCORE ? 1 : 0;
   if (a.NQ < 1 || a.max_len < 1) return cudaErrorInvalidValue;
   if (d != 64 && d != 128) return cudaErrorNotSupported;
   if (a.NQ > kMost) return launch_cache_score_tc(d, a, stream);

@@ -101,7 +101,7 @@ __device__ __forceinline__ void load_rows(const CacheScoreArgs& a, const CUtenso
   int p0 = page_of(0), p1 = page_of(1), it = 0;
   for (; it < total; ++it) {
     const int p2 = page_of(it + 2), st = it % kStages;
-    if (it >= kStages && !sm100::mbar_wait_warp(&sh.empty[st], (it / kStages - 1) & 1, &sh.abort)) {
+    if (it >= kStages && !sm100::mbar_wait_warp(&sh.empty[st], (it / kStages - 1) & 1, &sh.abort, a.wait_ns)) {
       if (lane == 0) give_up(sh, a.status, 63);
       break;
     }
@@ -119,7 +119,7 @@ __device__ __forceinline__ void load_rows(const CacheScoreArgs& a, const CUtenso
     p1 = p2;
   }
   // no copy may be in flight when the CTA ends, even if a wait gave up
-  for (int i = max(0, it - kStages); i < it; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1);
+  for (int i = max(0, it - kStages); i < it; ++i) sm100::mbar_drain(&sh.full[i % kStages], (i / kStages) & 1, a.wait_ns);
   if (bad) latch_status(a.status, 6 /* QUOKA_ERR_BOUNDS */);
 }
 
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_score_tc_kernel(const __gri
       sm100::mbar_init(&sh.empty[i], 1);
     }
     sm100::mbar_init(&sh.acc_full, 1);
-    sm100::mbar_init(&sh.acc_empty, 4);
+    sm100::mbar_init(&sh.acc_empty, a.inject ? 5 : 4);  // (the hook: an arrival that never comes)
     sm100::mbar_init(&sh.b_ready, 4);
     sm100::mbar_init(&sh.done, 1);
     sh.abort = 0;
@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(kThreads, 2) cache_score_tc_kernel(const __gri
     bool alive = true;
     for (int it = 0; it < total && alive; ++it) {
       const int st = it % kStages;
-      if (it % nst == 0) alive = sm100::mbar_wait_warp(&sh.b_ready, (it / nst) & 1, &sh.abort);
-      if (alive) alive = sm100::mbar_wait_warp(&sh.full[st], (it / kStages) & 1, &sh.abort);
-      if (alive && it > 0) alive = sm100::mbar_wait_warp(&sh.acc_empty, (it - 1) & 1, &sh.abort);
+      if (it % nst == 0) alive = sm100::mbar_wait_warp(&sh.b_ready, (it / nst) & 1, &sh.abort, a.wait_ns);
+      if (alive) alive = sm100::mbar_wait_warp(&sh.full[st], (it / kStages) & 1, &sh.abort, a.wait_ns);
+      if (alive && it > 0) alive = sm100::mbar_wait_warp(&sh.acc_empty, (it - 1) & 1, &sh.abort, a.wait_ns);
       if (!alive) break;
       sm100::tc_fence_after();
       const uint32_t k = sm100::smem_u32(ring + st * Ring<D>::kBytes);
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_score_tc_kernel(const __gri
     }
     if (!alive && lane == 0) give_up(sh, a.status, 64);
     sm100::umma_commit_warp(&sh.done);
-    if (!__all_sync(0xffffffffu, sm100::mbar_drain(&sh.done, 0)) && lane == 0) give_up(sh, a.status, 65);
+    if (!__all_sync(0xffffffffu, sm100::mbar_drain(&sh.done, 0, a.wait_ns)) && lane == 0) give_up(sh, a.status, 65);
     __syncwarp();
   } else {
     pdl_wait();
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_score_tc_kernel(const __gri
       if (lane == 0) sm100::mbar_arrive(&sh.b_ready);
       bool alive = true;
       for (int s = 0; s < nst; ++s, ++it) {
-        alive = sm100::mbar_wait_warp(&sh.acc_full, it & 1, &sh.abort);
+        alive = sm100::mbar_wait_warp(&sh.acc_full, it & 1, &sh.abort, a.wait_ns);
         if (!alive) {
           if (lane == 0) give_up(sh, a.status, 66);
           break;

@@ -9,12 +9,14 @@
 namespace quoka {
 
 // Test hooks, set through quoka_debug_set_wait_hooks and read by the
-// launchers of the tensor-core scoring and attention kernels: the bound of
-// every wait in those kernels (2 s by default), and an optional fault
-// injection that makes one barrier expect one arrival more than it ever
-// receives, so that the timeout path (give up, latch QUOKA_ERR_TIMEOUT and a
-// fault site, drain, free TMEM, exit) runs without hanging the GPU.
-enum : uint32_t { INJECT_NONE = 0u, INJECT_SCORE_TC = 1u, INJECT_ATTN_TMA = 2u };
+// launchers of the kernels that wait (tensor-core scoring and attention, the
+// cache's scoring and attention): the bound of every wait in those kernels (2 s
+// by default), and an optional fault injection that makes one barrier expect one
+// arrival more than it ever receives, so that the timeout path (give up, latch
+// QUOKA_ERR_TIMEOUT and a fault site, drain, free TMEM, exit) runs without hanging
+// the GPU.
+enum : uint32_t { INJECT_NONE = 0u, INJECT_SCORE_TC = 1u, INJECT_ATTN_TMA = 2u,
+                INJECT_CACHE_SCORE = 3u, INJECT_CACHE_ATTN = 4u };
 struct WaitHooks {
   uint64_t wait_ns;
   uint32_t inject;
@@ -242,6 +244,8 @@ struct CacheAttnArgs {
   int2* row_parts;          // (b, nkv): a row's first range and their number
   int* faults;              // (ranges, ceil(G * BCP / 64)): what a CTA has to latch
   int ranges, target;       // set by the launcher
+  uint64_t wait_ns;         // bound of every wait, and
+  int inject;               // test hook (both set by the launcher from wait_hooks())
   void* O;
   float* lse;
   int* status;
@@ -265,6 +269,8 @@ struct CacheScoreArgs {
   const int32_t* new_len = nullptr;  // (b) or null: queries of a padded chunk of BCP rows;
   int BCP = 0;                       // no key of a sequence without any is scored
   int target = 1;  // ranges asked for (set by the launcher)
+  uint64_t wait_ns = 0;  // bound of every wait, and
+  int inject = 0;        // test hook (both set by the launcher from wait_hooks())
 };
 cudaError_t launch_cache_score(int d, const CacheScoreArgs& a, cudaStream_t stream);
 // More than four group means of it (cache_score_tc.cu; called by launch_cache_score).

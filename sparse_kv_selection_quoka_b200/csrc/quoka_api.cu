@@ -1056,7 +1056,7 @@ quoka_status quoka_get_device_fault_site(const void* ws, void* stream, int32_t* 
 }
 
 quoka_status quoka_debug_set_wait_hooks(uint64_t wait_limit_ns, uint32_t inject) {
-  if (inject > QUOKA_DEBUG_INJECT_ATTN) return QUOKA_ERR_INVALID_ARG;
+  if (inject > QUOKA_DEBUG_INJECT_CACHE_ATTN) return QUOKA_ERR_INVALID_ARG;
   quoka::g_wait_ns.store(wait_limit_ns, std::memory_order_relaxed);
   quoka::g_inject.store(inject, std::memory_order_relaxed);
   return QUOKA_OK;

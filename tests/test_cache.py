@@ -1103,6 +1103,65 @@ def test_two_threads_at_once(lib):  # noqa: F811
     assert not faults
 
 
+def given_up(kind, call, ws):
+    """Runs call() with the waits bounded by 5 ms and the barrier of `kind` expecting
+    an arrival that never comes; the status and fault site of ws."""
+    q().quoka_debug_set_wait_hooks(5_000_000, kind)
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        q().quoka_debug_set_wait_hooks()
+    return q().quoka_get_device_status(ws), q().quoka_get_device_fault_site(ws)
+
+
+@gpu
+@pytest.mark.parametrize("NQ,d", [(2, 64), (2, 128), (40, 64), (100, 128)])
+def test_scoring_that_gives_up_unwinds(NQ, d):
+    """A wait that runs out is QUOKA_ERR_TIMEOUT with its site and a count of 0 (no
+    stale selection); the same call, workspace and device then give what they gave
+    before. One sequence, long enough that every range has more tiles than stages."""
+    m, n, BCP = q(), 200_000, 2 * NQ
+    c = Pages([n], [n], 1, d, 128, 7).cuda()
+    Q = randn(8, 1, 2, BCP, d).cuda()
+    ws = torch.zeros(m.quoka_select_workspace_size(1, 2, 1, d, n, BCP, NQ, 900, Q.dtype), dtype=torch.uint8, device="cuda")
+    idx, cnt = torch.zeros(1, 1, 900, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    s = torch.zeros(1, 1, n, device="cuda")
+    call = lambda: m.quoka_cache_select(Q, c, n, NQ, 900, kv_idx=idx, kv_count=cnt, s_agg=s, ws=ws)
+    call()
+    want = idx.clone(), s.clone()
+    for _ in range(3):
+        status, site = given_up(m._lib.DEBUG_INJECT_CACHE_SCORE, call, ws)
+        assert status == 5 and site in (63, 64, 65, 66) and int(cnt) == 0
+        idx.fill_(-1)
+        call()
+        assert m.quoka_get_device_status(ws) == 0 and m.quoka_get_device_fault_site(ws) == 0
+        assert int(cnt) == 900 and torch.equal(idx, want[0]) and torch.equal(s, want[1])
+
+
+@gpu
+@pytest.mark.parametrize("dt,d,BCP,listed", [("bf16", 128, 1, False), ("bf16", 64, 16, True), ("f32", 128, 1, True),
+                                             ("f32", 64, 40, False)])
+def test_attention_that_gives_up_unwinds(dt, d, BCP, listed):
+    """The same of the attention over the codes, whose second kernel reports the
+    first one's faults."""
+    m, n = q(), 200_000
+    c = Pages([n], [n], 1, d, 128, 7, scales=(-9, -5)).cuda()
+    Q = randn(8, 1, 2, BCP, d).to(TYPES[dt]).cuda()
+    idx = torch.randperm(n, generator=torch.Generator().manual_seed(1), dtype=torch.int32).view(1, 1, n).cuda() if listed else None
+    cnt = torch.full((1, 1), n, dtype=torch.int32, device="cuda") if listed else None
+    ws = torch.zeros(m.quoka_cache_attn_workspace_size(1, 2, 1, d, BCP, n, TYPES[dt]), dtype=torch.uint8, device="cuda")
+    O = torch.zeros_like(Q)
+    call = lambda: m.quoka_cache_attn(Q, c, n, idx, cnt, O=O, ws=ws)
+    call()
+    want = O.clone()
+    for _ in range(3):
+        status, site = given_up(m._lib.DEBUG_INJECT_CACHE_ATTN, call, ws)
+        assert status == 5 and site in (61, 62)
+        call()
+        assert m.quoka_get_device_status(ws) == 0 and m.quoka_get_device_fault_site(ws) == 0 and torch.equal(O, want)
+
+
 @gpu
 @pytest.mark.parametrize("rows,T,BSA", [(20, 33000, 4000), (40, 20001, 100), (130, 9000, 8999), (600, 5000, 1), (74, 40000, 777)])
 def test_topk_of_many_rows(rows, T, BSA):
