@@ -371,7 +371,7 @@ quoka_status quoka_combine_partials(const void* O_parts, const float* lse_parts,
  *   k, v       (npages, nkv, page, d) codes (1 byte each; sign, 4 bits of
  *              exponent with bias 7, 3 of fraction). page 16, 32, 64 or 128
  *              tokens; d 64 or 128. Strides in bytes, shared by k and v,
- *              multiples of 16; a row's d codes are contiguous; rows must
+ *              multiples of 16 below 2^40; a row's d codes are contiguous; rows must
  *              not overlap. k and v 16-byte aligned.
  *   k_scale, v_scale  (npages, nkv) float, contiguous: powers of two 2^e,
  *              -50 <= e <= 50. A row's value is code * scale. Anything else

@@ -442,6 +442,9 @@ quoka_status validate_cache(const quoka_cache* c, quoka::CacheView* v) {
   for (int i = 0; i < 3; ++i)
     if (st[i] < 0 || st[i] % 16 != 0 || (n[i] > 1 && st[i] < c->d)) return QUOKA_ERR_INVALID_ARG;
   if (!supported_d(c->d) || !cache_page_ok(c->page)) return QUOKA_ERR_UNSUPPORTED;
+  // (what a tensor map takes; refused here, before a call's first kernels are enqueued)
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && st[i] >= (int64_t)1 << 40) return QUOKA_ERR_UNSUPPORTED;
   if (c->b > kMaxHeads || c->nkv > kMaxHeads || c->npages > (int64_t)INT32_MAX) return QUOKA_ERR_UNSUPPORTED;
   v->k = static_cast<uint8_t*>(c->k);
   v->v = static_cast<uint8_t*>(c->v);

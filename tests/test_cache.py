@@ -1404,6 +1404,21 @@ def test_entry_points_reject_bad_arguments_on_host(lib):  # noqa: F811
     assert app(Q=Q, Qr=ctypes.c_void_p(0x10000)) == 1
 
 
+def test_cache_of_far_strides_is_refused_on_host(lib):  # noqa: F811
+    """Before anything is enqueued, by every call (a size of one has no stride)."""
+    B, ws, buf = ctypes.byref, ctypes.c_void_p(0x100000), ctypes.c_void_p(0x200000)
+    far = 1 << 40
+    for kw in (dict(page_stride=far), dict(head_stride=far), dict(row_stride=far)):
+        c = _cache(**kw)
+        assert lib.quoka_cache_select(B(_view((1, 4, 7, 128))), B(c), 100, 2, 10, buf, buf, None, None, ws, 1 << 30, None) == 2
+        assert lib.quoka_cache_attn(B(_view((1, 4, 7, 128))), B(c), 100, None, None, 100, None, None, 0.1, buf, None, ws, 1 << 30,
+                                    None) == 2
+        assert lib.quoka_cache_gather(B(c), 100, None, None, 100, 1, buf, buf, None, 0, None) == 2
+    none = _view((1, 1, 0, 128), data=None)
+    one = _cache(npages=1, nkv=1, page_stride=far, head_stride=far)
+    assert lib.quoka_cache_append(B(one), B(none), B(none), None, None, None, 0, 0, 0, None, None, None, None, 0, None) == 0
+
+
 def test_append_of_an_empty_chunk_on_host(lib):  # noqa: F811
     """Nothing to do, whatever goes with it (an empty tensor's address is null)."""
     B, none = ctypes.byref, _view((1, 2, 0, 128), data=None)
