@@ -475,6 +475,10 @@ quoka_status quoka_cache_select_padded(const quoka_tensor* Q, const int32_t* new
                                        int32_t* q_idx, float* s_agg, void* ws,
                                        size_t ws_bytes, void* stream);
 
+/* (Precision of both: queries are normalised and averaged in fp32; of an element of a
+ * group mean up to 4 of them keep 2^-22, up to 24 of them 2^-24, more 2^-19; codes are
+ * exact, and all sums are fp32.) */
+
 /* Step (f) over the cache: Ksel[b, j, n] = the value of key kv_idx[b, j, n]
  * for n < kv_count[b, j], and the same for V; with kv_idx and kv_count NULL,
  * N = max_len and row n is key n, n < seq_len[b]. Rows past the count are
@@ -495,6 +499,12 @@ quoka_status quoka_cache_gather(const quoka_cache* cache, int max_len,
  *   that the mask leaves out by zero); O out (b, nq, BCP, d), contiguous; lse
  *   out (b, nq, BCP) float or NULL. A row that sees no key gives O = 0,
  *   lse = -inf. An index listed twice counts twice.
+ *   Precision: scores, maxima and sums are fp32, and cached rows are exact. The
+ *   softmax weights that meet the values are rounded: with fp32 queries to two
+ *   fp16 halves (2^-21), with bf16 queries to fp16 (2^-11) for chunks of up to 32
+ *   query rows per KV head (nq / nkv * BCP), else to bf16 (2^-8), as in
+ *   quoka_sparse_gqa_attn; those longer chunks may be cut into up to 16 ranges of
+ *   keys, whose partial outputs are bf16 too.
  *   ws at least quoka_cache_attn_workspace_size() bytes, 256-byte aligned. */
 size_t quoka_cache_attn_workspace_size(int b, int nq, int nkv, int d, int BCP,
                                        int N, quoka_dtype dtype);
